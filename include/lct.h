@@ -31,7 +31,7 @@
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     lct_encode, lct_decode and the update calls (lct_sgd_step*,
  *     lct_momentum_step*) only enqueue work on it and return at once, as do
- *     the group calls and lct_group_fit; lct_codebook_build,
+ *     the group calls, lct_group_fit, the norms and the clip; lct_codebook_build,
  *     lct_codebook_reshift, lct_codebook_reshift_dense, lct_tensor_sample
  *     and lct_codebook_adapt synchronise it (they read a sample back), and
  *     lct_group_bind copies its table with a blocking copy.
@@ -438,6 +438,110 @@ lct_status lct_sgd_step_group(const lct_group *gw, const lct_tensor *w_all, cons
 lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
                                    const lct_tensor *m_all, const lct_group *gg, float mu, float eta,
                                    const lct_tensor *w_out, const lct_tensor *m_out, void *stream);
+
+/* ---- norms and clipping ----------------------------------------------------
+ * The global norm of a step's gradients, the coefficient that clips them to a
+ * largest norm, and the ways to apply it, so that a step with clipping never
+ * waits for the host: the norm calls leave their result in device memory, and
+ * the clip and the clipped steps read the coefficient from there.
+ *
+ * With x the elements of every tensor of a set and s the scale (the gradients
+ * stand for s * x: 1 / loss scale, or 1 / accumulated batches):
+ *   LCT_NORM_L2:   S = sum of x^2,          norm = |s| * sqrt(S)
+ *   LCT_NORM_MAX:  S = largest |x|,         norm = |s| * S
+ *   coef = s * min(1, max_norm / (norm + 1e-6))
+ * S is summed and the rest computed in 64 bits; norm and coef are rounded to
+ * fp32 once.  Equal calls give equal bits.  A NaN element makes norm and coef
+ * NaN, an infinite one makes norm infinite and coef 0 (NaN when max_norm is
+ * infinite too).  An empty set has S = 0, norm 0.  max_norm = INFINITY with
+ * finite elements gives coef = s.
+ *
+ * Common to the norm calls: scale finite, max_norm not negative and not NaN;
+ * d_scratch: device working memory of at least lct_norm_scratch() bytes
+ * (256-byte aligned), shared only by calls that do not overlap in time and
+ * overlapping no input; d_each (may be NULL): the norm of each tensor, as
+ * norm above; d_out: device, 8-byte aligned.  They only enqueue work on
+ * `stream`.  Unlike the codec's calls they write their result for an empty
+ * set too.  Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS (an output or the
+ * scratch overlapping an input or each other), LCT_EARCH, LCT_EHIP. */
+typedef enum { LCT_NORM_L2 = 0, LCT_NORM_MAX = 1 } lct_norm_kind;
+typedef enum { LCT_BF16 = 0, LCT_FP16 = 1, LCT_FP32 = 2 } lct_dtype;
+
+/* A norm's result (device memory). */
+typedef struct {
+    double sum;    /* S: the sum of squares, or the largest magnitude, unscaled */
+    float norm;
+    float coef;
+} lct_norm_t;
+
+/* A list of dense tensors: host arrays of the caller's, read during the call
+ * only (tensors may move from call to call).  Tensor k has n[k] contiguous
+ * elements (0 allowed) of type[k] (lct_dtype) from d_x[k], which needs the
+ * alignment of its elements only.  A list holds at most 2^44 elements. */
+typedef struct {
+    uint32_t count;
+    const uint64_t *n;
+    void *const *d_x;
+    const int32_t *type;
+} lct_list;
+
+/* Bytes of d_scratch of a norm: of a list of count tensors (nblk 0), or of a
+ * compressed tensor or group of nblk blocks (lct_sizes, lct_group_sizes);
+ * given both, enough for either.  Errors: LCT_EINVAL (null out, or nblk past
+ * 2^32 - 1). */
+lct_status lct_norm_scratch(uint32_t count, uint64_t nblk, uint64_t *bytes);
+
+/* Norm of a list (a tensor that is listed twice counts twice).  d_each: count
+ * floats. */
+lct_status lct_list_norm(const lct_list *x, int32_t kind, double max_norm, double scale, void *d_scratch,
+                         float *d_each, lct_norm_t *d_out, void *stream);
+
+/* Norms of a compressed tensor (decoded with *cb) and of a group (with its
+ * members' codebooks; no dense buffers needed), without a dense copy: the
+ * values are used as they are decoded.  d_each: g->count floats. */
+lct_status lct_tensor_norm(const lct_codebook *cb, const lct_tensor *t, int32_t kind, double max_norm,
+                           double scale, void *d_scratch, lct_norm_t *d_out, void *stream);
+lct_status lct_group_norm(const lct_group *g, const lct_tensor *all, int32_t kind, double max_norm,
+                          double scale, void *d_scratch, float *d_each, lct_norm_t *d_out, void *stream);
+
+/* The norm of the union of the sets behind `count` results (their sums, of
+ * the same kind): other ranks' gathered results, or a list's and a group's.
+ * d_out may be one of d_parts. */
+lct_status lct_norm_join(const lct_norm_t *d_parts, uint32_t count, int32_t kind, double max_norm,
+                         double scale, lct_norm_t *d_out, void *stream);
+
+/* Clip: y_k = coef * x_k for every tensor of a list, each product rounded to
+ * fp32 and then to y_k's type (nearest, ties to even; what is too large for
+ * FP16 becomes infinite; a NaN stays a NaN).  d_coef: a device
+ * float, such as a norm's coef.  x and y list the same sizes; y_k is x_k (the
+ * same memory and type: in place) or overlaps no tensor of x; tensors of y
+ * overlap neither each other nor d_coef.  In place, a coefficient of exactly
+ * 1 leaves memory untouched.  Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS,
+ * LCT_EARCH, LCT_EHIP. */
+lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list *y, void *stream);
+
+/* Clipped updates: lct_sgd_step, lct_momentum_step and their group forms with
+ * the step's M (or gradient) scaled by *d_coef, a device float (4-byte
+ * aligned, overlapping no output) that is read when the step runs.
+ *   SGD:       w' = rne_bf16(fmaf(-(eta * coef), m, w)), eta * coef in fp32
+ *   momentum:  m' = rne_bf16(fmaf(mu, m, coef * g)), coef * g in fp32, and w'
+ *              from m' as in lct_momentum_step
+ * Otherwise as the calls they clip (arguments, rules, errors); with a
+ * coefficient of 1 they write the same bytes. */
+lct_status lct_sgd_step_clip(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                             const lct_tensor *m, float eta, const float *d_coef,
+                             const lct_tensor *w_out, void *stream);
+lct_status lct_sgd_step_clip_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                   const lct_tensor *m_all, float eta, const float *d_coef,
+                                   const lct_tensor *w_out, void *stream);
+lct_status lct_momentum_step_clip(const lct_codebook *cw, const lct_tensor *w_in,
+                                  const lct_codebook *cm, const lct_tensor *m_in, const uint16_t *d_g,
+                                  const float *d_coef, float mu, float eta, const lct_tensor *w_out,
+                                  const lct_tensor *m_out, void *stream);
+lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                        const lct_tensor *m_all, const lct_group *gg, const float *d_coef,
+                                        float mu, float eta, const lct_tensor *w_out,
+                                        const lct_tensor *m_out, void *stream);
 
 /* Message for a status code (static string). */
 const char *lct_strerror(lct_status st);

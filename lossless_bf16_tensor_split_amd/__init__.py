@@ -25,8 +25,17 @@ Functions keep the C names:
     lct_encode_group(g, all) / lct_decode_group(g, all)
     lct_sgd_step_group(gw, w_all, gm, m_all, eta, w_out)
     lct_momentum_step_group(gw, w_all, gm, m_all, gg, mu, eta, w_out, m_out)
+    lct_list_norm(x, out, max_norm, scale, kind)        (x: LctList, out: LctNorm from alloc_norm)
+    lct_tensor_norm(cb, t, out, ...) / lct_group_norm(g, all, out, ...)
+    lct_norm_join(parts, out, ...)
+    lct_list_clip(x, coef, y)
+    lct_sgd_step_clip(cw, w_in, cm, m, eta, coef, w_out)
+    lct_sgd_step_clip_group(gw, w_all, gm, m_all, eta, coef, w_out)
+    lct_momentum_step_clip(cw, w_in, cm, m_in, g, coef, mu, eta, w_out, m_out)
+    lct_momentum_step_clip_group(gw, w_all, gm, m_all, gg, coef, mu, eta, w_out, m_out)
 plus ``alloc_tensor`` and the convenience wrappers ``encode`` / ``decode`` /
-``sgd_step`` / ``momentum_step`` that allocate their outputs.
+``sgd_step`` / ``momentum_step`` / ``grad_norm`` / ``clip_grad_norm`` that
+allocate their outputs.
 """
 from __future__ import annotations
 
@@ -43,6 +52,8 @@ CLEAN, MEDIUM, HIGH = 0, 1, 2
 ST_OVF_FULL, ST_LOOKBACK = 0x1, 0x2
 OK, EINVAL, EALIGN, EALIAS, EHIP, EARCH, ESIZE = 0, -1, -2, -3, -4, -5, -6
 NOALLOC_SCRATCH_BYTES = 16 << 20
+NORM_L2, NORM_MAX = 0, 1
+BF16, FP16, FP32 = 0, 1, 2
 
 EXPORTED = ["lct_layout_init", "lct_sizes", "lct_codebook_build", "lct_codebook_from_lengths",
             "lct_tensor_sample", "lct_codebook_reshift", "lct_codebook_reshift_dense",
@@ -50,6 +61,8 @@ EXPORTED = ["lct_layout_init", "lct_sizes", "lct_codebook_build", "lct_codebook_
             "lct_sgd_step", "lct_sgd_step_recode", "lct_sgd_step_noalloc", "lct_momentum_step", "lct_momentum_step_recode",
             "lct_group_table_bytes", "lct_group_bind", "lct_group_fit", "lct_group_sizes", "lct_group_tensor",
             "lct_encode_group", "lct_decode_group", "lct_sgd_step_group", "lct_momentum_step_group",
+            "lct_norm_scratch", "lct_list_norm", "lct_tensor_norm", "lct_group_norm", "lct_norm_join", "lct_list_clip",
+            "lct_sgd_step_clip", "lct_sgd_step_clip_group", "lct_momentum_step_clip", "lct_momentum_step_clip_group",
             "lct_strerror", "lct_last_hip_error"]
 
 
@@ -85,6 +98,10 @@ class Group(C.Structure):
     _fields_ = [("count", C.c_uint32), ("layout", Layout), ("nblk", C.c_uint64),
                 ("sf_bytes", C.c_uint64), ("shape_hash", C.c_uint64), ("n", C.c_void_p),
                 ("d_dense", C.c_void_p), ("d_table", C.c_void_p)]
+
+
+class _List(C.Structure):
+    _fields_ = [("count", C.c_uint32), ("n", C.c_void_p), ("d_x", C.c_void_p), ("type", C.c_void_p)]
 
 
 class LctError(RuntimeError):
@@ -127,6 +144,17 @@ def _load():
     L.lct_momentum_step.argtypes = [C.POINTER(Codebook), C.POINTER(_Tensor), C.POINTER(Codebook),
                                     C.POINTER(_Tensor), P, C.c_float, C.c_float, C.POINTER(_Tensor),
                                     C.POINTER(_Tensor), P]
+    LI, f32, f64 = C.POINTER(_List), C.c_float, C.c_double
+    L.lct_norm_scratch.argtypes = [C.c_uint32, u64, C.POINTER(u64)]
+    L.lct_list_norm.argtypes = [LI, i32, f64, f64, P, P, P, P]
+    L.lct_tensor_norm.argtypes = [CB, T, i32, f64, f64, P, P, P]
+    L.lct_group_norm.argtypes = [G, T, i32, f64, f64, P, P, P, P]
+    L.lct_norm_join.argtypes = [P, C.c_uint32, i32, f64, f64, P, P]
+    L.lct_list_clip.argtypes = [LI, P, LI, P]
+    L.lct_sgd_step_clip.argtypes = [CB, T, CB, T, f32, P, T, P]
+    L.lct_sgd_step_clip_group.argtypes = [G, T, G, T, f32, P, T, P]
+    L.lct_momentum_step_clip.argtypes = [CB, T, CB, T, P, P, f32, f32, T, T, P]
+    L.lct_momentum_step_clip_group.argtypes = [G, T, G, T, G, P, f32, f32, T, T, P]
     L.lct_strerror.restype = C.c_char_p
     L.lct_strerror.argtypes = [i32]
     L.lct_last_hip_error.restype = C.c_char_p
@@ -563,3 +591,217 @@ def lct_momentum_step_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all:
     _check(lib.lct_momentum_step_group(C.byref(gw.g), C.byref(a), C.byref(gm.g), C.byref(b), C.byref(gg.g),
                                        mu, eta, C.byref(ow), C.byref(om), _stream(stream)),
            "lct_momentum_step_group")
+
+
+# ------------------------------------------------------------------ norms and clipping
+
+_LIST_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+def _current(dev: torch.device, what: str) -> None:
+    """The library works on the current device: a buffer elsewhere is refused
+    here, since a kernel that reads it could fault."""
+    if dev.type != "cuda":
+        raise ValueError("%s must be on the GPU" % what)
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, dev, torch.cuda.current_device()))
+
+
+class LctList:
+    """Dense tensors (BF16, FP16 or FP32, contiguous, on one GPU) for
+    ``lct_list_norm`` and ``lct_list_clip``.  Keeps the tensors; makes host
+    arrays only, so a new list for tensors that moved costs no device work."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        count = len(self.tensors)
+        self.device = None
+        types = []
+        for k, t in enumerate(self.tensors):
+            ty = _LIST_TYPES.get(t.dtype)
+            if ty is None:
+                raise TypeError("tensor %d is %s; expected bfloat16, float16 or float32" % (k, t.dtype))
+            if not t.is_contiguous():
+                raise ValueError("tensor %d must be contiguous" % k)
+            if not t.is_cuda:
+                raise ValueError("tensor %d must be on the GPU" % k)
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError("tensor %d is on %s, tensor 0 on %s" % (k, t.device, self.device))
+            types.append(ty)
+        self.ns = (C.c_uint64 * count)(*[t.numel() for t in self.tensors])
+        self.ptrs = (C.c_void_p * count)(*[t.data_ptr() for t in self.tensors])
+        self.types = (C.c_int32 * count)(*types)
+        self.count = count
+        self.c = _List(count, C.cast(self.ns, C.c_void_p), C.cast(self.ptrs, C.c_void_p),
+                       C.cast(self.types, C.c_void_p))
+
+    def __len__(self):
+        return self.count
+
+
+class LctNorm:
+    """A norm's result on the device, and the working memory of the call.
+
+    ``sum`` (float64), ``norm`` and ``coef`` (float32) are 0-d views of one
+    buffer; ``each`` holds every tensor's norm, or is None."""
+
+    def __init__(self, members: int, nblk: int, each: bool, device, scratch=None):
+        need = C.c_uint64(0)
+        _check(lib.lct_norm_scratch(members, nblk, C.byref(need)), "lct_norm_scratch")
+        dev = torch.device(device)
+        if scratch is None:
+            scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        self.scratch = scratch
+        self.buf = torch.zeros(16, dtype=torch.uint8, device=dev)
+        self.sum = self.buf[0:8].view(torch.float64)[0]
+        self.norm = self.buf[8:12].view(torch.float32)[0]
+        self.coef = self.buf[12:16].view(torch.float32)[0]
+        self.each = torch.zeros(members, dtype=torch.float32, device=dev) if each else None
+
+    def _args(self, members: int, nblk: int | None = None):
+        """(scratch, each) for a call on so many tensors: a list, or with nblk
+        a compressed tensor or group."""
+        need = C.c_uint64(0)
+        _check(lib.lct_norm_scratch(members if nblk is None else 0, nblk or 0, C.byref(need)), "lct_norm_scratch")
+        for name, b, bytes_ in (("scratch", self.scratch, need.value), ("buf", self.buf, 16)):
+            _current(b.device, name)
+            if not b.is_contiguous() or b.numel() * b.element_size() < bytes_:
+                raise ValueError("%s must be contiguous and hold %d bytes" % (name, bytes_))
+        if self.each is not None:
+            _current(self.each.device, "each")
+            if self.each.dtype != torch.float32 or not self.each.is_contiguous() or self.each.numel() != members:
+                raise ValueError("each must be a contiguous float32 tensor of %d elements" % members)
+        return _ptr(self.scratch), _ptr(self.each)
+
+
+def alloc_norm(members: int = 0, each: bool = False, nblk: int = 0, device="cuda", scratch=None) -> LctNorm:
+    """Result and working memory of the norm of a list of ``members`` tensors,
+    or of a compressed tensor or group of ``nblk`` blocks (``members`` tensors);
+    each: with a norm for every tensor."""
+    return LctNorm(members, nblk, each, device, scratch)
+
+
+def lct_list_norm(x: LctList, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
+                  kind: int = NORM_L2, stream=None) -> None:
+    """Norm of the list's tensors (times scale), each tensor's where out has
+    room for them, and the coefficient that clips to max_norm."""
+    if x.device is not None:
+        _current(x.device, "the list")
+    scr, each = out._args(x.count)
+    _check(lib.lct_list_norm(C.byref(x.c), kind, max_norm, scale, scr, each, _ptr(out.buf), _stream(stream)),
+           "lct_list_norm")
+
+
+def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
+                    kind: int = NORM_L2, stream=None) -> None:
+    """Norm of a compressed tensor, without decoding it to memory."""
+    ct = t.c(need_scratch=False)
+    _current(t.sf.device, "the tensor")
+    if out.each is not None:
+        raise ValueError("each is for lists and groups")
+    scr, _ = out._args(1, t.sizes.nblk)
+    _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, scr, _ptr(out.buf),
+                               _stream(stream)), "lct_tensor_norm")
+
+
+def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
+                   kind: int = NORM_L2, stream=None) -> None:
+    """Norm of a compressed group and of each member where out has room."""
+    a = all_.c(need_scratch=False)
+    _current(all_.sf.device, "the group")
+    scr, each = out._args(g.count, all_.sizes.nblk)
+    _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, scr, each, _ptr(out.buf),
+                              _stream(stream)), "lct_group_norm")
+
+
+def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0, kind: int = NORM_L2,
+                  stream=None) -> None:
+    """Norm of the union of the sets behind several results: a sequence of
+    LctNorm, or their ``buf`` bytes gathered in one uint8 tensor [k, 16]."""
+    if not torch.is_tensor(parts):
+        parts = torch.stack([p.buf for p in parts]) if len(parts) else out.buf[:0]
+    if parts.dtype != torch.uint8 or not parts.is_contiguous() or parts.numel() % 16:
+        raise ValueError("parts must be a contiguous uint8 tensor of 16 bytes per result")
+    _current(parts.device, "parts")
+    _current(out.buf.device, "buf")
+    _check(lib.lct_norm_join(_ptr(parts), parts.numel() // 16, kind, max_norm, scale, _ptr(out.buf),
+                             _stream(stream)), "lct_norm_join")
+
+
+def _coef(coef) -> torch.Tensor:
+    """A device float32 scalar: a tensor of one element, or a norm's."""
+    if isinstance(coef, LctNorm):
+        coef = coef.coef
+    if not torch.is_tensor(coef) or coef.dtype != torch.float32 or coef.numel() != 1:
+        raise TypeError("coef must be an LctNorm or a float32 tensor of one element")
+    _current(coef.device, "coef")
+    return coef
+
+
+def lct_list_clip(x: LctList, coef, y: LctList | None = None, stream=None) -> None:
+    """y_k = coef * x_k (in place without y), rounded to y_k's type."""
+    y = x if y is None else y
+    coef = _coef(coef)
+    for li in (x, y):
+        if li.device is not None:
+            _current(li.device, "the list")
+    _check(lib.lct_list_clip(C.byref(x.c), _ptr(coef), C.byref(y.c), _stream(stream)), "lct_list_clip")
+
+
+def lct_sgd_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m: LctTensor, eta: float, coef,
+                      w_out: LctTensor, stream=None) -> None:
+    """lct_sgd_step with M scaled by coef."""
+    coef = _coef(coef)
+    a, b, o = w_in.c(), m.c(), w_out.c()
+    _check(lib.lct_sgd_step_clip(C.byref(cw), C.byref(a), C.byref(cm), C.byref(b), eta, _ptr(coef), C.byref(o),
+                                 _stream(stream)), "lct_sgd_step_clip")
+
+
+def lct_sgd_step_clip_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all: LctTensor, eta: float, coef,
+                            w_out: LctTensor, stream=None) -> None:
+    """lct_sgd_step_group with M scaled by coef."""
+    coef = _coef(coef)
+    a, b, o = w_all.c(), m_all.c(), w_out.c()
+    _check(lib.lct_sgd_step_clip_group(C.byref(gw.g), C.byref(a), C.byref(gm.g), C.byref(b), eta, _ptr(coef),
+                                       C.byref(o), _stream(stream)), "lct_sgd_step_clip_group")
+
+
+def lct_momentum_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m_in: LctTensor, g: torch.Tensor, coef,
+                           mu: float, eta: float, w_out: LctTensor, m_out: LctTensor, stream=None) -> None:
+    """lct_momentum_step with the gradient scaled by coef."""
+    _gradient(g, w_in.n)
+    coef = _coef(coef)
+    a, b, ow, om = w_in.c(), m_in.c(), w_out.c(), m_out.c()
+    _check(lib.lct_momentum_step_clip(C.byref(cw), C.byref(a), C.byref(cm), C.byref(b), _ptr(g), _ptr(coef), mu,
+                                      eta, C.byref(ow), C.byref(om), _stream(stream)), "lct_momentum_step_clip")
+
+
+def lct_momentum_step_clip_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all: LctTensor, gg: LctGroup,
+                                 coef, mu: float, eta: float, w_out: LctTensor, m_out: LctTensor,
+                                 stream=None) -> None:
+    """lct_momentum_step_group with the gradients scaled by coef."""
+    coef = _coef(coef)
+    a, b, ow, om = w_all.c(), m_all.c(), w_out.c(), m_out.c()
+    _check(lib.lct_momentum_step_clip_group(C.byref(gw.g), C.byref(a), C.byref(gm.g), C.byref(b), C.byref(gg.g),
+                                            _ptr(coef), mu, eta, C.byref(ow), C.byref(om), _stream(stream)),
+           "lct_momentum_step_clip_group")
+
+
+def grad_norm(tensors, max_norm: float = float("inf"), scale: float = 1.0, kind: int = NORM_L2,
+              each: bool = False) -> LctNorm:
+    """Norm of dense tensors and the coefficient that clips them to max_norm."""
+    x = tensors if isinstance(tensors, LctList) else LctList(tensors)
+    out = alloc_norm(x.count, each, device=x.device or "cuda")
+    lct_list_norm(x, out, max_norm, scale, kind)
+    return out
+
+
+def clip_grad_norm(tensors, max_norm: float, scale: float = 1.0, kind: int = NORM_L2) -> LctNorm:
+    """Clip dense tensors in place to a global norm of max_norm; the host never
+    waits for the norm."""
+    x = tensors if isinstance(tensors, LctList) else LctList(tensors)
+    out = grad_norm(x, max_norm, scale, kind)
+    lct_list_clip(x, out)
+    return out

@@ -1,12 +1,15 @@
 // api.cpp -- the extern "C" entry points declared in include/lct.h:
 // argument checks, size accounting and kernel launches.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <map>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "lct_internal.h"
@@ -109,6 +112,14 @@ bool overlaps_any(Range r, const Parts &p, bool with_writable = true) {
         if (overlap(r, a)) return true;
     if (with_writable && (overlap(r, p.status) || overlap(r, p.scratch))) return true;
     return false;
+}
+
+// A clipped step's coefficient (null: not a clipped step): aligned, and not
+// in what the step writes.
+lct_status check_coef(const float *coef, const Parts &out) {
+    if (!coef) return LCT_OK;
+    if (!aligned(coef, 4)) return LCT_EALIGN;
+    return overlaps_any(rng(coef, 4), out) ? LCT_EALIAS : LCT_OK;
 }
 
 std::mutex g_sample_mu;
@@ -310,7 +321,7 @@ bool momentum_alias_ok(const lct_tensor &w_in, const lct_tensor &m_in, const lct
 // Aliasing rules, parameters and launches of an update (a tensor, or a
 // group's storage when `group`); p's tables (or group references) are set.
 lct_status sgd_run(SgdParams &p, const lct_tensor &w_in, const lct_tensor &m, const lct_tensor &w_out,
-                   uint64_t nb, float eta, bool group, void *stream) {
+                   uint64_t nb, float eta, const float *coef, bool group, void *stream) {
     const Parts pw = parts(w_in, nb), pm = parts(m, nb), po = parts(w_out, nb);
     // M is read-only and must not share memory with the output
     const Range mr[] = {pm.sf, pm.pay, pm.cnt, pm.obase, pm.ovf};
@@ -330,10 +341,149 @@ lct_status sgd_run(SgdParams &p, const lct_tensor &w_in, const lct_tensor &m, co
     const Range ow[] = {po.ovf, po.status, po.scratch};
     for (const Range &r : ow)
         if (overlaps_any(r, pw, false) || overlaps_any(r, pm, false)) return LCT_EALIAS;
-    lct_status st = check_arch();
+    lct_status st = check_coef(coef, po);
+    if (st != LCT_OK) return st;
+    st = check_arch();
     if (st != LCT_OK) return st;
     sgd_params(p, w_in, m, w_out, nb, -eta);
+    p.coef = coef;
     return sgd_launch(p, nb, group, stream);
+}
+
+// ---- norms and clipping
+
+uint64_t type_bytes(int32_t type) { return type == LCT_FP32 ? 4 : 2; }
+
+Range member(const lct_list &x, uint32_t k) { return rng(x.d_x[k], x.n[k] * type_bytes(x.type[k])); }
+
+lct_status check_list(const lct_list *x) {
+    if (!x || (x->count > 0 && (!x->n || !x->d_x || !x->type))) return LCT_EINVAL;
+    uint64_t total = 0;
+    for (uint32_t k = 0; k < x->count; ++k) {
+        if (x->type[k] != LCT_BF16 && x->type[k] != LCT_FP16 && x->type[k] != LCT_FP32) return LCT_EINVAL;
+        if (x->n[k] > kListMaxElems) return LCT_EINVAL;
+        total += x->n[k];
+        if (total > kListMaxElems) return LCT_EINVAL;   // checked as it grows: it cannot wrap
+        if (x->n[k] == 0) continue;
+        if (!x->d_x[k]) return LCT_EINVAL;
+        if (!aligned(x->d_x[k], type_bytes(x->type[k]))) return LCT_EALIGN;
+    }
+    return LCT_OK;
+}
+
+lct_status check_norm_args(int32_t kind, double max_norm, double scale, const lct_norm_t *out) {
+    if (kind != LCT_NORM_L2 && kind != LCT_NORM_MAX) return LCT_EINVAL;
+    if (!(max_norm >= 0) || !std::isfinite(scale) || !out) return LCT_EINVAL;
+    return aligned(out, 8) ? LCT_OK : LCT_EALIGN;
+}
+
+// A norm's arguments and outputs (each: `count` floats, or null).
+lct_status check_norm(int32_t kind, double max_norm, double scale, const void *scratch, uint64_t scratch_bytes,
+                      const float *each, uint32_t count, const lct_norm_t *out) {
+    const lct_status st = check_norm_args(kind, max_norm, scale, out);
+    if (st != LCT_OK) return st;
+    if (!scratch) return LCT_EINVAL;
+    if (!aligned(scratch, 256) || !aligned(each, 4)) return LCT_EALIGN;
+    const Range s = rng(scratch, scratch_bytes), o = rng(out, sizeof *out), e = rng(each, each ? 4ull * count : 0);
+    return overlap(s, o) || overlap(s, e) || overlap(o, e) ? LCT_EALIAS : LCT_OK;
+}
+
+// The result from `count` part values (every stride-th double).  Many are
+// first folded into kFoldGrid (room for which `fold` gives).
+lct_status norm_join(const double *part, uint64_t count, uint64_t stride, bool squares, NormArgs args, double *fold,
+                     lct_norm_t *out, void *stream) {
+    NormJoinParams p;
+    memset(&p, 0, sizeof p);
+    p.part = part;
+    p.count = count;
+    p.stride = stride;
+    p.args = args;
+    p.squares = squares;
+    if (fold && count > kFoldFrom) {
+        p.fold = fold;
+        const int e = launch_norm_join(p, kFoldGrid, stream);
+        if (e != hipSuccess) return hip_fail(e, "norm join launch");
+        p.part = fold;
+        p.count = kFoldGrid;
+        p.stride = 1;
+        p.fold = nullptr;
+    }
+    p.out = out;
+    const int e = launch_norm_join(p, 1, stream);
+    return e == hipSuccess ? LCT_OK : hip_fail(e, "norm join launch");
+}
+
+// The norm of a compressed tensor, or (g set) of a group's storage; p's
+// tables are set.
+lct_status code_norm(CodeNormParams &p, const lct_tensor &t, uint64_t nb, const lct_group *g, int32_t kind,
+                     double max_norm, double scale, void *scratch, float *each, lct_norm_t *out, void *stream) {
+    const uint32_t count = g ? g->count : 1;
+    const uint64_t scr = norm_scratch_bytes(0, nb);
+    lct_status st = check_norm(kind, max_norm, scale, scratch, scr, each, count, out);
+    if (st != LCT_OK) return st;
+    if (nb > 0) {
+        const Parts in = parts(t, nb);
+        if (overlaps_any(rng(scratch, scr), in, false) || overlaps_any(rng(out, sizeof *out), in, false) ||
+            overlaps_any(rng(each, each ? 4ull * count : 0), in, false))
+            return LCT_EALIAS;
+    }
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    const bool squares = kind == LCT_NORM_L2;
+    double *part = static_cast<double *>(scratch);
+    if (nb > 0) {
+        p.sf = t.sf;
+        p.pay = t.pay;
+        p.cnt = t.cnt;
+        p.obase = t.obase;
+        p.ovf = t.ovf;
+        p.ovf_cap = t.ovf_cap;
+        p.n = t.n;
+        p.block_elems = t.layout.block_elems;
+        p.cap_words = t.layout.cap_words;
+        p.nblk = (uint32_t)nb;
+        p.part = part;
+        const int e = launch_code_norm(p, g != nullptr, squares, stream);
+        if (e != hipSuccess) return hip_fail(e, "code norm launch");
+    }
+    if (each) {
+        const int e = launch_group_each(p.grp.ent, count, part, {max_norm, scale}, squares, each, stream);
+        if (e != hipSuccess) return hip_fail(e, "group norms launch");
+    }
+    return norm_join(part, nb, 1, squares, {max_norm, scale}, part + nb, out, stream);
+}
+
+// The clip's aliasing rules.  Every range sorted by its start; an overlap of
+// neighbours in that order (against the furthest end so far) is one of the
+// list's, and only x_k with y_k in place, or x with x, may be.
+lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list &y) {
+    struct Span {
+        Range r;
+        uint32_t k;
+        bool written;
+    };
+    try {
+        std::vector<Span> v;
+        v.reserve(2 * (size_t)x.count + 1);
+        for (uint32_t k = 0; k < x.count; ++k) {
+            if (x.n[k] == 0) continue;
+            const Range rx = member(x, k), ry = member(y, k);
+            const bool inplace = rx.lo == ry.lo && x.type[k] == y.type[k];
+            if (!inplace) v.push_back({rx, k, false});
+            v.push_back({ry, k, true});
+        }
+        v.push_back({rng(coef, 4), 0, false});
+        std::sort(v.begin(), v.end(), [](const Span &a, const Span &b) { return a.r.lo < b.r.lo; });
+        uintptr_t any = 0, written = 0;   // furthest end of all spans so far, of the written ones
+        for (const Span &s : v) {
+            if (s.r.lo < written || (s.written && s.r.lo < any)) return LCT_EALIAS;
+            any = std::max(any, s.r.hi);
+            if (s.written) written = std::max(written, s.r.hi);
+        }
+    } catch (const std::bad_alloc &) {
+        return hip_fail(hipErrorOutOfMemory, "clip's table of ranges");
+    }
+    return LCT_OK;
 }
 
 }  // namespace
@@ -537,14 +687,10 @@ lct_status lct_decode(const lct_codebook *cb, const lct_tensor *in, uint16_t *d_
     return LCT_OK;
 }
 
-lct_status lct_sgd_step(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
-                        const lct_tensor *m, float eta, const lct_tensor *w_out, void *stream) {
-    return lct_sgd_step_recode(cw, w_in, cm, m, eta, cw, w_out, stream);
-}
-
-lct_status lct_sgd_step_recode(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
-                               const lct_tensor *m, float eta, const lct_codebook *cw_out,
-                               const lct_tensor *w_out, void *stream) {
+// The update of one tensor, plain (coef null) or clipped.
+static lct_status sgd_one(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                          const lct_tensor *m, float eta, const float *coef, const lct_codebook *cw_out,
+                          const lct_tensor *w_out, void *stream) {
     if (!cw || !cm || !cw_out || !w_in || !m || !w_out) return LCT_EINVAL;
     if (!tables_ok(*cw) || !tables_ok(*cm) || !tables_ok(*cw_out)) return LCT_EINVAL;
     if (w_in->n != m->n || w_in->n != w_out->n) return LCT_EINVAL;
@@ -565,7 +711,25 @@ lct_status lct_sgd_step_recode(const lct_codebook *cw, const lct_tensor *w_in, c
     fill_enc(*cw_out, &p.wenc);
     fill_dec(*cw, &p.wdec);
     fill_dec(*cm, &p.mdec);
-    return sgd_run(p, *w_in, *m, *w_out, nb, eta, false, stream);
+    return sgd_run(p, *w_in, *m, *w_out, nb, eta, coef, false, stream);
+}
+
+lct_status lct_sgd_step(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                        const lct_tensor *m, float eta, const lct_tensor *w_out, void *stream) {
+    return sgd_one(cw, w_in, cm, m, eta, nullptr, cw, w_out, stream);
+}
+
+lct_status lct_sgd_step_recode(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                               const lct_tensor *m, float eta, const lct_codebook *cw_out,
+                               const lct_tensor *w_out, void *stream) {
+    return sgd_one(cw, w_in, cm, m, eta, nullptr, cw_out, w_out, stream);
+}
+
+lct_status lct_sgd_step_clip(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                             const lct_tensor *m, float eta, const float *d_coef, const lct_tensor *w_out,
+                             void *stream) {
+    if (!d_coef) return LCT_EINVAL;
+    return sgd_one(cw, w_in, cm, m, eta, d_coef, cw, w_out, stream);
 }
 
 lct_status lct_sgd_step_noalloc(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
@@ -584,17 +748,11 @@ lct_status lct_sgd_step_noalloc(const lct_codebook *cw, const lct_tensor *w_in, 
     return lct_sgd_step(cw, w_in, cm, m, eta, &out, stream);
 }
 
-lct_status lct_momentum_step(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
-                             const lct_tensor *m_in, const uint16_t *d_g, float mu, float eta,
-                             const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
-    return lct_momentum_step_recode(cw, w_in, cm, m_in, d_g, mu, eta, cw, cm, w_out, m_out, stream);
-}
-
-lct_status lct_momentum_step_recode(const lct_codebook *cw, const lct_tensor *w_in,
-                                    const lct_codebook *cm, const lct_tensor *m_in,
-                                    const uint16_t *d_g, float mu, float eta,
-                                    const lct_codebook *cw_out, const lct_codebook *cm_out,
-                                    const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+// The momentum step of one tensor, plain (coef null) or clipped.
+static lct_status momentum_one(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                               const lct_tensor *m_in, const uint16_t *d_g, const float *coef, float mu,
+                               float eta, const lct_codebook *cw_out, const lct_codebook *cm_out,
+                               const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
     if (!cw || !cm || !cw_out || !cm_out || !w_in || !m_in || !w_out || !m_out) return LCT_EINVAL;
     if (!tables_ok(*cw) || !tables_ok(*cm) || !tables_ok(*cw_out) || !tables_ok(*cm_out)) return LCT_EINVAL;
     const lct_tensor *all[] = {w_in, m_in, w_out, m_out};
@@ -613,6 +771,9 @@ lct_status lct_momentum_step_recode(const lct_codebook *cw, const lct_tensor *w_
     if (overlaps_any(rng(d_g, w_in->n * 2), parts(*w_out)) || overlaps_any(rng(d_g, w_in->n * 2), parts(*m_out)))
         return LCT_EALIAS;   // the gradient is read only: no output may overlap it
     if (!momentum_alias_ok(*w_in, *m_in, *w_out, *m_out, ~0ull)) return LCT_EALIAS;
+    st = check_coef(coef, parts(*w_out));
+    if (st == LCT_OK) st = check_coef(coef, parts(*m_out));
+    if (st != LCT_OK) return st;
     st = check_arch();
     if (st != LCT_OK) return st;
 
@@ -623,11 +784,33 @@ lct_status lct_momentum_step_recode(const lct_codebook *cw, const lct_tensor *w_
     MomParams p;
     memset(&p, 0, sizeof p);
     mom_params(p, *w_in, *m_in, d_g, *w_out, *m_out, nb, mu, eta);
+    p.coef = coef;
     fill_enc_packed(*cw_out, p.wenc);
     fill_enc_packed(*cm_out, p.menc);
     fill_dec(*cw, &p.wdec);
     fill_dec(*cm, &p.mdec);
     return mom_launch(p, nb, false, stream);
+}
+
+lct_status lct_momentum_step(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                             const lct_tensor *m_in, const uint16_t *d_g, float mu, float eta,
+                             const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+    return momentum_one(cw, w_in, cm, m_in, d_g, nullptr, mu, eta, cw, cm, w_out, m_out, stream);
+}
+
+lct_status lct_momentum_step_recode(const lct_codebook *cw, const lct_tensor *w_in,
+                                    const lct_codebook *cm, const lct_tensor *m_in,
+                                    const uint16_t *d_g, float mu, float eta,
+                                    const lct_codebook *cw_out, const lct_codebook *cm_out,
+                                    const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+    return momentum_one(cw, w_in, cm, m_in, d_g, nullptr, mu, eta, cw_out, cm_out, w_out, m_out, stream);
+}
+
+lct_status lct_momentum_step_clip(const lct_codebook *cw, const lct_tensor *w_in, const lct_codebook *cm,
+                                  const lct_tensor *m_in, const uint16_t *d_g, const float *d_coef, float mu,
+                                  float eta, const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+    if (!d_coef) return LCT_EINVAL;
+    return momentum_one(cw, w_in, cm, m_in, d_g, d_coef, mu, eta, cw, cm, w_out, m_out, stream);
 }
 
 // ---- groups
@@ -838,9 +1021,9 @@ lct_status lct_decode_group(const lct_group *g, const lct_tensor *all, void *str
     return LCT_OK;
 }
 
-lct_status lct_sgd_step_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
-                              const lct_tensor *m_all, float eta, const lct_tensor *w_out,
-                              void *stream) {
+static lct_status sgd_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                            const lct_tensor *m_all, float eta, const float *coef, const lct_tensor *w_out,
+                            void *stream) {
     lct_status st = check_group(gw, w_all, false);
     if (st == LCT_OK) st = check_group(gm, m_all, false);
     if (st == LCT_OK) st = check_group(gw, w_out, true);
@@ -855,12 +1038,25 @@ lct_status lct_sgd_step_group(const lct_group *gw, const lct_tensor *w_all, cons
     memset(&p, 0, sizeof p);
     p.gw = group_ref(*gw);
     p.gm = group_ref(*gm);
-    return sgd_run(p, *w_all, *m_all, *w_out, gw->nblk, eta, true, stream);
+    return sgd_run(p, *w_all, *m_all, *w_out, gw->nblk, eta, coef, true, stream);
 }
 
-lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
-                                   const lct_tensor *m_all, const lct_group *gg, float mu, float eta,
-                                   const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+lct_status lct_sgd_step_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                              const lct_tensor *m_all, float eta, const lct_tensor *w_out,
+                              void *stream) {
+    return sgd_group(gw, w_all, gm, m_all, eta, nullptr, w_out, stream);
+}
+
+lct_status lct_sgd_step_clip_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                   const lct_tensor *m_all, float eta, const float *d_coef,
+                                   const lct_tensor *w_out, void *stream) {
+    if (!d_coef) return LCT_EINVAL;
+    return sgd_group(gw, w_all, gm, m_all, eta, d_coef, w_out, stream);
+}
+
+static lct_status momentum_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                 const lct_tensor *m_all, const lct_group *gg, const float *coef, float mu,
+                                 float eta, const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
     lct_status st = check_group(gw, w_all, false);
     if (st == LCT_OK) st = check_group(gm, m_all, false);
     if (st == LCT_OK) st = check_group(gw, w_out, true);
@@ -879,6 +1075,9 @@ lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all,
     if (st == LCT_OK) st = check_group_dense(*gg, parts(*m_out, gw->nblk));
     if (st != LCT_OK) return st;
     if (!momentum_alias_ok(*w_all, *m_all, *w_out, *m_out, gw->nblk)) return LCT_EALIAS;
+    st = check_coef(coef, parts(*w_out, gw->nblk));
+    if (st == LCT_OK) st = check_coef(coef, parts(*m_out, gw->nblk));
+    if (st != LCT_OK) return st;
     st = check_arch();
     if (st != LCT_OK) return st;
     if (gw->nblk == 0) return LCT_OK;
@@ -889,7 +1088,157 @@ lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all,
     p.gw = group_ref(*gw);
     p.gm = group_ref(*gm);
     p.gg = group_ref(*gg);
+    p.coef = coef;
     return mom_launch(p, nb, true, stream);
+}
+
+lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                   const lct_tensor *m_all, const lct_group *gg, float mu, float eta,
+                                   const lct_tensor *w_out, const lct_tensor *m_out, void *stream) {
+    return momentum_group(gw, w_all, gm, m_all, gg, nullptr, mu, eta, w_out, m_out, stream);
+}
+
+lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w_all, const lct_group *gm,
+                                        const lct_tensor *m_all, const lct_group *gg, const float *d_coef,
+                                        float mu, float eta, const lct_tensor *w_out,
+                                        const lct_tensor *m_out, void *stream) {
+    if (!d_coef) return LCT_EINVAL;
+    return momentum_group(gw, w_all, gm, m_all, gg, d_coef, mu, eta, w_out, m_out, stream);
+}
+
+// ---- norms and clipping
+
+lct_status lct_norm_scratch(uint32_t count, uint64_t nblk, uint64_t *bytes) {
+    if (!bytes || nblk > 0xFFFFFFFFull) return LCT_EINVAL;
+    *bytes = norm_scratch_bytes(count, nblk);
+    return LCT_OK;
+}
+
+lct_status lct_list_norm(const lct_list *x, int32_t kind, double max_norm, double scale, void *d_scratch,
+                         float *d_each, lct_norm_t *d_out, void *stream) {
+    lct_status st = check_list(x);
+    if (st != LCT_OK) return st;
+    const uint64_t scr = norm_scratch_bytes(x->count, 0);
+    st = check_norm(kind, max_norm, scale, d_scratch, scr, d_each, x->count, d_out);
+    if (st != LCT_OK) return st;
+    const Range out[] = {rng(d_scratch, scr), rng(d_each, d_each ? 4ull * x->count : 0), rng(d_out, sizeof *d_out)};
+    for (uint32_t k = 0; k < x->count; ++k)
+        for (const Range &r : out)
+            if (overlap(member(*x, k), r)) return LCT_EALIAS;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    const bool squares = kind == LCT_NORM_L2;
+    double *run = static_cast<double *>(d_scratch);
+    double *piece = run + list_launches(x->count) * kListGrid;
+    uint64_t runs = 0;
+    ListNormParams p;
+    ListEachParams q;
+    memset(&p, 0, sizeof p);
+    memset(&q, 0, sizeof q);
+    q.args = {max_norm, scale};
+    q.squares = squares;
+    for (uint32_t k0 = 0; k0 < x->count; k0 += kListMax) {
+        p.count = std::min(kListMax, x->count - k0);
+        uint64_t c = 0;
+        for (uint32_t j = 0; j < p.count; ++j) {
+            p.x[j] = x->d_x[k0 + j];
+            p.n[j] = x->n[k0 + j] | ((uint64_t)x->type[k0 + j] << kListTypeShift);
+            p.chunk0[j] = (uint32_t)c;
+            c += (x->n[k0 + j] + kListChunk - 1) / kListChunk;
+        }
+        p.chunks = p.chunk0[p.count] = (uint32_t)c;
+        const uint32_t grid = std::min(kListGrid, p.chunks);
+        p.run = run + runs;
+        p.piece = d_each ? piece : nullptr;
+        if (grid) {
+            const int e = launch_list_norm(p, grid, squares, stream);
+            if (e != hipSuccess) return hip_fail(e, "list norm launch");
+        }
+        if (d_each) {
+            q.piece = piece;
+            q.each = d_each + k0;
+            q.count = p.count;
+            q.chunks = p.chunks;
+            q.G = grid;
+            memcpy(q.chunk0, p.chunk0, sizeof q.chunk0);
+            const int e = launch_list_each(q, stream);
+            if (e != hipSuccess) return hip_fail(e, "list norm launch");
+        }
+        runs += grid;
+        piece += kListGrid + kListMax;
+    }
+    return norm_join(run, runs, 1, squares, {max_norm, scale}, nullptr, d_out, stream);
+}
+
+lct_status lct_tensor_norm(const lct_codebook *cb, const lct_tensor *t, int32_t kind, double max_norm,
+                           double scale, void *d_scratch, lct_norm_t *d_out, void *stream) {
+    if (!cb || !t || !tables_ok(*cb)) return LCT_EINVAL;
+    uint64_t nb = 0;
+    if (t->n > 0) {
+        const lct_status st = check_tensor(t, false);
+        if (st != LCT_OK) return st;
+        nb = nblocks(t->n, t->layout);
+    }
+    CodeNormParams p;
+    memset(&p, 0, sizeof p);
+    fill_dec(*cb, &p.dec);
+    return code_norm(p, *t, nb, nullptr, kind, max_norm, scale, d_scratch, nullptr, d_out, stream);
+}
+
+lct_status lct_group_norm(const lct_group *g, const lct_tensor *all, int32_t kind, double max_norm,
+                          double scale, void *d_scratch, float *d_each, lct_norm_t *d_out, void *stream) {
+    const lct_status st = check_group(g, all, false);
+    if (st != LCT_OK) return st;
+    CodeNormParams p;
+    memset(&p, 0, sizeof p);
+    p.grp = group_ref(*g);
+    return code_norm(p, *all, g->nblk, g, kind, max_norm, scale, d_scratch, d_each, d_out, stream);
+}
+
+lct_status lct_norm_join(const lct_norm_t *d_parts, uint32_t count, int32_t kind, double max_norm,
+                         double scale, lct_norm_t *d_out, void *stream) {
+    if (count > 0 && !d_parts) return LCT_EINVAL;
+    if (!aligned(d_parts, 8)) return LCT_EALIGN;
+    lct_status st = check_norm_args(kind, max_norm, scale, d_out);
+    if (st != LCT_OK) return st;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    static_assert(sizeof(lct_norm_t) == 16 && offsetof(lct_norm_t, sum) == 0, "sums are every second double");
+    return norm_join(reinterpret_cast<const double *>(d_parts), count, 2, kind == LCT_NORM_L2, {max_norm, scale},
+                     nullptr, d_out, stream);
+}
+
+lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list *y, void *stream) {
+    lct_status st = check_list(x);
+    if (st == LCT_OK) st = check_list(y);
+    if (st != LCT_OK) return st;
+    if (!d_coef || x->count != y->count) return LCT_EINVAL;
+    if (!aligned(d_coef, 4)) return LCT_EALIGN;
+    for (uint32_t k = 0; k < x->count; ++k)
+        if (x->n[k] != y->n[k]) return LCT_EINVAL;
+    st = check_clip_alias(*x, d_coef, *y);
+    if (st != LCT_OK) return st;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    ListClipParams p;
+    memset(&p, 0, sizeof p);
+    p.coef = d_coef;
+    for (uint32_t k0 = 0; k0 < x->count; k0 += kClipMax) {
+        p.count = std::min(kClipMax, x->count - k0);
+        uint64_t c = 0;
+        for (uint32_t j = 0; j < p.count; ++j) {
+            p.x[j] = x->d_x[k0 + j];
+            p.y[j] = y->d_x[k0 + j];
+            p.n[j] = x->n[k0 + j] | ((uint64_t)(x->type[k0 + j] | (y->type[k0 + j] << 2)) << kListTypeShift);
+            p.chunk0[j] = (uint32_t)c;
+            c += (x->n[k0 + j] + kListChunk - 1) / kListChunk;
+        }
+        p.chunks = p.chunk0[p.count] = (uint32_t)c;
+        if (p.chunks == 0) continue;
+        const int e = launch_list_clip(p, std::min(kListGrid, p.chunks), stream);
+        if (e != hipSuccess) return hip_fail(e, "clip launch");
+    }
+    return LCT_OK;
 }
 
 const char *lct_strerror(lct_status st) {

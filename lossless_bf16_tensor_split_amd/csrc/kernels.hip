@@ -1278,6 +1278,129 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_decode(const DecodeParams p)
     }
 }
 
+// ------------------------------------------------------------------ norm of the codes
+
+// The decoder's walk with every value joined into a norm in place of being
+// stored: a sum of squares in 64 bits, or the largest magnitude (its BF16 bits
+// without the sign, so that NaN is above infinity).  LDS as the decoder's; the
+// first 32 bytes take the waves' values at the block's end.
+template <bool SQ>
+struct CodeAcc {
+    double s = 0.0;
+    uint32_t m = 0;
+    // the value's fp32 bits
+    __device__ __forceinline__ void add(uint32_t f) {
+        if (SQ) {
+            const double d = (double)__uint_as_float(f);
+            s = __builtin_fma(d, d, s);
+        } else {
+            m = max(m, f & 0x7FFF0000u);
+        }
+    }
+};
+
+template <bool FAST, uint32_t CAPT, bool SQ>
+__device__ __forceinline__ void norm_stream(const CodeNormParams &p, uint32_t row0, uint32_t n_s, uint32_t c_s,
+                                            const uint8_t *sfu, uint64_t sp0, CodeAcc<SQ> &acc) {
+    const uint32_t s = lane();
+    const uint32_t npos = p.block_elems / NS;
+    const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap_of<CAPT>(p.cap_words) - 2;
+    const uint8_t *sfs = sfu + s;
+    Reader rd;
+    rd.init(row0, s);
+    triple_buffered<Buf1>(
+        npos, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FAST>(bf.v, sfs, j0, n_s); },
+        [&](Buf1 &bf, uint32_t j0) {
+            if (FAST) {
+                // four fields per window, as the decoder reads them; a window
+                // that ran out is read again one field at a time
+#pragma unroll
+                for (uint32_t g = 0; g < CH; g += 4) {
+                    const int32_t q0 = rd.q;
+                    uint32_t e23[4];
+                    const uint32_t c = rd.next_n<4>(kDecTab, qmax, e23);
+                    if (__builtin_expect(!__all(c <= 30), 0)) {
+                        rd.q = q0;
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            e23[k] = rd.next(kDecTab);
+                            rd.q = min(rd.q, qmax);
+                        }
+                    }
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) acc.add(join32(bf.v[g + k], e23[k]));
+                }
+                return;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < CH; ++i) {
+                const uint32_t j = j0 + i;
+                uint32_t e23 = rd.next(kDecTab);
+                rd.q = min(rd.q, qmax);
+                if (j >= c_s && j < n_s) {
+                    const uint64_t k = sp0 + (j - c_s);
+                    e23 = (k < p.ovf_cap ? (uint32_t)p.ovf[k] : 0u) << 23;
+                }
+                if (j < n_s) acc.add(join32(bf.v[i], e23));
+            }
+        });
+}
+
+template <uint32_t CAPT, bool GROUP, bool SQ>
+__global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p) {
+    const uint32_t b = blockIdx.x, h = wave_id();   // a workgroup is a block's four units
+    const uint32_t k = GROUP ? p.grp.blk_tensor[b] : 0u;
+    stage_dec(GROUP ? p.grp.dec[k] : p.dec, kDecTab);
+    __syncthreads();
+    const uint32_t l = lane();
+    const uint32_t cap = cap_of<CAPT>(p.cap_words);
+    const uint32_t base = kDecWave0 + wave_id() * dec_wave_bytes(cap);
+    const uint32_t row0 = base + ROWB;
+    st32(base + 4 * l, 0);                      // row -1
+    st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
+    rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
+    const BlockSpan sp = GROUP ? group_span(p.grp, k, p.block_elems, b) : flat_span(nullptr, p.n, p.block_elems, b);
+    const uint32_t nb = sp.nb;
+    const uint32_t n_s = stream_len(nb, h * US + l);
+    const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
+    const uint8_t *sfu = p.sf + sp.sf0 + h * US;
+    CodeAcc<SQ> acc;
+    if (nb == p.block_elems && ob0 == ob1) {
+        norm_stream<true, CAPT, SQ>(p, row0, n_s, n_s, sfu, 0, acc);
+    } else {
+        uint32_t c_s, excl;
+        unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
+        norm_stream<false, CAPT, SQ>(p, row0, n_s, c_s, sfu, ob0 + excl, acc);
+    }
+    // the wave's value, then the block's, in a fixed order
+    double v = SQ ? acc.s : 0.0;
+    uint32_t m = acc.m;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        if (SQ)
+            v += __shfl_xor(v, d, 64);
+        else
+            m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    }
+    if (l == 0) {
+        const uint64_t bits = SQ ? (uint64_t)__double_as_longlong(v) : m;
+        st32(8 * h, (uint32_t)bits);
+        st32(8 * h + 4, (uint32_t)(bits >> 32));
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    if (SQ) {
+        v = 0.0;
+        for (uint32_t j = 0; j < kDecWaves; ++j)
+            v += __longlong_as_double((long long)(((uint64_t)ld32(8 * j + 4) << 32) | ld32(8 * j)));
+        p.part[b] = v;
+    } else {
+        m = 0;
+        for (uint32_t j = 0; j < kDecWaves; ++j) m = max(m, ld32(8 * j));
+        p.part[b] = (double)__uint_as_float(m);
+    }
+}
+
 // ------------------------------------------------------------------ fused SGD
 
 constexpr uint32_t kSgdWaves = 2;
@@ -1313,6 +1436,13 @@ struct SgdLayout {
           end(z2 + ROWB) {}
 };
 __host__ __device__ constexpr uint32_t sgd_wave_bytes(uint32_t cap) { return SgdLayout(cap, 0).end; }
+
+// A clipped update's coefficient (a device scalar, the same for every lane);
+// 1, which changes no product, where there is none.
+__device__ __forceinline__ float device_factor(const float *coef) {
+    if (!coef) return 1.0f;
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(*coef)));
+}
 
 // One element: rne_bf16(fmaf(-eta, m, w)) in bits 31..16 of the result (bits
 // 15..0 hold rounding garbage); a NaN gives 0x7FC0.
@@ -1457,7 +1587,7 @@ struct RingReader {
 template <uint32_t CAPT>
 __device__ __forceinline__ void sgd_stream_general(const SgdParams &p, const SgdLayout &lay, PayWriter &st,
                                                    uint32_t n_s, uint32_t cw_s, uint32_t cm_s,
-                                                   uint64_t r0, uint64_t wsp, uint64_t msp) {
+                                                   uint64_t r0, uint64_t wsp, uint64_t msp, float mul) {
     const uint32_t s = lane();
     const uint32_t npos = p.block_elems / NS;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
@@ -1503,7 +1633,7 @@ __device__ __forceinline__ void sgd_stream_general(const SgdParams &p, const Sgd
                         const uint64_t k = msp + (j - cm_s);
                         em = (k < p.m_ovf_cap ? (uint32_t)p.m_ovf[k] : 0u) << 23;
                     }
-                    const uint32_t R = sgd_round(join32(bf.w[i], ew), join32(bf.m[i], em), p.mul);
+                    const uint32_t R = sgd_round(join32(bf.w[i], ew), join32(bf.m[i], em), mul);
                     if (j < n_s) o[i * NS] = (uint8_t)(sgd_sf16(R) >> 16);
                     e[i] = (R >> 20) & 0x7F8u;   // 8 * exponent field
                 }
@@ -1533,7 +1663,7 @@ __device__ __forceinline__ void sgd_stream_general(const SgdParams &p, const Sgd
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k) {
                         const uint32_t i = g + k;
-                        const uint32_t R = sgd_round(join32(bf.w[i], ew[k]), join32(bf.m[i], em[k]), p.mul);
+                        const uint32_t R = sgd_round(join32(bf.w[i], ew[k]), join32(bf.m[i], em[k]), mul);
                         if (j0 + i < n_s) o[i * NS] = (uint8_t)(sgd_sf16(R) >> 16);
                         e[i] = (R >> 20) & 0x7F8u;
                     }
@@ -1573,7 +1703,7 @@ struct HalfRegs {
 // M's payload (ring only).
 template <uint32_t CAPT, bool RING, class Lay>
 __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &lay, PayWriter &st,
-                                                uint64_t r0, const uint32_t *mrows) {
+                                                uint64_t r0, const uint32_t *mrows, float mul) {
     constexpr uint32_t TB = RING ? kRingTab : 0u;
     constexpr uint32_t tabE = TB + kSgdETab, tabW = TB + kSgdWTab, tabM = TB + kSgdMTab;
     const uint32_t l = lane();
@@ -1693,7 +1823,7 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
                 wkm = winm >> cm;
                 enm = ld32(tabM + (wkm & 0x3FCu));
             }
-            r[k] = __builtin_fmaf(p.mul, __uint_as_float(join32s(msP[k], emP[k], jsel)),
+            r[k] = __builtin_fmaf(mul, __uint_as_float(join32s(msP[k], emP[k], jsel)),
                                   __uint_as_float(join32s(wsP[k], ewP[k], jsel)));
             nan |= r[k] != r[k];
             if (k & 1) {
@@ -1742,9 +1872,9 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
 #pragma unroll
             for (uint32_t k = 0; k < 4; k += 2) {
                 const uint32_t R0 =
-                    sgd_round(join32s(wsP[k], ewP[k], jsel), join32s(msP[k], emP[k], jsel), p.mul);
+                    sgd_round(join32s(wsP[k], ewP[k], jsel), join32s(msP[k], emP[k], jsel), mul);
                 const uint32_t R1 = sgd_round(join32s(wsP[k + 1], ewP[k + 1], jsel),
-                                              join32s(msP[k + 1], emP[k + 1], jsel), p.mul);
+                                              join32s(msP[k + 1], emP[k + 1], jsel), mul);
                 const uint32_t hh = (R0 >> 16) | (R1 & 0xFFFF0000u);
                 ep[k] = (hh >> 4) & 0x7F8u;
                 ep[k + 1] = (hh >> 20) & 0x7F8u;
@@ -1883,6 +2013,7 @@ void k_sgd(const SgdParams p) {
     __syncthreads();
     uint64_t staged = ~0ull;   // the group tables in LDS: W's (and W''s) and M's, as table indices
     const uint32_t l = lane();
+    const float mul = p.mul * device_factor(p.coef);
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const SgdLayout lay(cap, kSgdWave0 + wave_id() * sgd_wave_bytes(cap));
     st32(lay.z0 + 4 * l, 0);
@@ -1944,7 +2075,7 @@ void k_sgd(const SgdParams p) {
         st.init(0, l, n_s);
         st.rows.init(p.o_pay, b, h, cap);
         if (!GEN) {
-            sgd_stream_full<CAPT, false>(p, lay, st, r0 + h * US, nullptr);
+            sgd_stream_full<CAPT, false>(p, lay, st, r0 + h * US, nullptr, mul);
             ++nfull;
             const UnitOut o{p.o_pay, p.o_cnt, p.scratch, p.nblk, p.ovf_cap, cap, 0, 0};
             unit_finish(st, n_s, u, b, h, 0, o);
@@ -1952,7 +2083,7 @@ void k_sgd(const SgdParams p) {
             uint32_t cw_s, cm_s, wex, mex;
             unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
             unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
-            sgd_stream_general<CAPT>(p, lay, st, n_s, cw_s, cm_s, r0 + h * US, wob + wex, mob + mex);
+            sgd_stream_general<CAPT>(p, lay, st, n_s, cw_s, cm_s, r0 + h * US, wob + wex, mob + mex, mul);
             // The result's counts overwrite W's when the update is in place:
             // other units of this block may still read W's, so they are
             // parked and put in place by the placing kernel.  (The
@@ -2026,6 +2157,7 @@ void k_sgd_ring(const SgdParams p) {
     __syncthreads();
     uint64_t staged = ~0ull;
     const uint32_t l = lane(), h = wave_id();
+    const float mul = p.mul * device_factor(p.coef);
     const RingLayout lay(cap, h * kRingWaveB);
     st32(lay.z0 + 4 * l, 0);
     st32(lay.z1 + 4 * l, 0);
@@ -2064,7 +2196,7 @@ void k_sgd_ring(const SgdParams p) {
         PayWriter st;
         st.init(0, l, n_s);
         st.rows.init(p.o_pay, b, h, cap);
-        sgd_stream_full<cap, true>(p, lay, st, r0 + h * US, p.m_pay + ((uint64_t)b * cap * NS + h * US));
+        sgd_stream_full<cap, true>(p, lay, st, r0 + h * US, p.m_pay + ((uint64_t)b * cap * NS + h * US), mul);
         ++nfull;
         const UnitOut o{p.o_pay, p.o_cnt, p.scratch, p.nblk, p.ovf_cap, cap, 0, 0};
         unit_finish(st, n_s, b * kMaxUnits + h, b, h, 0, o);
@@ -2102,12 +2234,20 @@ __device__ __forceinline__ void stage_enc_packed(const uint32_t *t, uint32_t tab
     }
 }
 
+// The gradient of a step from its BF16 bits, as fp32 bits: g, or the clipped
+// step's c * g, rounded to fp32 before it enters the momentum's fmaf.
+template <bool CLIP>
+__device__ __forceinline__ uint32_t gradient(uint32_t g, float c) {
+    return CLIP ? __float_as_uint(c * __uint_as_float(g << 16)) : g << 16;
+}
+
 // General path (partial blocks and inputs with spilled fields): byte-wide
 // accesses with per-element checks.
-template <uint32_t CAPT>
+template <uint32_t CAPT, bool CLIP>
 __device__ __forceinline__ void mom_stream_general(const MomParams &p, const SgdLayout &lay, PayWriter &stw,
                                                    PayWriter &stm, uint32_t n_s, uint32_t cw_s, uint32_t cm_s,
-                                                   uint64_t r0, const uint16_t *gu, uint64_t wsp, uint64_t msp) {
+                                                   uint64_t r0, const uint16_t *gu, uint64_t wsp, uint64_t msp,
+                                                   float c) {
     const uint32_t s = lane();
     const uint32_t npos = p.block_elems / NS;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
@@ -2159,7 +2299,7 @@ __device__ __forceinline__ void mom_stream_general(const MomParams &p, const Sgd
                         const uint64_t k = msp + (j - cm_s);
                         fm = (k < p.m_ovf_cap ? (uint32_t)p.m_ovf[k] : 0u) << 23;
                     }
-                    const uint32_t Rm = sgd_round(bf.g[i] << 16, join32(bf.m[i], fm), p.mu);
+                    const uint32_t Rm = sgd_round(gradient<CLIP>(bf.g[i], c), join32(bf.m[i], fm), p.mu);
                     const uint32_t Rw = sgd_round(join32(bf.w[i], fw), Rm & 0xFFFF0000u, p.neg_eta);
                     if (j < n_s) {
                         ow[i * NS] = (uint8_t)(sgd_sf16(Rw) >> 16);
@@ -2192,7 +2332,7 @@ __device__ __forceinline__ void mom_stream_general(const MomParams &p, const Sgd
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k) {
                         const uint32_t i = g4 + k;
-                        const uint32_t Rm = sgd_round(bf.g[i] << 16, join32(bf.m[i], fm[k]), p.mu);
+                        const uint32_t Rm = sgd_round(gradient<CLIP>(bf.g[i], c), join32(bf.m[i], fm[k]), p.mu);
                         const uint32_t Rw = sgd_round(join32(bf.w[i], fw[k]), Rm & 0xFFFF0000u, p.neg_eta);
                         if (j0 + i < n_s) {
                             ow[i * NS] = (uint8_t)(sgd_sf16(Rw) >> 16);
@@ -2214,9 +2354,9 @@ __device__ __forceinline__ void mom_stream_general(const MomParams &p, const Sgd
 
 // Full-block path (every stream has npos elements and no input field
 // spilled): the update's pipeline with both products and both writers.
-template <uint32_t CAPT>
+template <uint32_t CAPT, bool CLIP>
 __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLayout &lay, PayWriter &stw,
-                                                PayWriter &stm, uint64_t r0, const uint16_t *gu) {
+                                                PayWriter &stm, uint64_t r0, const uint16_t *gu, float c) {
     const uint32_t l = lane();
     const uint32_t npos = p.block_elems / NS;
     const uint32_t nh = npos / CH;
@@ -2332,7 +2472,7 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
                 enm = ld32(kMMD + (wkm & 0x3FCu));
             }
             rmv[k] = __builtin_fmaf(p.mu, __uint_as_float(join32s(msP[k], emP[k], jsel)),
-                                    __uint_as_float(gP[k] << 16));
+                                    __uint_as_float(gradient<CLIP>(gP[k], c)));
             if (k & 1) {
                 // M' of the pair, rounded; W' from M' as rounded
                 uint32_t hm = cvt_bf16x2(rmv[k - 1], rmv[k]);
@@ -2392,8 +2532,9 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
             // becomes the canonical one's)
 #pragma unroll
             for (uint32_t k = 0; k < 4; k += 2) {
-                const uint32_t Rm0 = sgd_round(gP[k] << 16, join32s(msP[k], emP[k], jsel), p.mu);
-                const uint32_t Rm1 = sgd_round(gP[k + 1] << 16, join32s(msP[k + 1], emP[k + 1], jsel), p.mu);
+                const uint32_t Rm0 = sgd_round(gradient<CLIP>(gP[k], c), join32s(msP[k], emP[k], jsel), p.mu);
+                const uint32_t Rm1 = sgd_round(gradient<CLIP>(gP[k + 1], c), join32s(msP[k + 1], emP[k + 1], jsel),
+                                               p.mu);
                 const uint32_t Rw0 = sgd_round(join32s(wsP[k], ewP[k], jsel), Rm0 & 0xFFFF0000u, p.neg_eta);
                 const uint32_t Rw1 = sgd_round(join32s(wsP[k + 1], ewP[k + 1], jsel), Rm1 & 0xFFFF0000u,
                                                p.neg_eta);
@@ -2473,7 +2614,8 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
 }
 
 // GEN: the general kernel (blocks that are not full), as for the update.
-template <uint32_t CAPT, bool GROUP, bool GEN>
+// CLIP: the clipped step's, whose gradient is c * g.
+template <uint32_t CAPT, bool GROUP, bool GEN, bool CLIP>
 __global__ __launch_bounds__(64 * kMomWaves) __attribute__((amdgpu_waves_per_eu(2)))
 void k_mom(const MomParams p) {
     if (!GROUP) {
@@ -2486,6 +2628,7 @@ void k_mom(const MomParams p) {
     __syncthreads();
     uint64_t staged = ~0ull;
     const uint32_t l = lane();
+    const float c = CLIP ? device_factor(p.coef) : 1.0f;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const SgdLayout lay(cap, kMWave0 + wave_id() * sgd_wave_bytes(cap));
     st32(lay.z0 + 4 * l, 0);
@@ -2539,13 +2682,14 @@ void k_mom(const MomParams p) {
         stm.init(0, l, n_s);
         stm.rows.init(p.om_pay, b, h, cap);
         if (!GEN) {
-            mom_stream_full<CAPT>(p, lay, stw, stm, r0 + h * US, gu);
+            mom_stream_full<CAPT, CLIP>(p, lay, stw, stm, r0 + h * US, gu, c);
             ++nfull;
         } else {
             uint32_t cw_s, cm_s, wex, mex;
             unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
             unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
-            mom_stream_general<CAPT>(p, lay, stw, stm, n_s, cw_s, cm_s, r0 + h * US, gu, wob + wex, mob + mex);
+            mom_stream_general<CAPT, CLIP>(p, lay, stw, stm, n_s, cw_s, cm_s, r0 + h * US, gu, wob + wex, mob + mex,
+                                           c);
         }
         // in place, the general kernel parks the counts (other units of the
         // block still read the inputs'); the full-block kernel reads none
@@ -2669,12 +2813,17 @@ int launch_encode(const EncodeParams &p, void *stream, bool group) {
                   g_lds_granted[group ? 3 : 0][cap_slot(p.cap_words)]);
 }
 
-template <uint32_t C> struct MomK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, false>); } };
-template <uint32_t C> struct MomGK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, false>); } };
-template <uint32_t C> struct MomXK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, true>); } };
-template <uint32_t C> struct MomGXK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, true>); } };
-// flat, group, and their general kernels
-std::atomic<size_t> g_mom_lds_granted[4][4];
+template <uint32_t C> struct MomK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, false, false>); } };
+template <uint32_t C> struct MomGK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, false, false>); } };
+template <uint32_t C> struct MomXK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, true, false>); } };
+template <uint32_t C> struct MomGXK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, true, false>); } };
+// the clipped steps'
+template <uint32_t C> struct MomCK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, false, true>); } };
+template <uint32_t C> struct MomGCK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, false, true>); } };
+template <uint32_t C> struct MomXCK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, false, true, true>); } };
+template <uint32_t C> struct MomGXCK { static const void *fn() { return reinterpret_cast<const void *>(&k_mom<C, true, true, true>); } };
+// flat, group, and their general kernels; then the clipped steps'
+std::atomic<size_t> g_mom_lds_granted[8][4];
 
 // The full-block kernel, then the general one (which ends at once when every
 // block is full).
@@ -2682,19 +2831,38 @@ int launch_mom(const MomParams &p, void *stream, bool group) {
     const size_t lds = kMWave0 + (size_t)kMomWaves * sgd_wave_bytes(p.cap_words);
     const int slot = cap_slot(p.cap_words);
     // persistent: one workgroup is one block at a time
-    const void *fn = group ? ByCap<MomGK>::pick(p.cap_words) : ByCap<MomK>::pick(p.cap_words);
-    int e = launch(fn, (uint64_t)p.nblk * kMomWaves, kMomWaves, true, lds, p, stream,
-                   g_mom_lds_granted[group ? 1 : 0][slot]);
+    const uint32_t cap = p.cap_words;
+    const bool clip = p.coef != nullptr;
+    const void *fn = clip ? (group ? ByCap<MomGCK>::pick(cap) : ByCap<MomCK>::pick(cap))
+                          : (group ? ByCap<MomGK>::pick(cap) : ByCap<MomK>::pick(cap));
+    const int base = (clip ? 4 : 0) + (group ? 1 : 0);
+    int e = launch(fn, (uint64_t)p.nblk * kMomWaves, kMomWaves, true, lds, p, stream, g_mom_lds_granted[base][slot]);
     if (e != hipSuccess) return e;
-    fn = group ? ByCap<MomGXK>::pick(p.cap_words) : ByCap<MomXK>::pick(p.cap_words);
+    fn = clip ? (group ? ByCap<MomGXCK>::pick(cap) : ByCap<MomXCK>::pick(cap))
+              : (group ? ByCap<MomGXK>::pick(cap) : ByCap<MomXK>::pick(cap));
     return launch(fn, (uint64_t)p.nblk * kMomWaves, kMomWaves, true, lds, p, stream,
-                  g_mom_lds_granted[group ? 3 : 2][slot]);
+                  g_mom_lds_granted[base + 2][slot]);
 }
 
 int launch_decode(const DecodeParams &p, void *stream, bool group) {
     const void *fn = group ? ByCap<DecGK>::pick(p.cap_words) : ByCap<DecK>::pick(p.cap_words);
     return launch(fn, (uint64_t)p.nblk * kMaxUnits, kDecWaves, false, decode_lds(p.cap_words), p, stream,
                   g_lds_granted[group ? 4 : 1][cap_slot(p.cap_words)]);
+}
+
+template <uint32_t C> struct NormK { static const void *fn() { return reinterpret_cast<const void *>(&k_norm<C, false, true>); } };
+template <uint32_t C> struct NormGK { static const void *fn() { return reinterpret_cast<const void *>(&k_norm<C, true, true>); } };
+template <uint32_t C> struct MaxK { static const void *fn() { return reinterpret_cast<const void *>(&k_norm<C, false, false>); } };
+template <uint32_t C> struct MaxGK { static const void *fn() { return reinterpret_cast<const void *>(&k_norm<C, true, false>); } };
+// flat and group, sums of squares and largest magnitudes
+std::atomic<size_t> g_norm_lds_granted[4][4];
+
+int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *stream) {
+    const uint32_t cap = p.cap_words;
+    const void *fn = squares ? (group ? ByCap<NormGK>::pick(cap) : ByCap<NormK>::pick(cap))
+                             : (group ? ByCap<MaxGK>::pick(cap) : ByCap<MaxK>::pick(cap));
+    return launch(fn, (uint64_t)p.nblk * kMaxUnits, kDecWaves, false, decode_lds(cap), p, stream,
+                  g_norm_lds_granted[(squares ? 0 : 2) + (group ? 1 : 0)][cap_slot(cap)]);
 }
 
 std::atomic<size_t> g_ring_granted[2];

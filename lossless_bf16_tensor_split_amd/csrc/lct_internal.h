@@ -169,6 +169,7 @@ struct SgdParams {
     uint64_t n;
     uint32_t block_elems, cap_words, nblk;
     float mul;           // the product's factor: -eta, for W - eta*M
+    const float *coef;   // a device factor of mul (null: 1)
     uint32_t park_cnt;   // the result's counts overwrite W's: park them in scratch
     GroupRef gw, gm;     // used by the group kernels only (W's codes for W and W';
                          // M's for M)
@@ -217,6 +218,7 @@ struct MomParams {
     float mu, neg_eta;
     uint32_t park_w, park_m;   // an output's counts overwrite its input's: park them
     uint32_t pad0;
+    const float *coef;         // clip kernels only: a device factor of g
     GroupRef gw, gm, gg;       // group kernels: W's and M's codes, the gradients' buffers
     uint32_t wenc[256], menc[256];   // packed: bits | len << 24 (W' and M')
     DecTab wdec, mdec;
@@ -252,6 +254,81 @@ struct FitParams {
     int32_t *shift_out;      // may be null
 };
 
+// Norms: the scale of the values and the norm to clip to.
+struct NormArgs {
+    double max_norm, scale;
+};
+
+// Lists of dense tensors: cut into chunks of kListChunk elements, numbered
+// through a launch's tensors (chunk0[k]: tensor k's first; chunk0[count]: all
+// of them).  A size travels with its element types above kListTypeShift.
+constexpr uint32_t kNormThreads = 256;
+constexpr uint32_t kListChunk = 16384;
+constexpr uint32_t kListMax = 192;        // tensors per launch of the norm
+constexpr uint32_t kClipMax = 128;        // and of the clip
+constexpr uint32_t kListGrid = 2048;      // workgroups per launch at most: eight per CU
+constexpr uint32_t kListTypeShift = 48;
+constexpr uint64_t kListElems = (1ull << kListTypeShift) - 1;
+constexpr uint64_t kListMaxElems = 1ull << 44;   // of a whole list: chunk numbers stay within 32 bits
+struct ListNormParams {
+    double *run;          // a value per workgroup
+    double *piece;        // a value per workgroup and tensor that meet (null: not wanted)
+    uint32_t count, chunks;
+    const void *x[kListMax];
+    uint64_t n[kListMax];
+    uint32_t chunk0[kListMax + 1];
+};
+struct ListEachParams {
+    const double *piece;
+    float *each;
+    NormArgs args;
+    uint32_t count, chunks, G;   // G: the norm launch's workgroups
+    bool squares;
+    uint32_t chunk0[kListMax + 1];
+};
+// Part values (every `stride`-th double) joined by the launch's workgroups,
+// into a value each (fold) or, by a single one, into the result (out).
+struct NormJoinParams {
+    const double *part;
+    uint64_t count, stride;
+    double *fold;
+    lct_norm_t *out;
+    NormArgs args;
+    bool squares;
+};
+struct ListClipParams {
+    const float *coef;
+    uint32_t count, chunks;
+    const void *x[kClipMax];
+    void *y[kClipMax];
+    uint64_t n[kClipMax];        // types: x's | y's << 2
+    uint32_t chunk0[kClipMax + 1];
+};
+// Norm of a compressed tensor (or a group's): a value per block.
+struct CodeNormParams {
+    const uint8_t *sf;
+    const uint32_t *pay;
+    const uint16_t *cnt;
+    const uint64_t *obase;
+    const uint8_t *ovf;
+    uint64_t ovf_cap;
+    uint64_t n;
+    uint32_t block_elems, cap_words, nblk, pad0;
+    double *part;
+    GroupRef grp;         // used by the group kernels only
+    DecTab dec;
+};
+// Scratch of the norms, in doubles: the blocks' (or launches' workgroups')
+// values, then the values they are folded into when there are many.
+constexpr uint64_t kFoldFrom = 4096;      // more part values than this are folded first
+constexpr uint32_t kFoldGrid = 256;
+inline uint64_t list_launches(uint64_t count) { return (count + kListMax - 1) / kListMax; }
+inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
+    const uint64_t runs = list_launches(count) * kListGrid;
+    const uint64_t list = runs + list_launches(count) * (kListGrid + kListMax);
+    return align256(8 * ((list > nblk ? list : nblk) + kFoldGrid));
+}
+
 // The allocation-free update's static working memory (per device).
 constexpr uint64_t kNoAllocScratch = LCT_NOALLOC_SCRATCH_BYTES;
 constexpr int kMaxDevices = 64;
@@ -272,6 +349,14 @@ int launch_gather(const uint16_t *x, uint64_t n, uint32_t m, void *stream, uint1
 int launch_sample(const SampleParams &p, void *stream, uint16_t *host_out);
 // The device fit (enqueues only).
 int launch_fit(const FitParams &p, void *stream);
+// Norms and clipping (norms.hip; the codes' norm in kernels.hip).
+int launch_list_norm(const ListNormParams &p, uint32_t grid, bool squares, void *stream);
+int launch_list_each(const ListEachParams &p, void *stream);
+int launch_norm_join(const NormJoinParams &p, uint32_t grid, void *stream);
+int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part, const NormArgs &args, bool squares,
+                      float *each, void *stream);
+int launch_list_clip(const ListClipParams &p, uint32_t grid, void *stream);
+int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *stream);
 
 // Host codebook construction (codebook.cpp).
 // The model's probability of each exponent field (its range of |x|).

@@ -1,0 +1,439 @@
+// norms.hip -- norms of many dense tensors, the clip coefficient, and the
+// scaling of many tensors by it, for CDNA4 (gfx950, wave64).
+//
+// A list's tensors are cut into chunks of kListChunk elements, numbered
+// through the list; a launch covers at most kListMax tensors, whose pointers
+// and sizes travel as kernel arguments (no table to upload, so tensors may
+// move from step to step).  Sums of squares are kept in 64 bits from the
+// first product on: a BF16 or FP32 square does not fit 32 bits for values
+// past 2^64 or below 2^-75, and the sum then needs no care for its order or
+// length.  The order is fixed all the same (no atomics), so equal calls give
+// equal bits.  The largest magnitude is an integer maximum of the values'
+// bits without their sign, which puts infinity above every finite value and
+// NaN above infinity: a NaN is never lost.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "lct_internal.h"
+
+namespace lct {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes that start at any element (tensors may be views at any offset)
+typedef uint32_t u32x4e __attribute__((ext_vector_type(4), aligned(2)));
+
+constexpr uint32_t kWaves = kNormThreads / 64;
+
+// ------------------------------------------------------------------ accumulators
+
+// A running sum of squares (in 64 bits), or the running maximum of the
+// magnitudes' bits.
+struct SumSq {
+    double a = 0.0, b = 0.0;
+    __device__ __forceinline__ void add(float x, float y) {
+        a = __builtin_fma((double)x, (double)x, a);
+        b = __builtin_fma((double)y, (double)y, b);
+    }
+    __device__ __forceinline__ double value() const { return a + b; }
+    __device__ static __forceinline__ double join(double x, double y) { return x + y; }
+};
+struct MaxAbs {
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(float x, float y) {
+        m = max(m, max(__float_as_uint(x) & 0x7FFFFFFFu, __float_as_uint(y) & 0x7FFFFFFFu));
+    }
+    __device__ __forceinline__ double value() const { return (double)__uint_as_float(m); }
+    // of two magnitudes, NaN above all
+    __device__ static __forceinline__ double join(double x, double y) {
+        const uint64_t a = (uint64_t)__double_as_longlong(x) & ~(1ull << 63);
+        const uint64_t b = (uint64_t)__double_as_longlong(y) & ~(1ull << 63);
+        return __longlong_as_double((long long)(a > b ? a : b));
+    }
+};
+
+template <class A>
+__device__ __forceinline__ double wave_join(double v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v = A::join(v, __shfl_xor(v, d, 64));
+    return v;
+}
+
+// The workgroup's value in every thread; `slots` holds one double per wave.
+// A barrier before the first store lets slots be used again at once.
+template <class A>
+__device__ __forceinline__ double group_join(double v, double *slots) {
+    v = wave_join<A>(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double r = slots[0];
+    for (uint32_t k = 1; k < blockDim.x / 64; ++k) r = A::join(r, slots[k]);
+    return r;
+}
+
+// ------------------------------------------------------------------ values
+
+template <int TYPE>
+constexpr uint32_t per16() { return TYPE == LCT_FP32 ? 4 : 8; }
+
+__device__ __forceinline__ float half_bits(uint32_t h) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+
+template <int TYPE>
+__device__ __forceinline__ float element(const void *x, uint64_t i) {
+    if (TYPE == LCT_FP32) return static_cast<const float *>(x)[i];
+    const uint32_t b = static_cast<const uint16_t *>(x)[i];
+    return TYPE == LCT_BF16 ? __uint_as_float(b << 16) : half_bits(b);
+}
+
+// The elements of 16 bytes, as floats.
+template <int TYPE>
+__device__ __forceinline__ void unpack(u32x4 v, float (&f)[per16<TYPE>()]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (TYPE == LCT_FP32) {
+            f[k] = __uint_as_float(v[k]);
+        } else if constexpr (TYPE == LCT_BF16) {
+            f[2 * k] = __uint_as_float(v[k] << 16);
+            f[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u);
+        } else {
+            f[2 * k] = half_bits(v[k] & 0xFFFFu);
+            f[2 * k + 1] = half_bits(v[k] >> 16);
+        }
+    }
+}
+
+template <int TYPE, class A>
+__device__ __forceinline__ void add16(u32x4 v, A &acc) {
+    float f[per16<TYPE>()];
+    unpack<TYPE>(v, f);
+#pragma unroll
+    for (uint32_t k = 0; k < per16<TYPE>(); k += 2) acc.add(f[k], f[k + 1]);
+}
+
+// Elements [e0, e0 + m) of x into acc, by `threads` threads of which this is
+// number t.
+template <int TYPE, class A>
+__device__ __forceinline__ void add_range(const void *x, uint64_t e0, uint32_t m, uint32_t t, uint32_t threads,
+                                          A &acc) {
+    constexpr uint32_t V = per16<TYPE>();
+    constexpr uint32_t ES = TYPE == LCT_FP32 ? 4 : 2;
+    const char *p = static_cast<const char *>(x) + e0 * ES;
+    const uint32_t nv = m / V;
+    uint32_t v = t;
+    // eight loads in flight per thread
+    for (; v + 7 * threads < nv; v += 8 * threads) {
+        u32x4 r[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            r[k] = *reinterpret_cast<const u32x4e *>(p + 16ull * (v + k * threads));
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) add16<TYPE>(r[k], acc);
+    }
+    for (; v < nv; v += threads) add16<TYPE>(*reinterpret_cast<const u32x4e *>(p + 16ull * v), acc);
+    const uint32_t tail = m - nv * V;
+    if (t < tail) acc.add(element<TYPE>(x, e0 + nv * V + t), 0.0f);
+}
+
+template <class A>
+__device__ __forceinline__ void add_typed(uint32_t type, const void *x, uint64_t e0, uint32_t m, uint32_t t,
+                                          uint32_t threads, A &acc) {
+    if (type == LCT_BF16)
+        add_range<LCT_BF16>(x, e0, m, t, threads, acc);
+    else if (type == LCT_FP16)
+        add_range<LCT_FP16>(x, e0, m, t, threads, acc);
+    else
+        add_range<LCT_FP32>(x, e0, m, t, threads, acc);
+}
+
+// ------------------------------------------------------------------ results
+
+// The norm and the coefficient from the joined value (a sum of squares, or
+// the largest magnitude).  A NaN quotient stays NaN: no comparison with it
+// holds.
+__device__ __forceinline__ lct_norm_t result(double v, const NormArgs &a, bool squares) {
+    const double n = fabs(a.scale) * (squares ? sqrt(v) : v);
+    const double q = a.max_norm / (n + 1e-6);
+    lct_norm_t r;
+    r.sum = v;
+    r.norm = (float)n;
+    r.coef = (float)(a.scale * (q >= 1.0 ? 1.0 : q));
+    return r;
+}
+
+// The last tensor that starts at or before chunk c (tensors of no elements
+// have no chunks, so it is the one that holds c).
+__device__ __forceinline__ uint32_t tensor_of(const uint32_t *chunk0, uint32_t count, uint32_t c) {
+    uint32_t lo = 0, hi = count;   // chunk0[lo] <= c < chunk0[hi]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (chunk0[mid] <= c)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Workgroup i of G takes chunks [first(i), first(i + 1)); chunk c belongs to
+// workgroup owner(c).
+__device__ __forceinline__ uint32_t run_first(uint32_t i, uint32_t chunks, uint32_t G) {
+    return (uint32_t)((uint64_t)i * chunks / G);
+}
+__device__ __forceinline__ uint32_t run_owner(uint32_t c, uint32_t chunks, uint32_t G) {
+    return (uint32_t)((((uint64_t)c + 1) * G - 1) / chunks);
+}
+
+// ------------------------------------------------------------------ the list's norm
+
+// Each workgroup walks its run of chunks and leaves the run's value in
+// p.run[i]; where the tensors' own norms are wanted, the part of the run that
+// lies in tensor k goes to p.piece[i + k] (runs and tensors both ascend, so no
+// two pairs share a place).
+template <class A>
+__global__ __launch_bounds__(kNormThreads) void k_list_norm(const ListNormParams p) {
+    __shared__ double slots[kWaves];
+    const uint32_t i = blockIdx.x, G = gridDim.x;
+    uint32_t c = run_first(i, p.chunks, G);
+    const uint32_t end = run_first(i + 1, p.chunks, G);
+    uint32_t k = tensor_of(p.chunk0, p.count, c);
+    double run = 0.0;
+    A acc;
+    while (c < end) {
+        while (p.chunk0[k + 1] <= c) ++k;
+        const uint32_t stop = min(end, p.chunk0[k + 1]);
+        const uint64_t n = p.n[k] & kListElems;
+        const uint32_t type = (uint32_t)(p.n[k] >> kListTypeShift);
+        for (; c < stop; ++c) {
+            const uint64_t at = (uint64_t)(c - p.chunk0[k]) * kListChunk;
+            add_typed(type, p.x[k], at, (uint32_t)min<uint64_t>(kListChunk, n - at), threadIdx.x, kNormThreads, acc);
+        }
+        if (p.piece) {
+            const double v = group_join<A>(acc.value(), slots);
+            if (threadIdx.x == 0) p.piece[i + k] = v;
+            run = A::join(run, v);
+            acc = A();
+        }
+    }
+    if (!p.piece) run = group_join<A>(acc.value(), slots);
+    if (threadIdx.x == 0) p.run[i] = run;
+}
+
+// The norm of each of a launch's tensors, a wave per tensor.
+template <class A>
+__global__ __launch_bounds__(kNormThreads) void k_list_each(const ListEachParams p) {
+    const uint32_t k = blockIdx.x * kWaves + (threadIdx.x >> 6), l = threadIdx.x & 63;
+    if (k >= p.count) return;
+    double v = 0.0;
+    if (p.chunk0[k + 1] > p.chunk0[k]) {
+        const uint32_t a = run_owner(p.chunk0[k], p.chunks, p.G), b = run_owner(p.chunk0[k + 1] - 1, p.chunks, p.G);
+        for (uint32_t i = a + l; i <= b; i += 64) v = A::join(v, p.piece[i + k]);
+    }
+    v = wave_join<A>(v);
+    if (l == 0) p.each[k] = result(v, p.args, p.squares).norm;
+}
+
+// Part values joined by G workgroups into G values (G = 1: the result).
+template <class A>
+__global__ __launch_bounds__(1024) void k_norm_join(const NormJoinParams p) {
+    __shared__ double slots[16];
+    const uint64_t G = gridDim.x, i = blockIdx.x;
+    const uint64_t lo = i * p.count / G, hi = (i + 1) * p.count / G;
+    double v = 0.0;
+    for (uint64_t j = lo + threadIdx.x; j < hi; j += blockDim.x) v = A::join(v, p.part[j * p.stride]);
+    v = group_join<A>(v, slots);
+    if (threadIdx.x != 0) return;
+    if (p.fold)
+        p.fold[i] = v;
+    else
+        *p.out = result(v, p.args, p.squares);
+}
+
+// The norm of each tensor of a group from its blocks' values.
+template <class A>
+__global__ __launch_bounds__(kNormThreads) void k_group_each(const GroupEntry *ent, uint32_t count, const double *part,
+                                                             const NormArgs args, bool squares, float *each) {
+    __shared__ double slots[kWaves];
+    for (uint32_t k = blockIdx.x; k < count; k += gridDim.x) {
+        const GroupEntry e = ent[k];
+        double v = 0.0;
+        for (uint32_t j = threadIdx.x; j < e.nblk; j += kNormThreads) v = A::join(v, part[(uint64_t)e.blk0 + j]);
+        v = group_join<A>(v, slots);
+        if (threadIdx.x == 0) each[k] = result(v, args, squares).norm;
+    }
+}
+
+// ------------------------------------------------------------------ clip
+
+// x * c rounded to fp32.  The empty statement keeps the product in a register
+// of its own: the compiler otherwise makes one mixed-precision instruction of
+// it and a rounding to FP16 that follows, which skips the fp32 rounding, so
+// that the bits would depend on the code around.
+__device__ __forceinline__ float product(float x, float c) {
+    float p = x * c;
+    asm("" : "+v"(p));
+    return p;
+}
+
+// f rounded to a 16-bit type (nearest, ties to even; an overflow of FP16
+// gives infinity).
+template <int TYPE>
+__device__ __forceinline__ uint32_t round16(float f) {
+    if (TYPE == LCT_FP16) return __builtin_bit_cast(uint16_t, (_Float16)f);
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+// y[i] = c * x[i] for elements [e0, e0 + m).  Eight elements a thread and
+// step: one or two 16-byte accesses on either side.
+template <int FROM, int TO>
+__device__ __forceinline__ void clip_range(const void *x, void *y, uint64_t e0, uint32_t m, float c) {
+    constexpr uint32_t FS = FROM == LCT_FP32 ? 4 : 2, TS = TO == LCT_FP32 ? 4 : 2;
+    const char *px = static_cast<const char *>(x) + e0 * FS;
+    char *py = static_cast<char *>(y) + e0 * TS;
+    const uint32_t nv = m / 8;
+    auto load = [&](uint32_t v, u32x4 (&r)[FS / 2]) {
+#pragma unroll
+        for (uint32_t k = 0; k < FS / 2; ++k)
+            r[k] = *reinterpret_cast<const u32x4e *>(px + 8ull * FS * v + 16 * k);
+    };
+    auto store = [&](uint32_t v, const u32x4 (&r)[FS / 2]) {
+        float f[8];
+        if constexpr (FROM == LCT_FP32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(r[k / 4][k % 4]);
+        } else {
+            unpack<FROM>(r[0], f);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = product(f[k], c);
+        char *q = py + 8ull * TS * v;
+        if constexpr (TO == LCT_FP32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 o;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(f[4 * h + k]);
+                *reinterpret_cast<u32x4e *>(q + 16 * h) = o;
+            }
+        } else {
+            u32x4 o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = round16<TO>(f[2 * k]) | (round16<TO>(f[2 * k + 1]) << 16);
+            *reinterpret_cast<u32x4e *>(q) = o;
+        }
+    };
+    uint32_t v = threadIdx.x;
+    for (; v + 3 * kNormThreads < nv; v += 4 * kNormThreads) {
+        u32x4 r[4][FS / 2];
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) load(v + k * kNormThreads, r[k]);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) store(v + k * kNormThreads, r[k]);
+    }
+    for (; v < nv; v += kNormThreads) {
+        u32x4 r[FS / 2];
+        load(v, r);
+        store(v, r);
+    }
+    const uint32_t t = nv * 8 + threadIdx.x;
+    if (t < m) {
+        const float f = product(element<FROM>(px, t), c);
+        if constexpr (TO == LCT_FP32)
+            reinterpret_cast<float *>(py)[t] = f;
+        else
+            reinterpret_cast<uint16_t *>(py)[t] = (uint16_t)round16<TO>(f);
+    }
+}
+
+template <int FROM>
+__device__ __forceinline__ void clip_from(uint32_t to, const void *x, void *y, uint64_t e0, uint32_t m, float c) {
+    if (to == LCT_BF16)
+        clip_range<FROM, LCT_BF16>(x, y, e0, m, c);
+    else if (to == LCT_FP16)
+        clip_range<FROM, LCT_FP16>(x, y, e0, m, c);
+    else
+        clip_range<FROM, LCT_FP32>(x, y, e0, m, c);
+}
+
+__global__ __launch_bounds__(kNormThreads) void k_list_clip(const ListClipParams p) {
+    const float c = *p.coef;
+    const uint32_t G = gridDim.x;
+    uint32_t at = run_first(blockIdx.x, p.chunks, G);
+    const uint32_t end = run_first(blockIdx.x + 1, p.chunks, G);
+    uint32_t k = tensor_of(p.chunk0, p.count, at);
+    for (; at < end; ++at) {
+        while (p.chunk0[k + 1] <= at) ++k;
+        const uint32_t types = (uint32_t)(p.n[k] >> kListTypeShift);
+        const uint32_t from = types & 3u, to = types >> 2;
+        // in place, a coefficient of 1 leaves every value as it is
+        if (c == 1.0f && p.x[k] == p.y[k]) continue;
+        const uint64_t e0 = (uint64_t)(at - p.chunk0[k]) * kListChunk;
+        const uint32_t m = (uint32_t)min<uint64_t>(kListChunk, (p.n[k] & kListElems) - e0);
+        if (from == LCT_BF16)
+            clip_from<LCT_BF16>(to, p.x[k], p.y[k], e0, m, c);
+        else if (from == LCT_FP16)
+            clip_from<LCT_FP16>(to, p.x[k], p.y[k], e0, m, c);
+        else
+            clip_from<LCT_FP32>(to, p.x[k], p.y[k], e0, m, c);
+    }
+}
+
+template <class F>
+int launched(F f) {
+    f();
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_list_norm(const ListNormParams &p, uint32_t grid, bool squares, void *stream) {
+    return launched([&] {
+        if (squares)
+            hipLaunchKernelGGL(k_list_norm<SumSq>, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+        else
+            hipLaunchKernelGGL(k_list_norm<MaxAbs>, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+    });
+}
+
+int launch_list_each(const ListEachParams &p, void *stream) {
+    const dim3 grid((p.count + kWaves - 1) / kWaves);
+    return launched([&] {
+        if (p.squares)
+            hipLaunchKernelGGL(k_list_each<SumSq>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, p);
+        else
+            hipLaunchKernelGGL(k_list_each<MaxAbs>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, p);
+    });
+}
+
+int launch_norm_join(const NormJoinParams &p, uint32_t grid, void *stream) {
+    return launched([&] {
+        if (p.squares)
+            hipLaunchKernelGGL(k_norm_join<SumSq>, dim3(grid), dim3(1024), 0, (hipStream_t)stream, p);
+        else
+            hipLaunchKernelGGL(k_norm_join<MaxAbs>, dim3(grid), dim3(1024), 0, (hipStream_t)stream, p);
+    });
+}
+
+int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part, const NormArgs &args, bool squares,
+                      float *each, void *stream) {
+    const dim3 grid(std::min<uint32_t>(count, 4096));
+    return launched([&] {
+        if (squares)
+            hipLaunchKernelGGL(k_group_each<SumSq>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, ent, count, part,
+                               args, squares, each);
+        else
+            hipLaunchKernelGGL(k_group_each<MaxAbs>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, ent, count,
+                               part, args, squares, each);
+    });
+}
+
+int launch_list_clip(const ListClipParams &p, uint32_t grid, void *stream) {
+    return launched([&] {
+        hipLaunchKernelGGL(k_list_clip, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+    });
+}
+
+}  // namespace lct

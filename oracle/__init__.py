@@ -90,6 +90,9 @@ def lib():
         L.lcto_sgd_elem.argtypes = [C.c_uint16, C.c_uint16, C.c_float]
         L.lcto_sgd.argtypes = ([P, P, P, P, P, P] + [P, P, P, P, P, P] +
                                [C.c_float, P, u64, u32, u32, P, P, P, P, P, u64])
+        L.lcto_momentum_clip_dense.restype = None
+        L.lcto_momentum_clip_dense.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_float, C.c_float,
+                                               C.c_float, C.c_void_p, C.c_void_p]
         L.lcto_momentum_elem.restype = None
         L.lcto_momentum_elem.argtypes = [C.c_uint16, C.c_uint16, C.c_uint16, C.c_float, C.c_float,
                                          C.POINTER(C.c_uint16), C.POINTER(C.c_uint16)]
@@ -398,6 +401,16 @@ def momentum_dense(w: np.ndarray, m: np.ndarray, g: np.ndarray, mu: float, eta: 
     mo = np.empty_like(m)
     for i in range(w.size):
         wo[i], mo[i] = momentum_elem(int(w[i]), int(m[i]), int(g[i]), mu, eta)
+    return wo, mo
+
+
+def momentum_clip_dense(w: np.ndarray, m: np.ndarray, g: np.ndarray, c: float, mu: float, eta: float):
+    """(w', m') of the momentum step whose gradient is scaled by c, on raw BF16
+    bit patterns."""
+    w, m, g = (np.ascontiguousarray(x, np.uint16).reshape(-1) for x in (w, m, g))
+    assert w.size == m.size == g.size
+    wo, mo = np.empty_like(w), np.empty_like(m)
+    lib().lcto_momentum_clip_dense(_p(w), _p(m), _p(g), w.size, c, mu, eta, _p(wo), _p(mo))
     return wo, mo
 
 

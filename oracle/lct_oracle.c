@@ -668,6 +668,19 @@ void lcto_momentum_elem(uint16_t w, uint16_t m, uint16_t g, float mu, float eta,
     *w_out = lcto_rne_bf16(fmaf(-eta, bf16_to_f32(m2), bf16_to_f32(w)));
 }
 
+/* The momentum step with its gradient scaled by c, on dense values: c * g is
+ * rounded to fp32 before it enters the fused multiply-add.  Serial. */
+void lcto_momentum_clip_dense(const uint16_t *w, const uint16_t *m, const uint16_t *g, uint64_t n, float c,
+                              float mu, float eta, uint16_t *w_out, uint16_t *m_out)
+{
+    for (uint64_t i = 0; i < n; i++) {
+        volatile float cg = c * bf16_to_f32(g[i]);
+        uint16_t m2 = lcto_rne_bf16(fmaf(mu, bf16_to_f32(m[i]), cg));
+        w_out[i] = lcto_rne_bf16(fmaf(-eta, bf16_to_f32(m2), bf16_to_f32(w[i])));
+        m_out[i] = m2;
+    }
+}
+
 /* Encode one block's values and append its spilled bytes to ovf at obase[b]. */
 static void encode_block_out(const lcto_codebook *cb, const uint16_t *x, uint32_t nb, uint32_t cap_words,
                              uint64_t b, uint64_t r0, uint64_t po, uint8_t *spill,

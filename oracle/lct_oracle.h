@@ -169,6 +169,11 @@ int  lcto_sgd(const lcto_codebook *cw, const uint8_t *w_sf, const uint32_t *w_pa
 void lcto_momentum_elem(uint16_t w, uint16_t m, uint16_t g, float mu, float eta,
                         uint16_t *w_out, uint16_t *m_out);
 
+/* The same over n dense values with the gradient scaled by c, c * g rounded
+ * to fp32: m' = rne(fmaf(mu, f32(m), c * f32(g))), w' from m' as above. */
+void lcto_momentum_clip_dense(const uint16_t *w, const uint16_t *m, const uint16_t *g, uint64_t n, float c,
+                              float mu, float eta, uint16_t *w_out, uint16_t *m_out);
+
 /* Naive round trip of one momentum step: decode W (codebook cw) and M (cm)
  * fully, update densely with the dense gradient g, re-encode W' with cw_out
  * and M' with cm_out (cw and cm when NULL).  Inputs and outputs share n,
