@@ -1048,12 +1048,13 @@ __device__ __forceinline__ void load_chunk(uint32_t (&dst)[CH], const T *base, u
 // next step's inputs loaded (load(buf, j0)) while the current one works.  Two
 // buffers alternate, so no value is copied between steps and the waits for a
 // load fall one step after it was issued.  The load for the step past the end
-// re-reads the last step's positions.
+// re-reads the last step's positions.  first (a multiple of CH below npos):
+// where to begin.
 template <typename Buf, typename Load, typename Step>
-__device__ __forceinline__ void double_buffered(uint32_t npos, Load load, Step step) {
+__device__ __forceinline__ void double_buffered(uint32_t first, uint32_t npos, Load load, Step step) {
     Buf a, b;
-    load(a, 0u);
-    for (uint32_t j0 = 0; j0 < npos; j0 += 2 * CH) {
+    load(a, first);
+    for (uint32_t j0 = first; j0 < npos; j0 += 2 * CH) {
         load(b, min(j0 + CH, npos - CH));
         step(a, j0);
         if (j0 + CH >= npos) break;
@@ -1065,11 +1066,11 @@ __device__ __forceinline__ void double_buffered(uint32_t npos, Load load, Step s
 // The same with the loads two chunks ahead (three buffers): a wave's stream
 // waits less on memory when few waves share a compute unit (small tensors).
 template <typename Buf, typename Load, typename Step>
-__device__ __forceinline__ void triple_buffered(uint32_t npos, Load load, Step step) {
+__device__ __forceinline__ void triple_buffered(uint32_t first, uint32_t npos, Load load, Step step) {
     Buf a, b, c;
-    load(a, 0u);
-    load(b, min(CH, npos - CH));
-    for (uint32_t j0 = 0; j0 < npos; j0 += 3 * CH) {
+    load(a, first);
+    load(b, min(first + CH, npos - CH));
+    for (uint32_t j0 = first; j0 < npos; j0 += 3 * CH) {
         load(c, min(j0 + 2 * CH, npos - CH));
         step(a, j0);
         if (j0 + CH >= npos) break;
@@ -1080,6 +1081,14 @@ __device__ __forceinline__ void triple_buffered(uint32_t npos, Load load, Step s
         step(c, j0 + 2 * CH);
     }
 }
+
+// How a block without spilled input fields is walked: its streams all have
+// at least CH * halves() positions, which the full-block path does whatever
+// the block's length, and walk_end() is where the checked path stops (the
+// longest stream's end in whole steps).  A block of a few hundred elements so
+// costs one step, not a full block's.
+__device__ __forceinline__ uint32_t halves(uint32_t nb) { return nb / (NS * CH); }
+__device__ __forceinline__ uint32_t walk_end(uint32_t nb) { return (stream_len(nb, 0) + CH - 1) / CH * CH; }
 
 struct Buf1 {
     uint32_t v[CH];
@@ -1111,7 +1120,7 @@ __device__ __forceinline__ void encode_stream(const EncodeParams &p, Writer &st,
     uint64_t *stage_ctr = reinterpret_cast<uint64_t *>(p.scratch + kScrStage);
     uint8_t *stage = p.scratch + scr_stage_offset(p.nblk);
     triple_buffered<Buf1>(
-        npos, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FULL>(bf.v, xs, j0, n_s); },
+        0u, npos, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FULL>(bf.v, xs, j0, n_s); },
         [&](Buf1 &bf, uint32_t j0) {
             uint32_t e[CH];
             uint8_t *o = sfs + (size_t)j0 * NS;
@@ -1180,19 +1189,18 @@ constexpr uint32_t kDecWaves = 4;
 constexpr uint32_t kDecTab = 256, kDecWave0 = 1280;
 __host__ __device__ constexpr uint32_t dec_wave_bytes(uint32_t cap) { return (cap + 2) * ROWB; }
 
+// Positions first .. end of this lane's stream (multiples of CH).  FAST: no
+// stream ends before, no field is spilled.
 template <bool FAST, uint32_t CAPT>
-__device__ __forceinline__ void decode_stream(const DecodeParams &p, uint32_t row0, uint32_t n_s,
+__device__ __forceinline__ void decode_stream(const DecodeParams &p, Reader &rd, uint32_t row0, uint32_t n_s,
                                               uint32_t c_s, const uint8_t *sfu, uint16_t *yu,
-                                              uint64_t sp0) {
+                                              uint64_t sp0, uint32_t first, uint32_t end) {
     const uint32_t s = lane();
-    const uint32_t npos = p.block_elems / NS;
     const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap_of<CAPT>(p.cap_words) - 2;
     const uint8_t *sfs = sfu + s;
     uint16_t *ys = yu + s;
-    Reader rd;
-    rd.init(row0, s);
     triple_buffered<Buf1>(
-        npos, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FAST>(bf.v, sfs, j0, n_s); },
+        first, end, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FAST>(bf.v, sfs, j0, n_s); },
         [&](Buf1 &bf, uint32_t j0) {
             uint16_t *o = ys + (size_t)j0 * NS;
             uint16_t *o2 = o + (CH / 2) * NS;
@@ -1269,12 +1277,14 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_decode(const DecodeParams p)
     const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
     const uint8_t *sfu = p.sf + sp.sf0 + h * US;
     uint16_t *yu = sp.dense + h * US;
-    if (nb == p.block_elems && ob0 == ob1) {
-        decode_stream<true, CAPT>(p, row0, n_s, n_s, sfu, yu, 0);
-    } else {
-        uint32_t c_s, excl;
-        unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
-        decode_stream<false, CAPT>(p, row0, n_s, c_s, sfu, yu, ob0 + excl);
+    Reader rd;
+    rd.init(row0, l);
+    const uint32_t done = ob0 == ob1 ? CH * halves(nb) : 0u;
+    if (done) decode_stream<true, CAPT>(p, rd, row0, n_s, n_s, sfu, yu, 0, 0, done);
+    if (done < walk_end(nb)) {
+        uint32_t c_s = n_s, excl = 0;
+        if (ob0 != ob1) unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
+        decode_stream<false, CAPT>(p, rd, row0, n_s, c_s, sfu, yu, ob0 + excl, done, walk_end(nb));
     }
 }
 
@@ -1299,51 +1309,84 @@ struct CodeAcc {
     }
 };
 
-template <bool FAST, uint32_t CAPT, bool SQ>
-__device__ __forceinline__ void norm_stream(const CodeNormParams &p, uint32_t row0, uint32_t n_s, uint32_t c_s,
-                                            const uint8_t *sfu, uint64_t sp0, CodeAcc<SQ> &acc) {
-    const uint32_t s = lane();
-    const uint32_t npos = p.block_elems / NS;
-    const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap_of<CAPT>(p.cap_words) - 2;
-    const uint8_t *sfs = sfu + s;
-    Reader rd;
-    rd.init(row0, s);
-    triple_buffered<Buf1>(
-        npos, [&](Buf1 &bf, uint32_t j0) { load_chunk<!FAST>(bf.v, sfs, j0, n_s); },
-        [&](Buf1 &bf, uint32_t j0) {
-            if (FAST) {
-                // four fields per window, as the decoder reads them; a window
-                // that ran out is read again one field at a time
+// Per wave: the decoder's rows, then two regions of sign-fraction bytes, one
+// half (CH positions of the unit's streams) each.
+constexpr uint32_t kNormRegB = CH * US;
+__host__ __device__ constexpr uint32_t norm_wave_bytes(uint32_t cap) { return dec_wave_bytes(cap) + 2 * kNormRegB; }
+
+// Positions [0, CH * nh) of every stream, none of them spilled.  The
+// sign-fraction bytes move by 16-byte loads through the wave's LDS regions (a
+// byte load per position and lane keeps the address unit busy for as long as
+// the arithmetic takes).
+template <uint32_t CAPT, bool SQ>
+__device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t row0, uint32_t slab, uint32_t nh,
+                                            const uint8_t *sfu, CodeAcc<SQ> &acc) {
+    const uint32_t l = lane();
+    const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap - 2;
+    const uint32_t lw = l & ~3u;
+    const uint32_t jsel = (l & 3u) * 0x01010000u | 0x0C0Cu;
+    constexpr uint32_t kNone = 0x80000000u;
+    constexpr uint32_t kHalfB = CH * NS;
+    const uint32_t piece = (l >> 2) * NS + 16 * (l & 3);
+    const __amdgpu_buffer_rsrc_t r = wave_rsrc(sfu, (nh * CH - 1) * NS + US);
+    auto load = [&](uint32_t h) {
+        return __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, h < nh ? h * kHalfB + piece : kNone, 0, 0));
+    };
+    auto region = [&](uint32_t h) { return slab + (h & 1u) * kNormRegB; };
+    st128(region(0) + 16 * l, load(0));
+    u32x4 next = load(1);
+    for (uint32_t h = 0; h < nh; ++h) {
+        uint32_t w[CH];
 #pragma unroll
-                for (uint32_t g = 0; g < CH; g += 4) {
-                    const int32_t q0 = rd.q;
-                    uint32_t e23[4];
-                    const uint32_t c = rd.next_n<4>(kDecTab, qmax, e23);
-                    if (__builtin_expect(!__all(c <= 30), 0)) {
-                        rd.q = q0;
+        for (uint32_t i = 0; i < CH; ++i) w[i] = ld32(region(h) + i * US + lw);
+        st128(region(h + 1) + 16 * l, next);
+        next = load(h + 2);
+        // four fields per window, as the decoder reads them; a window that
+        // ran out is read again one field at a time
 #pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k) {
-                            e23[k] = rd.next(kDecTab);
-                            rd.q = min(rd.q, qmax);
-                        }
-                    }
+        for (uint32_t g = 0; g < CH; g += 4) {
+            const int32_t q0 = rd.q;
+            uint32_t e23[4];
+            const uint32_t c = rd.next_n<4>(kDecTab, qmax, e23);
+            if (__builtin_expect(!__all(c <= 30), 0)) {
+                rd.q = q0;
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) acc.add(join32(bf.v[g + k], e23[k]));
+                for (uint32_t k = 0; k < 4; ++k) {
+                    e23[k] = rd.next(kDecTab);
+                    rd.q = min(rd.q, qmax);
                 }
-                return;
             }
 #pragma unroll
-            for (uint32_t i = 0; i < CH; ++i) {
-                const uint32_t j = j0 + i;
-                uint32_t e23 = rd.next(kDecTab);
-                rd.q = min(rd.q, qmax);
-                if (j >= c_s && j < n_s) {
-                    const uint64_t k = sp0 + (j - c_s);
-                    e23 = (k < p.ovf_cap ? (uint32_t)p.ovf[k] : 0u) << 23;
-                }
-                if (j < n_s) acc.add(join32(bf.v[i], e23));
+            for (uint32_t k = 0; k < 4; ++k) acc.add(join32s(w[g + k], e23[k], jsel));
+        }
+    }
+}
+
+// Positions from j0 on (a multiple of CH) to the longest stream's end, with
+// per-element checks and spilled fields.
+template <bool SQ>
+__device__ __forceinline__ void norm_rest(const CodeNormParams &p, Reader &rd, uint32_t cap, uint32_t row0,
+                                          uint32_t j0, uint32_t nb, uint32_t n_s, uint32_t c_s, const uint8_t *sfu,
+                                          uint64_t sp0, CodeAcc<SQ> &acc) {
+    const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap - 2;
+    const uint32_t end = stream_len(nb, 0);
+    const uint8_t *sfs = sfu + lane();
+    for (; j0 < end; j0 += CH) {
+        Buf1 bf;
+        load_chunk<true>(bf.v, sfs, j0, n_s);
+#pragma unroll
+        for (uint32_t i = 0; i < CH; ++i) {
+            const uint32_t j = j0 + i;
+            uint32_t e23 = rd.next(kDecTab);
+            rd.q = min(rd.q, qmax);
+            if (j >= c_s && j < n_s) {
+                const uint64_t k = sp0 + (j - c_s);
+                e23 = (k < p.ovf_cap ? (uint32_t)p.ovf[k] : 0u) << 23;
             }
-        });
+            if (j < n_s) acc.add(join32(bf.v[i], e23));
+        }
+    }
 }
 
 template <uint32_t CAPT, bool GROUP, bool SQ>
@@ -1354,23 +1397,26 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p)
     __syncthreads();
     const uint32_t l = lane();
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
-    const uint32_t base = kDecWave0 + wave_id() * dec_wave_bytes(cap);
+    const uint32_t base = kDecWave0 + wave_id() * norm_wave_bytes(cap);
     const uint32_t row0 = base + ROWB;
     st32(base + 4 * l, 0);                      // row -1
     st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
     rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
     const BlockSpan sp = GROUP ? group_span(p.grp, k, p.block_elems, b) : flat_span(nullptr, p.n, p.block_elems, b);
     const uint32_t nb = sp.nb;
-    const uint32_t n_s = stream_len(nb, h * US + l);
     const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
     const uint8_t *sfu = p.sf + sp.sf0 + h * US;
     CodeAcc<SQ> acc;
-    if (nb == p.block_elems && ob0 == ob1) {
-        norm_stream<true, CAPT, SQ>(p, row0, n_s, n_s, sfu, 0, acc);
-    } else {
-        uint32_t c_s, excl;
-        unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
-        norm_stream<false, CAPT, SQ>(p, row0, n_s, c_s, sfu, ob0 + excl, acc);
+    Reader rd;
+    rd.init(row0, l);
+    const bool spills = ob0 != ob1;
+    const uint32_t nh = spills ? 0u : halves(nb);
+    if (nh) norm_halves<CAPT, SQ>(rd, cap, row0, base + dec_wave_bytes(cap), nh, sfu, acc);
+    if (nh * CH < walk_end(nb)) {
+        const uint32_t n_s = stream_len(nb, h * US + l);
+        uint32_t c_s = n_s, excl = 0;
+        if (spills) unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
+        norm_rest<SQ>(p, rd, cap, row0, nh * CH, nb, n_s, c_s, sfu, ob0 + excl, acc);
     }
     // the wave's value, then the block's, in a fixed order
     double v = SQ ? acc.s : 0.0;
@@ -1582,14 +1628,15 @@ struct RingReader {
     }
 };
 
-// General path: partial blocks and inputs with spilled fields; byte-wide
-// accesses with per-element checks.
+// General path: inputs with spilled fields, and what the full-block path
+// leaves of a partial block (positions first .. end, the readers at q);
+// byte-wide accesses with per-element checks.
 template <uint32_t CAPT>
 __device__ __forceinline__ void sgd_stream_general(const SgdParams &p, const SgdLayout &lay, PayWriter &st,
                                                    uint32_t n_s, uint32_t cw_s, uint32_t cm_s,
-                                                   uint64_t r0, uint64_t wsp, uint64_t msp, float mul) {
+                                                   uint64_t r0, uint64_t wsp, uint64_t msp, float mul,
+                                                   uint32_t first, uint32_t end, const int32_t *q) {
     const uint32_t s = lane();
-    const uint32_t npos = p.block_elems / NS;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const uint32_t capbits = 32 * cap;
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
@@ -1602,8 +1649,12 @@ __device__ __forceinline__ void sgd_stream_general(const SgdParams &p, const Sgd
     Reader rw, rm;
     rw.init(lay.w0, s);
     rm.init(lay.m0, s);
+    if (first) {
+        rw.q = q[0];
+        rm.q = q[1];
+    }
     double_buffered<Buf2>(
-        npos,
+        first, end,
         [&](Buf2 &bf, uint32_t j0) {
             load_chunk<true>(bf.w, wsf, j0, n_s);
             load_chunk<true>(bf.m, msf, j0, n_s);
@@ -1700,15 +1751,16 @@ struct HalfRegs {
 // RING: M's rows come through a ring (the ring kernel's layout, Lay =
 // RingLayout, its tables from kRingTab); M's sign-fraction bytes then take
 // one region, refilled at the end of each half.  mrows: this unit's row 0 of
-// M's payload (ring only).
+// M's payload (ring only).  nh: halves to do (all of a full block's, or as
+// many as every stream of a partial one has); n_s: this lane's stream's
+// positions; q (may be null): where both readers stopped.
 template <uint32_t CAPT, bool RING, class Lay>
 __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &lay, PayWriter &st,
-                                                uint64_t r0, const uint32_t *mrows, float mul) {
+                                                uint64_t r0, const uint32_t *mrows, float mul, uint32_t nh,
+                                                uint32_t n_s, int32_t *q) {
     constexpr uint32_t TB = RING ? kRingTab : 0u;
     constexpr uint32_t tabE = TB + kSgdETab, tabW = TB + kSgdWTab, tabM = TB + kSgdMTab;
     const uint32_t l = lane();
-    const uint32_t npos = p.block_elems / NS;
-    const uint32_t nh = npos / CH;                // halves (the block size is a multiple of 4096)
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const uint32_t capbits = 32 * cap;
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
@@ -1720,7 +1772,7 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
     // resources spanning them: 32-bit offsets, and an offset past the range
     // makes a load that returns nothing (no traffic) or a store that is
     // dropped.
-    const uint32_t span = (npos - 1) * NS + US;
+    const uint32_t span = (nh * CH - 1) * NS + US;
     const __amdgpu_buffer_rsrc_t rws = wave_rsrc(p.w_sf + r0, span);
     const __amdgpu_buffer_rsrc_t rms = wave_rsrc(p.m_sf + r0, span);
     const __amdgpu_buffer_rsrc_t ros = wave_rsrc(p.o_sf + r0, span);
@@ -1783,7 +1835,7 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
             }
             wc[k] = u32x2{0u, 0u};
         }
-        writer_spill<false>(st, ew8, jw, npos, stage_ctr, stage, p.ovf_cap);
+        writer_spill<false>(st, ew8, jw, n_s, stage_ctr, stage, p.ovf_cap);
     };
 
     // One stage.  DEC: group s exists (decode it).  GS = s % 4; h = s / 4.
@@ -1958,6 +2010,10 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
     code_checked();
     outv = ld128(lay.sw + region(nh - 1) + mine);
     __builtin_amdgcn_raw_buffer_store_b128(outv, ros, (nh - 1) * kHalfB + g, 0, 0);
+    if (q) {
+        q[0] = rw.q;
+        q[1] = rm.q;
+    }
 }
 
 // A block takes the full-block path when it is whole and neither input has
@@ -1978,7 +2034,8 @@ __device__ __forceinline__ bool block_full(const P &p, uint32_t b, uint32_t nb, 
 }
 // The general kernel's walk: f(i) for every i < count taken by this
 // workgroup (i = blockIdx.x, + gridDim.x, ...) whose block is not full;
-// blk(i) names i's block.  Every wave of the workgroup takes the same i in
+// blk(i) names i's block; with p.all, for every i (the general kernel alone
+// does the update).  Every wave of the workgroup takes the same i in
 // the same order.
 template <bool GROUP, class P, class Blk, class F>
 __device__ __forceinline__ void for_general(const P &p, uint32_t count, Blk blk, F f) {
@@ -1988,8 +2045,8 @@ __device__ __forceinline__ void for_general(const P &p, uint32_t count, Blk blk,
         bool gen = false;
         if (i < count) {
             const uint32_t b = blk((uint32_t)i);
-            gen = !block_full(p, b, block_len<GROUP>(p, b), p.w_obase[b], p.w_obase[b + 1], p.m_obase[b],
-                              p.m_obase[b + 1]);
+            gen = p.all || !block_full(p, b, block_len<GROUP>(p, b), p.w_obase[b], p.w_obase[b + 1], p.m_obase[b],
+                                       p.m_obase[b + 1]);
         }
         for (uint64_t mask = __ballot(gen); mask; mask &= mask - 1)
             f((uint32_t)(base + (uint64_t)__builtin_ctzll(mask) * G));
@@ -2075,15 +2132,26 @@ void k_sgd(const SgdParams p) {
         st.init(0, l, n_s);
         st.rows.init(p.o_pay, b, h, cap);
         if (!GEN) {
-            sgd_stream_full<CAPT, false>(p, lay, st, r0 + h * US, nullptr, mul);
+            sgd_stream_full<CAPT, false>(p, lay, st, r0 + h * US, nullptr, mul, halves(p.block_elems), n_s, nullptr);
             ++nfull;
             const UnitOut o{p.o_pay, p.o_cnt, p.scratch, p.nblk, p.ovf_cap, cap, 0, 0};
             unit_finish(st, n_s, u, b, h, 0, o);
         } else {
-            uint32_t cw_s, cm_s, wex, mex;
-            unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
-            unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
-            sgd_stream_general<CAPT>(p, lay, st, n_s, cw_s, cm_s, r0 + h * US, wob + wex, mob + mex, mul);
+            const bool spills = wob != wob1 || mob != mob1;
+            const uint32_t nh = spills ? 0u : halves(nb);
+            int32_t q[2] = {0, 0};
+            if (nh) sgd_stream_full<CAPT, false>(p, lay, st, r0 + h * US, nullptr, mul, nh, n_s, q);
+            if (nh * CH < walk_end(nb)) {
+                uint32_t cw_s = n_s, cm_s = n_s, wex = 0, mex = 0;
+                if (spills) {
+                    unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
+                    unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
+                }
+                sgd_stream_general<CAPT>(p, lay, st, n_s, cw_s, cm_s, r0 + h * US, wob + wex, mob + mex, mul, nh * CH,
+                                         walk_end(nb), q);
+            } else {
+                nfull += nb == p.block_elems;
+            }
             // The result's counts overwrite W's when the update is in place:
             // other units of this block may still read W's, so they are
             // parked and put in place by the placing kernel.  (The
@@ -2095,11 +2163,11 @@ void k_sgd(const SgdParams p) {
     if (!GEN) {
         const uint32_t stride = gridDim.x * kSgdWaves;
         for (uint32_t u = first_unit(kSgdWaves); u < nunits; u += stride) unit(u);
-        if (l == 0 && nfull) atomicAdd(reinterpret_cast<uint32_t *>(p.scratch + kScrFullUnits), nfull);
     } else {
         for_general<GROUP>(p, p.nblk, [](uint32_t i) { return i; },
                            [&](uint32_t b) { unit(kMaxUnits * b + wave_id()); });
     }
+    if (l == 0 && nfull) atomicAdd(reinterpret_cast<uint32_t *>(p.scratch + kScrFullUnits), nfull);
 }
 
 // W's rows (cap) and M's first kRing-1 rows into the ring kernel's LDS with
@@ -2196,7 +2264,8 @@ void k_sgd_ring(const SgdParams p) {
         PayWriter st;
         st.init(0, l, n_s);
         st.rows.init(p.o_pay, b, h, cap);
-        sgd_stream_full<cap, true>(p, lay, st, r0 + h * US, p.m_pay + ((uint64_t)b * cap * NS + h * US), mul);
+        sgd_stream_full<cap, true>(p, lay, st, r0 + h * US, p.m_pay + ((uint64_t)b * cap * NS + h * US), mul,
+                                   halves(p.block_elems), n_s, nullptr);
         ++nfull;
         const UnitOut o{p.o_pay, p.o_cnt, p.scratch, p.nblk, p.ovf_cap, cap, 0, 0};
         unit_finish(st, n_s, b * kMaxUnits + h, b, h, 0, o);
@@ -2247,9 +2316,8 @@ template <uint32_t CAPT, bool CLIP>
 __device__ __forceinline__ void mom_stream_general(const MomParams &p, const SgdLayout &lay, PayWriter &stw,
                                                    PayWriter &stm, uint32_t n_s, uint32_t cw_s, uint32_t cm_s,
                                                    uint64_t r0, const uint16_t *gu, uint64_t wsp, uint64_t msp,
-                                                   float c) {
+                                                   float c, uint32_t first, uint32_t end, const int32_t *q) {
     const uint32_t s = lane();
-    const uint32_t npos = p.block_elems / NS;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const uint32_t capbits = 32 * cap;
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
@@ -2266,11 +2334,15 @@ __device__ __forceinline__ void mom_stream_general(const MomParams &p, const Sgd
     Reader rw, rm;
     rw.init(lay.w0, s);
     rm.init(lay.m0, s);
+    if (first) {
+        rw.q = q[0];
+        rm.q = q[1];
+    }
     struct Buf3 {
         uint32_t w[CH], m[CH], g[CH];
     };
     double_buffered<Buf3>(
-        npos,
+        first, end,
         [&](Buf3 &bf, uint32_t j0) {
             load_chunk<true>(bf.w, wsf, j0, n_s);
             load_chunk<true>(bf.m, msf, j0, n_s);
@@ -2356,10 +2428,9 @@ __device__ __forceinline__ void mom_stream_general(const MomParams &p, const Sgd
 // spilled): the update's pipeline with both products and both writers.
 template <uint32_t CAPT, bool CLIP>
 __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLayout &lay, PayWriter &stw,
-                                                PayWriter &stm, uint64_t r0, const uint16_t *gu, float c) {
+                                                PayWriter &stm, uint64_t r0, const uint16_t *gu, float c,
+                                                uint32_t nh, uint32_t n_s, int32_t *q) {
     const uint32_t l = lane();
-    const uint32_t npos = p.block_elems / NS;
-    const uint32_t nh = npos / CH;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const uint32_t capbits = 32 * cap;
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
@@ -2367,7 +2438,7 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
     const uint32_t mine = 16 * l;
     const uint32_t lw = l & ~3u;
     const uint32_t jsel = (l & 3u) * 0x01010000u | 0x0C0Cu;
-    const uint32_t span = (npos - 1) * NS + US;
+    const uint32_t span = (nh * CH - 1) * NS + US;
     const __amdgpu_buffer_rsrc_t rws = wave_rsrc(p.w_sf + r0, span);
     const __amdgpu_buffer_rsrc_t rms = wave_rsrc(p.m_sf + r0, span);
     const __amdgpu_buffer_rsrc_t rows_ = wave_rsrc(p.ow_sf + r0, span);
@@ -2430,7 +2501,7 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
             }
             wc[k] = u32x2{0u, 0u};
         }
-        writer_spill<false>(st, e8, jw, npos, ctr, stg, stg_cap);
+        writer_spill<false>(st, e8, jw, n_s, ctr, stg, stg_cap);
     };
     auto code_checked = [&]() {
         checked(stw, wcw, ew8, wctr, wstage, p.ow_ovf_cap);
@@ -2611,6 +2682,10 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
     outm = ld128(lay.sm + region(nh - 1) + mine);
     __builtin_amdgcn_raw_buffer_store_b128(outw, rows_, (nh - 1) * kHalfB + piece, 0, 0);
     __builtin_amdgcn_raw_buffer_store_b128(outm, roms, (nh - 1) * kHalfB + piece, 0, 0);
+    if (q) {
+        q[0] = rw.q;
+        q[1] = rm.q;
+    }
 }
 
 // GEN: the general kernel (blocks that are not full), as for the update.
@@ -2682,14 +2757,24 @@ void k_mom(const MomParams p) {
         stm.init(0, l, n_s);
         stm.rows.init(p.om_pay, b, h, cap);
         if (!GEN) {
-            mom_stream_full<CAPT, CLIP>(p, lay, stw, stm, r0 + h * US, gu, c);
+            mom_stream_full<CAPT, CLIP>(p, lay, stw, stm, r0 + h * US, gu, c, halves(p.block_elems), n_s, nullptr);
             ++nfull;
         } else {
-            uint32_t cw_s, cm_s, wex, mex;
-            unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
-            unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
-            mom_stream_general<CAPT, CLIP>(p, lay, stw, stm, n_s, cw_s, cm_s, r0 + h * US, gu, wob + wex, mob + mex,
-                                           c);
+            const bool spills = wob != wob1 || mob != mob1;
+            const uint32_t nh = spills ? 0u : halves(nb);
+            int32_t q[2] = {0, 0};
+            if (nh) mom_stream_full<CAPT, CLIP>(p, lay, stw, stm, r0 + h * US, gu, c, nh, n_s, q);
+            if (nh * CH < walk_end(nb)) {
+                uint32_t cw_s = n_s, cm_s = n_s, wex = 0, mex = 0;
+                if (spills) {
+                    unit_spills(p.w_cnt + (uint64_t)b * NS, nb, h, cw_s, wex);
+                    unit_spills(p.m_cnt + (uint64_t)b * NS, nb, h, cm_s, mex);
+                }
+                mom_stream_general<CAPT, CLIP>(p, lay, stw, stm, n_s, cw_s, cm_s, r0 + h * US, gu, wob + wex,
+                                               mob + mex, c, nh * CH, walk_end(nb), q);
+            } else {
+                nfull += nb == p.block_elems;
+            }
         }
         // in place, the general kernel parks the counts (other units of the
         // block still read the inputs'); the full-block kernel reads none
@@ -2702,12 +2787,12 @@ void k_mom(const MomParams p) {
     };
     if (!GEN) {
         for (uint32_t b = blockIdx.x; b < p.nblk; b += gridDim.x) block(b);
-        if (l == 0 && nfull) {
-            atomicAdd(reinterpret_cast<uint32_t *>(p.ow_scratch + kScrFullUnits), nfull);
-            atomicAdd(reinterpret_cast<uint32_t *>(p.om_scratch + kScrFullUnits), nfull);
-        }
     } else {
         for_general<GROUP>(p, p.nblk, [](uint32_t i) { return i; }, block);
+    }
+    if (l == 0 && nfull) {
+        atomicAdd(reinterpret_cast<uint32_t *>(p.ow_scratch + kScrFullUnits), nfull);
+        atomicAdd(reinterpret_cast<uint32_t *>(p.om_scratch + kScrFullUnits), nfull);
     }
 }
 
@@ -2754,36 +2839,67 @@ std::atomic<size_t> g_lds_granted[8][4];
 
 int cap_slot(uint32_t cap) { return cap == 25 ? 0 : cap == 12 ? 1 : cap == 11 ? 2 : 3; }
 
+// Workgroups of a kernel that the current device holds at once.
+int resident_groups(const void *fn, uint32_t waves, size_t lds_bytes, std::atomic<size_t> &granted, uint64_t *out) {
+    const int attr = ensure_lds(fn, lds_bytes, granted);
+    if (attr != hipSuccess) return attr;
+    int dev = 0, cus = 0, per_cu = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e == hipSuccess) e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, (int)(64 * waves), lds_bytes);
+    if (e != hipSuccess) return (int)e;
+    if (per_cu < 1) return (int)hipErrorInvalidConfiguration;
+    *out = (uint64_t)per_cu * cus;
+    return hipSuccess;
+}
+
 // One wave per unit, or (persistent) as many workgroups as the device holds
 // at once, never more than there are units to go round.
 template <typename P>
 int launch(const void *fn, uint64_t nunits, uint32_t waves, bool persistent, size_t lds_bytes,
            const P &p, void *stream, std::atomic<size_t> &granted) {
-    const int attr = ensure_lds(fn, lds_bytes, granted);
-    if (attr != hipSuccess) return attr;
     const uint64_t want = (nunits + waves - 1) / waves;
     uint32_t grid = (uint32_t)want;
-    hipError_t e = hipSuccess;
     if (persistent) {
-        int dev = 0, cus = 0, per_cu = 0;
-        e = hipGetDevice(&dev);
-        if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e == hipSuccess)
-            e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, (int)(64 * waves), lds_bytes);
-        if (e != hipSuccess) return (int)e;
-        if (per_cu < 1) return (int)hipErrorInvalidConfiguration;
-        grid = (uint32_t)std::min<uint64_t>(want, (uint64_t)per_cu * cus);
+        uint64_t held = 0;
+        const int e = resident_groups(fn, waves, lds_bytes, granted, &held);
+        if (e != hipSuccess) return e;
+        grid = (uint32_t)std::min<uint64_t>(want, held);
+    } else {
+        const int attr = ensure_lds(fn, lds_bytes, granted);
+        if (attr != hipSuccess) return attr;
     }
     void *args[] = {const_cast<P *>(&p)};
-    e = hipLaunchKernel(fn, dim3(grid), dim3(64 * waves), args, lds_bytes, (hipStream_t)stream);
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(64 * waves), args, lds_bytes, (hipStream_t)stream);
     if (e != hipSuccess) return (int)e;
     return (int)hipGetLastError();
+}
+
+// The two launches of an update: the kernel of the full blocks, then the
+// general one (p.all 0), or the general one for every block (p.all 1) where
+// each block gets a workgroup of its own at once.  Then the two would only
+// follow each other: a block takes the full-block path in either.
+template <typename P>
+int launch_update(P p, const void *full, uint32_t full_waves, size_t full_lds, std::atomic<size_t> &full_granted,
+                  const void *gen, uint32_t gen_waves, size_t gen_lds, std::atomic<size_t> &gen_granted,
+                  void *stream) {
+    const uint64_t nunits = (uint64_t)p.nblk * kMaxUnits;
+    uint64_t held = 0;
+    int e = resident_groups(gen, gen_waves, gen_lds, gen_granted, &held);
+    if (e != hipSuccess) return e;
+    p.all = p.nblk <= held;
+    if (!p.all) {
+        e = launch(full, nunits, full_waves, true, full_lds, p, stream, full_granted);
+        if (e != hipSuccess) return e;
+    }
+    return launch(gen, nunits, gen_waves, true, gen_lds, p, stream, gen_granted);
 }
 
 }  // namespace
 
 size_t encode_lds(uint32_t cap) { return kEncWave0 + (size_t)kEncWaves * enc_wave_bytes(cap); }
 size_t decode_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * dec_wave_bytes(cap); }
+size_t norm_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * norm_wave_bytes(cap); }
 size_t sgd_lds(uint32_t cap, uint32_t waves) { return kSgdWave0 + (size_t)waves * sgd_wave_bytes(cap); }
 
 int launch_clear(uint8_t *scratch, uint64_t nblk, uint32_t *status, void *stream) {
@@ -2825,23 +2941,18 @@ template <uint32_t C> struct MomGXCK { static const void *fn() { return reinterp
 // flat, group, and their general kernels; then the clipped steps'
 std::atomic<size_t> g_mom_lds_granted[8][4];
 
-// The full-block kernel, then the general one (which ends at once when every
-// block is full).
 int launch_mom(const MomParams &p, void *stream, bool group) {
     const size_t lds = kMWave0 + (size_t)kMomWaves * sgd_wave_bytes(p.cap_words);
-    const int slot = cap_slot(p.cap_words);
-    // persistent: one workgroup is one block at a time
     const uint32_t cap = p.cap_words;
     const bool clip = p.coef != nullptr;
-    const void *fn = clip ? (group ? ByCap<MomGCK>::pick(cap) : ByCap<MomCK>::pick(cap))
-                          : (group ? ByCap<MomGK>::pick(cap) : ByCap<MomK>::pick(cap));
-    const int base = (clip ? 4 : 0) + (group ? 1 : 0);
-    int e = launch(fn, (uint64_t)p.nblk * kMomWaves, kMomWaves, true, lds, p, stream, g_mom_lds_granted[base][slot]);
-    if (e != hipSuccess) return e;
-    fn = clip ? (group ? ByCap<MomGXCK>::pick(cap) : ByCap<MomXCK>::pick(cap))
-              : (group ? ByCap<MomGXK>::pick(cap) : ByCap<MomXK>::pick(cap));
-    return launch(fn, (uint64_t)p.nblk * kMomWaves, kMomWaves, true, lds, p, stream,
-                  g_mom_lds_granted[base + 2][slot]);
+    const void *full = clip ? (group ? ByCap<MomGCK>::pick(cap) : ByCap<MomCK>::pick(cap))
+                            : (group ? ByCap<MomGK>::pick(cap) : ByCap<MomK>::pick(cap));
+    const void *gen = clip ? (group ? ByCap<MomGXCK>::pick(cap) : ByCap<MomXCK>::pick(cap))
+                           : (group ? ByCap<MomGXK>::pick(cap) : ByCap<MomXK>::pick(cap));
+    std::atomic<size_t>(&granted)[4] = g_mom_lds_granted[(clip ? 4 : 0) + (group ? 1 : 0)];
+    std::atomic<size_t>(&gen_granted)[4] = g_mom_lds_granted[(clip ? 4 : 0) + (group ? 3 : 2)];
+    const int slot = cap_slot(cap);
+    return launch_update(p, full, kMomWaves, lds, granted[slot], gen, kMomWaves, lds, gen_granted[slot], stream);
 }
 
 int launch_decode(const DecodeParams &p, void *stream, bool group) {
@@ -2861,33 +2972,23 @@ int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *st
     const uint32_t cap = p.cap_words;
     const void *fn = squares ? (group ? ByCap<NormGK>::pick(cap) : ByCap<NormK>::pick(cap))
                              : (group ? ByCap<MaxGK>::pick(cap) : ByCap<MaxK>::pick(cap));
-    return launch(fn, (uint64_t)p.nblk * kMaxUnits, kDecWaves, false, decode_lds(cap), p, stream,
+    return launch(fn, (uint64_t)p.nblk * kMaxUnits, kDecWaves, false, norm_lds(cap), p, stream,
                   g_norm_lds_granted[(squares ? 0 : 2) + (group ? 1 : 0)][cap_slot(cap)]);
 }
 
 std::atomic<size_t> g_ring_granted[2];
 
-// The full-block kernel (the ring kernel at the CLEAN capacity), then the
-// general one (which ends at once when every block is full).
+// The full-block kernel is the ring kernel at the CLEAN capacity.
 int launch_sgd(const SgdParams &p, void *stream, bool group) {
     const int slot = cap_slot(p.cap_words);
-    int e;
-    if (p.cap_words == kRingCap) {
-        const void *fn = group ? reinterpret_cast<const void *>(&k_sgd_ring<true>)
-                               : reinterpret_cast<const void *>(&k_sgd_ring<false>);
-        e = launch(fn, (uint64_t)p.nblk * kRingWaves, kRingWaves, true, kRingLds, p, stream,
-                   g_ring_granted[group ? 1 : 0]);
-    } else {
-        const void *fn = group ? ByCap<SgdGK>::pick(p.cap_words) : ByCap<SgdK>::pick(p.cap_words);
-        e = launch(fn, (uint64_t)p.nblk * kMaxUnits, kSgdWaves, true, sgd_lds(p.cap_words, kSgdWaves), p, stream,
-                   g_lds_granted[group ? 5 : 2][slot]);
-    }
-    if (e != hipSuccess) return e;
-    const void *fn;
-    fn = group ? ByCap<SgdGXK>::pick(p.cap_words) : ByCap<SgdXK>::pick(p.cap_words);
-    return launch(fn, (uint64_t)p.nblk * kMaxUnits, kSgdGenWaves, true, sgd_lds(p.cap_words, kSgdGenWaves), p,
-                  stream,
-                  g_lds_granted[group ? 7 : 6][slot]);
+    const bool ring = p.cap_words == kRingCap;
+    const void *full = ring ? (group ? reinterpret_cast<const void *>(&k_sgd_ring<true>)
+                                     : reinterpret_cast<const void *>(&k_sgd_ring<false>))
+                            : (group ? ByCap<SgdGK>::pick(p.cap_words) : ByCap<SgdK>::pick(p.cap_words));
+    const void *gen = group ? ByCap<SgdGXK>::pick(p.cap_words) : ByCap<SgdXK>::pick(p.cap_words);
+    return launch_update(p, full, ring ? kRingWaves : kSgdWaves, ring ? kRingLds : sgd_lds(p.cap_words, kSgdWaves),
+                         ring ? g_ring_granted[group ? 1 : 0] : g_lds_granted[group ? 5 : 2][slot], gen, kSgdGenWaves,
+                         sgd_lds(p.cap_words, kSgdGenWaves), g_lds_granted[group ? 7 : 6][slot], stream);
 }
 
 

@@ -171,6 +171,7 @@ struct SgdParams {
     float mul;           // the product's factor: -eta, for W - eta*M
     const float *coef;   // a device factor of mul (null: 1)
     uint32_t park_cnt;   // the result's counts overwrite W's: park them in scratch
+    uint32_t all;        // the general kernel does every block
     GroupRef gw, gm;     // used by the group kernels only (W's codes for W and W';
                          // M's for M)
     EncTab wenc;
@@ -217,7 +218,7 @@ struct MomParams {
     uint32_t block_elems, cap_words, nblk;
     float mu, neg_eta;
     uint32_t park_w, park_m;   // an output's counts overwrite its input's: park them
-    uint32_t pad0;
+    uint32_t all;              // the general kernel does every block
     const float *coef;         // clip kernels only: a device factor of g
     GroupRef gw, gm, gg;       // group kernels: W's and M's codes, the gradients' buffers
     uint32_t wenc[256], menc[256];   // packed: bits | len << 24 (W' and M')
