@@ -176,8 +176,9 @@ def _check(rc: int, what: str):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    if stream is None:   # the current stream's handle (a Stream object costs 2.5 us to make)
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return C.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t):
@@ -598,19 +599,29 @@ def lct_momentum_step_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all:
 _LIST_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 
 
-def _current(dev: torch.device, what: str) -> None:
-    """The library works on the current device: a buffer elsewhere is refused
-    here, since a kernel that reads it could fault."""
-    if dev.type != "cuda":
-        raise ValueError("%s must be on the GPU" % what)
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, dev, torch.cuda.current_device()))
+def _current(dev, what: str) -> None:
+    """The library works on the current device: a buffer elsewhere (dev: its
+    device, or its GPU's index) is refused here, since a kernel that reads it
+    could fault."""
+    if isinstance(dev, torch.device):
+        if dev.type != "cuda":
+            raise ValueError("%s must be on the GPU" % what)
+        dev = dev.index
+    if dev != torch.cuda.current_device():
+        raise ValueError("%s is on cuda:%s, the current device is cuda:%d" % (what, dev, torch.cuda.current_device()))
+
+
+def _norm_scratch(count: int, nblk: int) -> int:
+    need = C.c_uint64(0)
+    _check(lib.lct_norm_scratch(count, nblk, C.byref(need)), "lct_norm_scratch")
+    return int(need.value)
 
 
 class LctList:
     """Dense tensors (BF16, FP16 or FP32, contiguous, on one GPU) for
-    ``lct_list_norm`` and ``lct_list_clip``.  Keeps the tensors; makes host
-    arrays only, so a new list for tensors that moved costs no device work."""
+    ``lct_list_norm`` and ``lct_list_clip``.  Keeps the tensors and the
+    addresses they have now; makes host arrays only, so a new list for tensors
+    that moved costs no device work."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -636,6 +647,9 @@ class LctList:
         self.count = count
         self.c = _List(count, C.cast(self.ns, C.c_void_p), C.cast(self.ptrs, C.c_void_p),
                        C.cast(self.types, C.c_void_p))
+        self.ref = C.byref(self.c)
+        self.dev = None if self.device is None else self.device.index
+        self.need = _norm_scratch(count, 0)      # scratch bytes of its norm
 
     def __len__(self):
         return self.count
@@ -645,35 +659,45 @@ class LctNorm:
     """A norm's result on the device, and the working memory of the call.
 
     ``sum`` (float64), ``norm`` and ``coef`` (float32) are 0-d views of one
-    buffer; ``each`` holds every tensor's norm, or is None."""
+    buffer; ``each`` holds every tensor's norm, or is None.  ``scratch`` may be
+    replaced; it is checked when it is set and its size at every call."""
 
     def __init__(self, members: int, nblk: int, each: bool, device, scratch=None):
-        need = C.c_uint64(0)
-        _check(lib.lct_norm_scratch(members, nblk, C.byref(need)), "lct_norm_scratch")
         dev = torch.device(device)
         if scratch is None:
-            scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        self.scratch = scratch
+            scratch = torch.empty(_norm_scratch(members, nblk), dtype=torch.uint8, device=dev)
         self.buf = torch.zeros(16, dtype=torch.uint8, device=dev)
         self.sum = self.buf[0:8].view(torch.float64)[0]
         self.norm = self.buf[8:12].view(torch.float32)[0]
         self.coef = self.buf[12:16].view(torch.float32)[0]
         self.each = torch.zeros(members, dtype=torch.float32, device=dev) if each else None
+        self.members = members
+        self.dev = self.buf.device.index
+        self.buf_ptr = self.buf.data_ptr()
+        self.each_ptr = self.each.data_ptr() if each else None
+        self.scratch = scratch
 
-    def _args(self, members: int, nblk: int | None = None):
-        """(scratch, each) for a call on so many tensors: a list, or with nblk
-        a compressed tensor or group."""
-        need = C.c_uint64(0)
-        _check(lib.lct_norm_scratch(members if nblk is None else 0, nblk or 0, C.byref(need)), "lct_norm_scratch")
-        for name, b, bytes_ in (("scratch", self.scratch, need.value), ("buf", self.buf, 16)):
-            _current(b.device, name)
-            if not b.is_contiguous() or b.numel() * b.element_size() < bytes_:
-                raise ValueError("%s must be contiguous and hold %d bytes" % (name, bytes_))
-        if self.each is not None:
-            _current(self.each.device, "each")
-            if self.each.dtype != torch.float32 or not self.each.is_contiguous() or self.each.numel() != members:
-                raise ValueError("each must be a contiguous float32 tensor of %d elements" % members)
-        return _ptr(self.scratch), _ptr(self.each)
+    @property
+    def scratch(self):
+        return self._scratch
+
+    @scratch.setter
+    def scratch(self, t):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("scratch must be a contiguous tensor on the GPU")
+        if t.device.index != self.dev:
+            raise ValueError("scratch is on %s, the result on cuda:%s" % (t.device, self.dev))
+        self._scratch = t
+        self.scratch_ptr = t.data_ptr()
+        self.scratch_bytes = t.numel() * t.element_size()
+
+    def _check(self, members: int, need: int) -> None:
+        """Fit for a norm of so many tensors that needs so much scratch."""
+        _current(self.dev, "the result")
+        if self.scratch_bytes < need:
+            raise ValueError("scratch holds %d bytes; the norm needs %d" % (self.scratch_bytes, need))
+        if self.each is not None and self.members != members:
+            raise ValueError("each has room for %d norms, the set has %d tensors" % (self.members, members))
 
 
 def alloc_norm(members: int = 0, each: bool = False, nblk: int = 0, device="cuda", scratch=None) -> LctNorm:
@@ -687,11 +711,11 @@ def lct_list_norm(x: LctList, out: LctNorm, max_norm: float = float("inf"), scal
                   kind: int = NORM_L2, stream=None) -> None:
     """Norm of the list's tensors (times scale), each tensor's where out has
     room for them, and the coefficient that clips to max_norm."""
-    if x.device is not None:
-        _current(x.device, "the list")
-    scr, each = out._args(x.count)
-    _check(lib.lct_list_norm(C.byref(x.c), kind, max_norm, scale, scr, each, _ptr(out.buf), _stream(stream)),
-           "lct_list_norm")
+    if x.dev is not None:
+        _current(x.dev, "the list")
+    out._check(x.count, x.need)
+    _check(lib.lct_list_norm(x.ref, kind, max_norm, scale, out.scratch_ptr, out.each_ptr, out.buf_ptr,
+                             _stream(stream)), "lct_list_norm")
 
 
 def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
@@ -701,8 +725,8 @@ def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = 
     _current(t.sf.device, "the tensor")
     if out.each is not None:
         raise ValueError("each is for lists and groups")
-    scr, _ = out._args(1, t.sizes.nblk)
-    _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, scr, _ptr(out.buf),
+    out._check(1, _norm_scratch(0, t.sizes.nblk))
+    _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, out.scratch_ptr, out.buf_ptr,
                                _stream(stream)), "lct_tensor_norm")
 
 
@@ -711,9 +735,9 @@ def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float =
     """Norm of a compressed group and of each member where out has room."""
     a = all_.c(need_scratch=False)
     _current(all_.sf.device, "the group")
-    scr, each = out._args(g.count, all_.sizes.nblk)
-    _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, scr, each, _ptr(out.buf),
-                              _stream(stream)), "lct_group_norm")
+    out._check(g.count, _norm_scratch(0, all_.sizes.nblk))
+    _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, out.scratch_ptr, out.each_ptr,
+                              out.buf_ptr, _stream(stream)), "lct_group_norm")
 
 
 def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0, kind: int = NORM_L2,
@@ -744,10 +768,11 @@ def lct_list_clip(x: LctList, coef, y: LctList | None = None, stream=None) -> No
     """y_k = coef * x_k (in place without y), rounded to y_k's type."""
     y = x if y is None else y
     coef = _coef(coef)
-    for li in (x, y):
-        if li.device is not None:
-            _current(li.device, "the list")
-    _check(lib.lct_list_clip(C.byref(x.c), _ptr(coef), C.byref(y.c), _stream(stream)), "lct_list_clip")
+    if x.dev is not None:
+        _current(x.dev, "the list")
+    if y.dev is not None:
+        _current(y.dev, "the output list")
+    _check(lib.lct_list_clip(x.ref, coef.data_ptr(), y.ref, _stream(stream)), "lct_list_clip")
 
 
 def lct_sgd_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m: LctTensor, eta: float, coef,

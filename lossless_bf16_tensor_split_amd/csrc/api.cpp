@@ -413,6 +413,81 @@ lct_status norm_join(const double *part, uint64_t count, uint64_t stride, bool s
     return e == hipSuccess ? LCT_OK : hip_fail(e, "norm join launch");
 }
 
+// Tensors [k0, k0 + count) of a list, in chunks of `chunk` elements.
+template <uint32_t N>
+void list_args(ListArgs<N> &a, const lct_list &x, uint32_t k0, uint32_t count, uint32_t chunk) {
+    uint64_t c = 0;
+    for (uint32_t j = 0; j < count; ++j) {
+        a.x[j] = x.d_x[k0 + j];
+        a.n[j] = x.n[k0 + j] | ((uint64_t)x.type[k0 + j] << kListTypeShift);
+        a.chunk0[j] = (uint32_t)c;
+        c += (x.n[k0 + j] + chunk - 1) / chunk;
+    }
+    a.count = count;
+    a.chunks = a.chunk0[count] = (uint32_t)c;
+}
+
+template <uint32_t N>
+lct_status list_one(const lct_list &x, bool squares, NormArgs args, float *each, lct_norm_t *out, void *stream) {
+    ListOneParams<N> p;
+    memset(&p, 0, sizeof p);
+    p.each = each;
+    p.out = out;
+    p.args = args;
+    list_args(p.list, x, 0, x.count, kOneChunk);
+    const int e = launch_list_one(p, squares, stream);
+    return e == hipSuccess ? LCT_OK : hip_fail(e, "list norm launch");
+}
+
+// One launch for tensors [k0, k0 + count); *grid gets its workgroups and q
+// the list's cut.
+template <uint32_t N>
+int list_part(const lct_list &x, uint32_t k0, uint32_t count, bool squares, double *run, double *piece,
+              ListFinishParams &q, void *stream) {
+    ListNormParams<N> p;
+    memset(&p, 0, sizeof p);
+    list_args(p.list, x, k0, count, kListChunk);
+    p.run = run;
+    p.piece = piece;
+    q.count = count;
+    q.chunks = p.list.chunks;
+    q.G = std::min(kListGrid, p.list.chunks);
+    memcpy(q.chunk0, p.list.chunk0, sizeof p.list.chunk0);
+    return q.G ? launch_list_norm(p, q.G, squares, stream) : (int)hipSuccess;
+}
+
+lct_status list_norm(const lct_list &x, bool squares, NormArgs args, double *run, float *each, lct_norm_t *out,
+                     void *stream) {
+    uint64_t ones = 0;   // chunks of the one-launch form
+    for (uint32_t k = 0; k < x.count && ones <= kOneMax; ++k) ones += (x.n[k] + kOneChunk - 1) / kOneChunk;
+    if (x.count <= kListMax && ones <= kOneMax)
+        return x.count <= kListFew ? list_one<kListFew>(x, squares, args, each, out, stream)
+                                   : list_one<kListMax>(x, squares, args, each, out, stream);
+    ListFinishParams q;
+    memset(&q, 0, sizeof q);
+    q.args = args;
+    q.squares = squares;
+    q.run = run;
+    double *piece = run + list_launches(x.count) * kListGrid;
+    for (uint32_t k0 = 0; k0 < x.count; k0 += kListMax) {
+        const uint32_t count = std::min(kListMax, x.count - k0);
+        double *pc = each ? piece : nullptr;
+        int e = count <= kListFew ? list_part<kListFew>(x, k0, count, squares, run + q.runs, pc, q, stream)
+                                  : list_part<kListMax>(x, k0, count, squares, run + q.runs, pc, q, stream);
+        if (e != hipSuccess) return hip_fail(e, "list norm launch");
+        q.runs += q.G;
+        q.piece = piece;
+        q.each = each ? each + k0 : nullptr;
+        q.out = k0 + count == x.count ? out : nullptr;
+        if (q.each || q.out) {
+            e = launch_list_finish(q, stream);
+            if (e != hipSuccess) return hip_fail(e, "list norm launch");
+        }
+        piece += kListGrid + kListMax;
+    }
+    return LCT_OK;
+}
+
 // The norm of a compressed tensor, or (g set) of a group's storage; p's
 // tables are set.
 lct_status code_norm(CodeNormParams &p, const lct_tensor &t, uint64_t nb, const lct_group *g, int32_t kind,
@@ -451,6 +526,20 @@ lct_status code_norm(CodeNormParams &p, const lct_tensor &t, uint64_t nb, const 
         if (e != hipSuccess) return hip_fail(e, "group norms launch");
     }
     return norm_join(part, nb, 1, squares, {max_norm, scale}, part + nb, out, stream);
+}
+
+// One launch of the clip for tensors [k0, k0 + count).
+template <uint32_t N>
+int clip_part(const lct_list &x, const lct_list &y, uint32_t k0, uint32_t count, const float *coef, void *stream) {
+    ListClipParams<N> p;
+    memset(&p, 0, sizeof p);
+    list_args(p.list, x, k0, count, kListChunk);
+    for (uint32_t j = 0; j < count; ++j) {
+        p.list.n[j] |= (uint64_t)(y.type[k0 + j] << 2) << kListTypeShift;
+        p.y[j] = y.d_x[k0 + j];
+    }
+    p.coef = coef;
+    return p.list.chunks ? launch_list_clip(p, stream) : (int)hipSuccess;
 }
 
 // The clip's aliasing rules.  Every range sorted by its start; an overlap of
@@ -1127,47 +1216,8 @@ lct_status lct_list_norm(const lct_list *x, int32_t kind, double max_norm, doubl
             if (overlap(member(*x, k), r)) return LCT_EALIAS;
     st = check_arch();
     if (st != LCT_OK) return st;
-    const bool squares = kind == LCT_NORM_L2;
-    double *run = static_cast<double *>(d_scratch);
-    double *piece = run + list_launches(x->count) * kListGrid;
-    uint64_t runs = 0;
-    ListNormParams p;
-    ListEachParams q;
-    memset(&p, 0, sizeof p);
-    memset(&q, 0, sizeof q);
-    q.args = {max_norm, scale};
-    q.squares = squares;
-    for (uint32_t k0 = 0; k0 < x->count; k0 += kListMax) {
-        p.count = std::min(kListMax, x->count - k0);
-        uint64_t c = 0;
-        for (uint32_t j = 0; j < p.count; ++j) {
-            p.x[j] = x->d_x[k0 + j];
-            p.n[j] = x->n[k0 + j] | ((uint64_t)x->type[k0 + j] << kListTypeShift);
-            p.chunk0[j] = (uint32_t)c;
-            c += (x->n[k0 + j] + kListChunk - 1) / kListChunk;
-        }
-        p.chunks = p.chunk0[p.count] = (uint32_t)c;
-        const uint32_t grid = std::min(kListGrid, p.chunks);
-        p.run = run + runs;
-        p.piece = d_each ? piece : nullptr;
-        if (grid) {
-            const int e = launch_list_norm(p, grid, squares, stream);
-            if (e != hipSuccess) return hip_fail(e, "list norm launch");
-        }
-        if (d_each) {
-            q.piece = piece;
-            q.each = d_each + k0;
-            q.count = p.count;
-            q.chunks = p.chunks;
-            q.G = grid;
-            memcpy(q.chunk0, p.chunk0, sizeof q.chunk0);
-            const int e = launch_list_each(q, stream);
-            if (e != hipSuccess) return hip_fail(e, "list norm launch");
-        }
-        runs += grid;
-        piece += kListGrid + kListMax;
-    }
-    return norm_join(run, runs, 1, squares, {max_norm, scale}, nullptr, d_out, stream);
+    return list_norm(*x, kind == LCT_NORM_L2, {max_norm, scale}, static_cast<double *>(d_scratch), d_each, d_out,
+                     stream);
 }
 
 lct_status lct_tensor_norm(const lct_codebook *cb, const lct_tensor *t, int32_t kind, double max_norm,
@@ -1220,22 +1270,10 @@ lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list 
     if (st != LCT_OK) return st;
     st = check_arch();
     if (st != LCT_OK) return st;
-    ListClipParams p;
-    memset(&p, 0, sizeof p);
-    p.coef = d_coef;
     for (uint32_t k0 = 0; k0 < x->count; k0 += kClipMax) {
-        p.count = std::min(kClipMax, x->count - k0);
-        uint64_t c = 0;
-        for (uint32_t j = 0; j < p.count; ++j) {
-            p.x[j] = x->d_x[k0 + j];
-            p.y[j] = y->d_x[k0 + j];
-            p.n[j] = x->n[k0 + j] | ((uint64_t)(x->type[k0 + j] | (y->type[k0 + j] << 2)) << kListTypeShift);
-            p.chunk0[j] = (uint32_t)c;
-            c += (x->n[k0 + j] + kListChunk - 1) / kListChunk;
-        }
-        p.chunks = p.chunk0[p.count] = (uint32_t)c;
-        if (p.chunks == 0) continue;
-        const int e = launch_list_clip(p, std::min(kListGrid, p.chunks), stream);
+        const uint32_t count = std::min(kClipMax, x->count - k0);
+        const int e = count <= kListFew ? clip_part<kListFew>(*x, *y, k0, count, d_coef, stream)
+                                        : clip_part<kClipMax>(*x, *y, k0, count, d_coef, stream);
         if (e != hipSuccess) return hip_fail(e, "clip launch");
     }
     return LCT_OK;

@@ -266,22 +266,44 @@ struct NormArgs {
 constexpr uint32_t kNormThreads = 256;
 constexpr uint32_t kListChunk = 16384;
 constexpr uint32_t kListMax = 192;        // tensors per launch of the norm
+constexpr uint32_t kListFew = 16;         // short lists take kernels with shorter arguments
 constexpr uint32_t kClipMax = 128;        // and of the clip
 constexpr uint32_t kListGrid = 2048;      // workgroups per launch at most: eight per CU
 constexpr uint32_t kListTypeShift = 48;
 constexpr uint64_t kListElems = (1ull << kListTypeShift) - 1;
 constexpr uint64_t kListMaxElems = 1ull << 44;   // of a whole list: chunk numbers stay within 32 bits
+// Short lists in one launch: a workgroup of kOneThreads does every chunk of
+// kOneChunk elements, a wave each.
+constexpr uint32_t kOneThreads = 1024;
+constexpr uint32_t kOneChunk = 2048;
+constexpr uint32_t kOneMax = 64;          // chunks
+template <uint32_t N>
+struct ListArgs {
+    uint32_t count, chunks;
+    const void *x[N];
+    uint64_t n[N];
+    uint32_t chunk0[N + 1];
+};
+template <uint32_t N>
 struct ListNormParams {
     double *run;          // a value per workgroup
     double *piece;        // a value per workgroup and tensor that meet (null: not wanted)
-    uint32_t count, chunks;
-    const void *x[kListMax];
-    uint64_t n[kListMax];
-    uint32_t chunk0[kListMax + 1];
+    ListArgs<N> list;
 };
-struct ListEachParams {
-    const double *piece;
-    float *each;
+template <uint32_t N>
+struct ListOneParams {
+    float *each;          // null: not wanted
+    lct_norm_t *out;
+    NormArgs args;
+    ListArgs<N> list;
+};
+// What follows a launch of the norm: the tensors' own norms (each) and, after
+// the last, the result of `runs` workgroups' values (out).
+struct ListFinishParams {
+    const double *piece, *run;
+    float *each;          // null: not wanted
+    lct_norm_t *out;      // null: not yet
+    uint64_t runs;
     NormArgs args;
     uint32_t count, chunks, G;   // G: the norm launch's workgroups
     bool squares;
@@ -297,13 +319,11 @@ struct NormJoinParams {
     NormArgs args;
     bool squares;
 };
+template <uint32_t N>
 struct ListClipParams {
     const float *coef;
-    uint32_t count, chunks;
-    const void *x[kClipMax];
-    void *y[kClipMax];
-    uint64_t n[kClipMax];        // types: x's | y's << 2
-    uint32_t chunk0[kClipMax + 1];
+    ListArgs<N> list;     // types: x's | y's << 2
+    void *y[N];
 };
 // Norm of a compressed tensor (or a group's): a value per block.
 struct CodeNormParams {
@@ -351,12 +371,16 @@ int launch_sample(const SampleParams &p, void *stream, uint16_t *host_out);
 // The device fit (enqueues only).
 int launch_fit(const FitParams &p, void *stream);
 // Norms and clipping (norms.hip; the codes' norm in kernels.hip).
-int launch_list_norm(const ListNormParams &p, uint32_t grid, bool squares, void *stream);
-int launch_list_each(const ListEachParams &p, void *stream);
+template <uint32_t N>
+int launch_list_norm(const ListNormParams<N> &p, uint32_t grid, bool squares, void *stream);
+template <uint32_t N>
+int launch_list_one(const ListOneParams<N> &p, bool squares, void *stream);
+int launch_list_finish(const ListFinishParams &p, void *stream);
 int launch_norm_join(const NormJoinParams &p, uint32_t grid, void *stream);
 int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part, const NormArgs &args, bool squares,
                       float *each, void *stream);
-int launch_list_clip(const ListClipParams &p, uint32_t grid, void *stream);
+template <uint32_t N>
+int launch_list_clip(const ListClipParams<N> &p, void *stream);
 int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *stream);
 
 // Host codebook construction (codebook.cpp).

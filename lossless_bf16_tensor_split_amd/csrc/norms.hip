@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lct_internal.h"
 
@@ -124,15 +125,23 @@ __device__ __forceinline__ void add_range(const void *x, uint64_t e0, uint32_t m
     const char *p = static_cast<const char *>(x) + e0 * ES;
     const uint32_t nv = m / V;
     uint32_t v = t;
-    // eight loads in flight per thread
-    for (; v + 7 * threads < nv; v += 8 * threads) {
-        u32x4 r[8];
+    // B loads in flight per thread.  Non-temporal: read once, the values leave
+    // the caches to others; 8 GB of BF16 then take 1.21 ms in place of 1.37,
+    // and a clip that follows loses nothing it would still have found.
+    auto batch = [&](auto B_) {
+        constexpr uint32_t B = decltype(B_)::value;
+        for (; v + (B - 1) * threads < nv; v += B * threads) {
+            u32x4 r[B];
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k)
-            r[k] = *reinterpret_cast<const u32x4e *>(p + 16ull * (v + k * threads));
+            for (uint32_t k = 0; k < B; ++k)
+                r[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4e *>(p + 16ull * (v + k * threads)));
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) add16<TYPE>(r[k], acc);
-    }
+            for (uint32_t k = 0; k < B; ++k) add16<TYPE>(r[k], acc);
+        }
+    };
+    if (TYPE == LCT_FP32) batch(std::integral_constant<uint32_t, 16>{});   // a whole chunk: 104 us for 110 at 0.65 GB
+    batch(std::integral_constant<uint32_t, 8>{});
+    batch(std::integral_constant<uint32_t, 4>{});
     for (; v < nv; v += threads) add16<TYPE>(*reinterpret_cast<const u32x4e *>(p + 16ull * v), acc);
     const uint32_t tail = m - nv * V;
     if (t < tail) acc.add(element<TYPE>(x, e0 + nv * V + t), 0.0f);
@@ -193,23 +202,24 @@ __device__ __forceinline__ uint32_t run_owner(uint32_t c, uint32_t chunks, uint3
 // p.run[i]; where the tensors' own norms are wanted, the part of the run that
 // lies in tensor k goes to p.piece[i + k] (runs and tensors both ascend, so no
 // two pairs share a place).
-template <class A>
-__global__ __launch_bounds__(kNormThreads) void k_list_norm(const ListNormParams p) {
+template <class A, uint32_t N>
+__global__ __launch_bounds__(kNormThreads) void k_list_norm(const ListNormParams<N> p) {
     __shared__ double slots[kWaves];
+    const ListArgs<N> &li = p.list;
     const uint32_t i = blockIdx.x, G = gridDim.x;
-    uint32_t c = run_first(i, p.chunks, G);
-    const uint32_t end = run_first(i + 1, p.chunks, G);
-    uint32_t k = tensor_of(p.chunk0, p.count, c);
+    uint32_t c = run_first(i, li.chunks, G);
+    const uint32_t end = run_first(i + 1, li.chunks, G);
+    uint32_t k = tensor_of(li.chunk0, li.count, c);
     double run = 0.0;
     A acc;
     while (c < end) {
-        while (p.chunk0[k + 1] <= c) ++k;
-        const uint32_t stop = min(end, p.chunk0[k + 1]);
-        const uint64_t n = p.n[k] & kListElems;
-        const uint32_t type = (uint32_t)(p.n[k] >> kListTypeShift);
+        while (li.chunk0[k + 1] <= c) ++k;
+        const uint32_t stop = min(end, li.chunk0[k + 1]);
+        const uint64_t n = li.n[k] & kListElems;
+        const uint32_t type = (uint32_t)(li.n[k] >> kListTypeShift);
         for (; c < stop; ++c) {
-            const uint64_t at = (uint64_t)(c - p.chunk0[k]) * kListChunk;
-            add_typed(type, p.x[k], at, (uint32_t)min<uint64_t>(kListChunk, n - at), threadIdx.x, kNormThreads, acc);
+            const uint64_t at = (uint64_t)(c - li.chunk0[k]) * kListChunk;
+            add_typed(type, li.x[k], at, (uint32_t)min<uint64_t>(kListChunk, n - at), threadIdx.x, kNormThreads, acc);
         }
         if (p.piece) {
             const double v = group_join<A>(acc.value(), slots);
@@ -222,18 +232,64 @@ __global__ __launch_bounds__(kNormThreads) void k_list_norm(const ListNormParams
     if (threadIdx.x == 0) p.run[i] = run;
 }
 
-// The norm of each of a launch's tensors, a wave per tensor.
+// After a launch: a wave per tensor joins its pieces (the workgroups after
+// the first), and the first workgroup joins all runs into the result.
 template <class A>
-__global__ __launch_bounds__(kNormThreads) void k_list_each(const ListEachParams p) {
-    const uint32_t k = blockIdx.x * kWaves + (threadIdx.x >> 6), l = threadIdx.x & 63;
+__global__ __launch_bounds__(1024) void k_list_finish(const ListFinishParams p) {
+    __shared__ double slots[16];
+    uint32_t b = blockIdx.x;
+    if (p.out) {
+        if (b == 0) {
+            double v = 0.0;
+            for (uint64_t j = threadIdx.x; j < p.runs; j += 1024) v = A::join(v, p.run[j]);
+            v = group_join<A>(v, slots);
+            if (threadIdx.x == 0) *p.out = result(v, p.args, p.squares);
+            return;
+        }
+        --b;
+    }
+    const uint32_t k = b * 16 + (threadIdx.x >> 6), l = threadIdx.x & 63;
     if (k >= p.count) return;
     double v = 0.0;
     if (p.chunk0[k + 1] > p.chunk0[k]) {
-        const uint32_t a = run_owner(p.chunk0[k], p.chunks, p.G), b = run_owner(p.chunk0[k + 1] - 1, p.chunks, p.G);
-        for (uint32_t i = a + l; i <= b; i += 64) v = A::join(v, p.piece[i + k]);
+        const uint32_t first = run_owner(p.chunk0[k], p.chunks, p.G);
+        const uint32_t last = run_owner(p.chunk0[k + 1] - 1, p.chunks, p.G);
+        for (uint32_t i = first + l; i <= last; i += 64) v = A::join(v, p.piece[i + k]);
     }
     v = wave_join<A>(v);
     if (l == 0) p.each[k] = result(v, p.args, p.squares).norm;
+}
+
+// A short list in one launch: every wave of a single workgroup takes chunks
+// in turn and leaves their values in LDS.
+template <class A, uint32_t N>
+__global__ __launch_bounds__(kOneThreads) void k_list_one(const ListOneParams<N> p, bool squares) {
+    __shared__ double vals[kOneMax];
+    const ListArgs<N> &li = p.list;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+    for (uint32_t c = w; c < li.chunks; c += kOneThreads / 64) {
+        const uint32_t k = tensor_of(li.chunk0, li.count, c);
+        const uint64_t n = li.n[k] & kListElems, at = (uint64_t)(c - li.chunk0[k]) * kOneChunk;
+        A acc;
+        add_typed((uint32_t)(li.n[k] >> kListTypeShift), li.x[k], at, (uint32_t)min<uint64_t>(kOneChunk, n - at), l, 64,
+                  acc);
+        const double v = wave_join<A>(acc.value());
+        if (l == 0) vals[c] = v;
+    }
+    __syncthreads();
+    if (w == 0) {
+        double v = 0.0;
+        for (uint32_t c = l; c < li.chunks; c += 64) v = A::join(v, vals[c]);
+        v = wave_join<A>(v);
+        if (l == 0) *p.out = result(v, p.args, squares);
+    }
+    if (!p.each) return;
+    for (uint32_t k = w; k < li.count; k += kOneThreads / 64) {
+        double v = 0.0;
+        for (uint32_t c = li.chunk0[k] + l; c < li.chunk0[k + 1]; c += 64) v = A::join(v, vals[c]);
+        v = wave_join<A>(v);
+        if (l == 0) p.each[k] = result(v, p.args, squares).norm;
+    }
 }
 
 // Part values joined by G workgroups into G values (G = 1: the result).
@@ -278,12 +334,16 @@ __device__ __forceinline__ float product(float x, float c) {
     return p;
 }
 
-// f rounded to a 16-bit type (nearest, ties to even; an overflow of FP16
-// gives infinity).
+// Two values rounded to a 16-bit type (nearest, ties to even; an overflow of
+// FP16 gives infinity), the first in the low half.
 template <int TYPE>
-__device__ __forceinline__ uint32_t round16(float f) {
-    if (TYPE == LCT_FP16) return __builtin_bit_cast(uint16_t, (_Float16)f);
-    return __builtin_bit_cast(uint16_t, (__bf16)f);
+__device__ __forceinline__ uint32_t round16(float f, float g) {
+    if (TYPE == LCT_FP16) {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, f16x2{(_Float16)f, (_Float16)g});
+    }
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)f, (__bf16)g});
 }
 
 // y[i] = c * x[i] for elements [e0, e0 + m).  Eight elements a thread and
@@ -321,7 +381,7 @@ __device__ __forceinline__ void clip_range(const void *x, void *y, uint64_t e0, 
         } else {
             u32x4 o;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = round16<TO>(f[2 * k]) | (round16<TO>(f[2 * k + 1]) << 16);
+            for (int k = 0; k < 4; ++k) o[k] = round16<TO>(f[2 * k], f[2 * k + 1]);
             *reinterpret_cast<u32x4e *>(q) = o;
         }
     };
@@ -344,7 +404,7 @@ __device__ __forceinline__ void clip_range(const void *x, void *y, uint64_t e0, 
         if constexpr (TO == LCT_FP32)
             reinterpret_cast<float *>(py)[t] = f;
         else
-            reinterpret_cast<uint16_t *>(py)[t] = (uint16_t)round16<TO>(f);
+            reinterpret_cast<uint16_t *>(py)[t] = (uint16_t)round16<TO>(f, f);
     }
 }
 
@@ -358,27 +418,26 @@ __device__ __forceinline__ void clip_from(uint32_t to, const void *x, void *y, u
         clip_range<FROM, LCT_FP32>(x, y, e0, m, c);
 }
 
-__global__ __launch_bounds__(kNormThreads) void k_list_clip(const ListClipParams p) {
+// A workgroup per chunk: 1.6 G elements from FP32 to BF16 in 1.81 ms (5.3
+// TB/s), where 2048 workgroups that walk a run of chunks each take 1.88 ms.
+template <uint32_t N>
+__global__ __launch_bounds__(kNormThreads) void k_list_clip(const ListClipParams<N> p) {
     const float c = *p.coef;
-    const uint32_t G = gridDim.x;
-    uint32_t at = run_first(blockIdx.x, p.chunks, G);
-    const uint32_t end = run_first(blockIdx.x + 1, p.chunks, G);
-    uint32_t k = tensor_of(p.chunk0, p.count, at);
-    for (; at < end; ++at) {
-        while (p.chunk0[k + 1] <= at) ++k;
-        const uint32_t types = (uint32_t)(p.n[k] >> kListTypeShift);
-        const uint32_t from = types & 3u, to = types >> 2;
-        // in place, a coefficient of 1 leaves every value as it is
-        if (c == 1.0f && p.x[k] == p.y[k]) continue;
-        const uint64_t e0 = (uint64_t)(at - p.chunk0[k]) * kListChunk;
-        const uint32_t m = (uint32_t)min<uint64_t>(kListChunk, (p.n[k] & kListElems) - e0);
-        if (from == LCT_BF16)
-            clip_from<LCT_BF16>(to, p.x[k], p.y[k], e0, m, c);
-        else if (from == LCT_FP16)
-            clip_from<LCT_FP16>(to, p.x[k], p.y[k], e0, m, c);
-        else
-            clip_from<LCT_FP32>(to, p.x[k], p.y[k], e0, m, c);
-    }
+    const ListArgs<N> &li = p.list;
+    const uint32_t at = blockIdx.x;
+    const uint32_t k = tensor_of(li.chunk0, li.count, at);
+    const uint32_t types = (uint32_t)(li.n[k] >> kListTypeShift);
+    const uint32_t from = types & 3u, to = types >> 2;
+    // in place, a coefficient of 1 leaves every value as it is
+    if (c == 1.0f && li.x[k] == p.y[k]) return;
+    const uint64_t e0 = (uint64_t)(at - li.chunk0[k]) * kListChunk;
+    const uint32_t m = (uint32_t)min<uint64_t>(kListChunk, (li.n[k] & kListElems) - e0);
+    if (from == LCT_BF16)
+        clip_from<LCT_BF16>(to, li.x[k], p.y[k], e0, m, c);
+    else if (from == LCT_FP16)
+        clip_from<LCT_FP16>(to, li.x[k], p.y[k], e0, m, c);
+    else
+        clip_from<LCT_FP32>(to, li.x[k], p.y[k], e0, m, c);
 }
 
 template <class F>
@@ -389,22 +448,38 @@ int launched(F f) {
 
 }  // namespace
 
-int launch_list_norm(const ListNormParams &p, uint32_t grid, bool squares, void *stream) {
+template <uint32_t N>
+int launch_list_norm(const ListNormParams<N> &p, uint32_t grid, bool squares, void *stream) {
     return launched([&] {
         if (squares)
-            hipLaunchKernelGGL(k_list_norm<SumSq>, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL((k_list_norm<SumSq, N>), dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
         else
-            hipLaunchKernelGGL(k_list_norm<MaxAbs>, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL((k_list_norm<MaxAbs, N>), dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
     });
 }
+template int launch_list_norm(const ListNormParams<kListFew> &, uint32_t, bool, void *);
+template int launch_list_norm(const ListNormParams<kListMax> &, uint32_t, bool, void *);
 
-int launch_list_each(const ListEachParams &p, void *stream) {
-    const dim3 grid((p.count + kWaves - 1) / kWaves);
+template <uint32_t N>
+int launch_list_one(const ListOneParams<N> &p, bool squares, void *stream) {
+    return launched([&] {
+        if (squares)
+            hipLaunchKernelGGL((k_list_one<SumSq, N>), dim3(1), dim3(kOneThreads), 0, (hipStream_t)stream, p, squares);
+        else
+            hipLaunchKernelGGL((k_list_one<MaxAbs, N>), dim3(1), dim3(kOneThreads), 0, (hipStream_t)stream, p,
+                               squares);
+    });
+}
+template int launch_list_one(const ListOneParams<kListFew> &, bool, void *);
+template int launch_list_one(const ListOneParams<kListMax> &, bool, void *);
+
+int launch_list_finish(const ListFinishParams &p, void *stream) {
+    const dim3 grid((p.out ? 1 : 0) + (p.each ? (p.count + 15) / 16 : 0));
     return launched([&] {
         if (p.squares)
-            hipLaunchKernelGGL(k_list_each<SumSq>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL(k_list_finish<SumSq>, grid, dim3(1024), 0, (hipStream_t)stream, p);
         else
-            hipLaunchKernelGGL(k_list_each<MaxAbs>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL(k_list_finish<MaxAbs>, grid, dim3(1024), 0, (hipStream_t)stream, p);
     });
 }
 
@@ -430,10 +505,13 @@ int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part,
     });
 }
 
-int launch_list_clip(const ListClipParams &p, uint32_t grid, void *stream) {
+template <uint32_t N>
+int launch_list_clip(const ListClipParams<N> &p, void *stream) {
     return launched([&] {
-        hipLaunchKernelGGL(k_list_clip, dim3(grid), dim3(kNormThreads), 0, (hipStream_t)stream, p);
+        hipLaunchKernelGGL(k_list_clip<N>, dim3(p.list.chunks), dim3(kNormThreads), 0, (hipStream_t)stream, p);
     });
 }
+template int launch_list_clip(const ListClipParams<kListFew> &, void *);
+template int launch_list_clip(const ListClipParams<kClipMax> &, void *);
 
 }  // namespace lct
