@@ -223,11 +223,12 @@ void sgd_params(SgdParams &p, const lct_tensor &w_in, const lct_tensor &m, const
 
 // Clear, update, scan.
 lct_status sgd_launch(const SgdParams &p, uint64_t nb, bool group, void *stream) {
-    int e = launch_clear(p.scratch, nb, p.status, stream);
+    const OutSides o{{{p.scratch, p.o_obase, p.o_ovf, p.ovf_cap, p.status, p.o_cnt}}, 1, nb};
+    int e = launch_clear(o, stream);
     if (e != hipSuccess) return hip_fail(e, "clear launch");
     e = launch_sgd(p, stream, group);
     if (e != hipSuccess) return hip_fail(e, "sgd launch");
-    e = launch_scan(p.scratch, nb, p.o_obase, p.o_ovf, p.ovf_cap, p.status, p.o_cnt, stream);
+    e = launch_scan(o, stream);
     if (e != hipSuccess) return hip_fail(e, "scan launch");
     return LCT_OK;
 }
@@ -277,14 +278,14 @@ void mom_params(MomParams &p, const lct_tensor &w_in, const lct_tensor &m_in, co
 // Clear both outputs' scratch headers and status words, the fused kernel,
 // both outputs' overflow scans.
 lct_status mom_launch(const MomParams &p, uint64_t nb, bool group, void *stream) {
-    int e = launch_clear(p.ow_scratch, nb, p.ow_status, stream);
-    if (e == hipSuccess) e = launch_clear(p.om_scratch, nb, p.om_status, stream);
+    const OutSides o{{{p.ow_scratch, p.ow_obase, p.ow_ovf, p.ow_ovf_cap, p.ow_status, p.ow_cnt},
+                      {p.om_scratch, p.om_obase, p.om_ovf, p.om_ovf_cap, p.om_status, p.om_cnt}},
+                     2, nb};
+    int e = launch_clear(o, stream);
     if (e != hipSuccess) return hip_fail(e, "clear launch");
     e = launch_mom(p, stream, group);
     if (e != hipSuccess) return hip_fail(e, "momentum launch");
-    e = launch_scan(p.ow_scratch, nb, p.ow_obase, p.ow_ovf, p.ow_ovf_cap, p.ow_status, p.ow_cnt, stream);
-    if (e == hipSuccess)
-        e = launch_scan(p.om_scratch, nb, p.om_obase, p.om_ovf, p.om_ovf_cap, p.om_status, p.om_cnt, stream);
+    e = launch_scan(o, stream);
     if (e != hipSuccess) return hip_fail(e, "scan launch");
     return LCT_OK;
 }
@@ -736,11 +737,12 @@ lct_status lct_encode(const lct_codebook *cb, const uint16_t *d_x, const lct_ten
     p.status = out->status;
     p.scratch = (uint8_t *)out->scratch;
     fill_enc(*cb, &p.enc);
-    int e = launch_clear(p.scratch, nb, p.status, stream);
+    const OutSides o{{{p.scratch, p.obase, p.ovf, p.ovf_cap, p.status, p.cnt}}, 1, nb};
+    int e = launch_clear(o, stream);
     if (e != hipSuccess) return hip_fail(e, "clear launch");
     e = launch_encode(p, stream);
     if (e != hipSuccess) return hip_fail(e, "encode launch");
-    e = launch_scan(p.scratch, nb, p.obase, p.ovf, p.ovf_cap, p.status, p.cnt, stream);
+    e = launch_scan(o, stream);
     if (e != hipSuccess) return hip_fail(e, "scan launch");
     return LCT_OK;
 }
@@ -1075,11 +1077,12 @@ lct_status lct_encode_group(const lct_group *g, const lct_tensor *all, void *str
     p.status = all->status;
     p.scratch = (uint8_t *)all->scratch;
     p.grp = group_ref(*g);
-    int e = launch_clear(p.scratch, g->nblk, p.status, stream);
+    const OutSides o{{{p.scratch, p.obase, p.ovf, p.ovf_cap, p.status, p.cnt}}, 1, g->nblk};
+    int e = launch_clear(o, stream);
     if (e != hipSuccess) return hip_fail(e, "clear launch");
     e = launch_encode(p, stream, true);
     if (e != hipSuccess) return hip_fail(e, "group encode launch");
-    e = launch_scan(p.scratch, g->nblk, p.obase, p.ovf, p.ovf_cap, p.status, p.cnt, stream);
+    e = launch_scan(o, stream);
     if (e != hipSuccess) return hip_fail(e, "scan launch");
     return LCT_OK;
 }

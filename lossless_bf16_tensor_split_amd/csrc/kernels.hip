@@ -708,31 +708,20 @@ __device__ __forceinline__ void unit_finish(const WriterT<Rows> &st, uint32_t n_
 
 // ------------------------------------------------------------------ small kernels
 
-// A scratch header and the status word, cleared by a fill kernel (no
-// memset node if a caller captures the call in a graph).
-__global__ void k_clear(uint64_t *words, uint64_t nwords, uint32_t *status) {
+// A scratch header and the status word of every output, cleared by a fill
+// kernel (no memset node if a caller captures the call in a graph).
+__global__ void k_clear(const OutSides o, uint64_t nwords) {
+    const OutSide &d = o.side[blockIdx.y];
     const uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < nwords) words[i] = 0;
-    if (i == 0) *status = 0u;
+    if (i < nwords) reinterpret_cast<uint64_t *>(d.scratch)[i] = 0;
+    if (i == 0) *d.status = 0u;
 }
 
-// Overflow offsets: an exclusive scan of the blocks' spill totals (each the
-// sum of its units' records), one block per thread, groups chained by the
-// look-back.  Writes obase and flags a too-small overflow region; the
-// placing kernel finds a unit's place within its block from the records.
-__global__ __launch_bounds__(kScanGroup) void k_scan(uint8_t *scratch, uint64_t nblk, uint64_t *obase,
-                                                     uint64_t ovf_cap, uint32_t *status) {
-    __shared__ uint32_t s_g;
-    __shared__ uint64_t s_wave[kScanGroup / 64], s_excl;
-    const uint32_t t = threadIdx.x;
-    if (t == 0) s_g = atomicAdd(reinterpret_cast<uint32_t *>(scratch + kScrTicket2), 1u);
-    __syncthreads();
-    const uint32_t g = s_g;
-    // one thread per block: its units' records are contiguous
-    const uint64_t b = (uint64_t)g * kScanGroup + t;
-    const UnitRec *rec = reinterpret_cast<const UnitRec *>(scratch + scr_rec_offset(nblk));
+// The spill total of block b (0 past the last) from its units' records, which
+// are contiguous; parked: whether some unit parked its counts.
+__device__ __forceinline__ uint64_t block_spill(const UnitRec *rec, uint64_t b, uint64_t nblk, uint32_t &parked) {
     uint64_t total = 0;
-    uint32_t parked = 0;
+    parked = 0;
     if (b < nblk) {
         UnitRec r[kMaxUnits];
 #pragma unroll
@@ -743,8 +732,14 @@ __global__ __launch_bounds__(kScanGroup) void k_scan(uint8_t *scratch, uint64_t 
             parked |= r[k].flags & 1u;
         }
     }
-    // group scan of the totals (64-bit sums)
-    uint64_t inc = total;
+    return total;
+}
+
+// Inclusive scan over a workgroup of kScanGroup threads (64-bit sums); agg:
+// the whole sum.
+__device__ __forceinline__ uint64_t group_scan(uint64_t v, uint64_t (&s_wave)[kScanGroup / 64], uint64_t &agg) {
+    const uint32_t t = threadIdx.x;
+    uint64_t inc = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const uint64_t x = __shfl_up(inc, d, 64);
@@ -752,57 +747,116 @@ __global__ __launch_bounds__(kScanGroup) void k_scan(uint8_t *scratch, uint64_t 
     }
     if (lane() == 63) s_wave[t >> 6] = inc;
     __syncthreads();
-    uint64_t before = 0, agg = 0;
+    uint64_t before = 0;
+    agg = 0;
 #pragma unroll
     for (uint32_t k = 0; k < kScanGroup / 64; ++k) {
         before += k < (t >> 6) ? s_wave[k] : 0;
         agg += s_wave[k];
     }
-    inc += before;
+    return inc + before;
+}
+
+// A unit's parked counts go in place, and its spilled bytes from the second
+// staging area to the overflow region from `to` on; run by one wave.
+__device__ __forceinline__ void place_unit(const OutSide &d, const UnitRec &r, uint64_t u, uint64_t nblk, uint64_t to) {
+    const uint32_t l = lane();
+    if (r.flags & 1u) {
+        const uint16_t *parked_cnt = reinterpret_cast<const uint16_t *>(d.scratch + scr_cnt_offset(nblk));
+        const uint64_t at = u / kMaxUnits * NS + (u % kMaxUnits) * US;
+        d.cnt[at + l] = parked_cnt[at + l];
+    }
+    const uint8_t *stage2 = d.scratch + scr_stage2_offset(nblk, d.ovf_cap);
+    for (uint64_t i = l; i < r.total; i += 64)
+        if (r.base + i < d.ovf_cap && to + i < d.ovf_cap) d.ovf[to + i] = stage2[r.base + i];
+}
+
+// Overflow offsets: an exclusive scan of the blocks' spill totals, one block
+// per thread, groups chained by the look-back.  Writes obase and flags a
+// too-small overflow region; the placing kernel finds a unit's place within
+// its block from the records.
+__global__ __launch_bounds__(kScanGroup) void k_scan(const OutSides o) {
+    __shared__ uint32_t s_g;
+    __shared__ uint64_t s_wave[kScanGroup / 64], s_excl;
+    const OutSide &d = o.side[blockIdx.y];
+    const uint64_t nblk = o.nblk;
+    const uint32_t t = threadIdx.x;
+    if (t == 0) s_g = atomicAdd(reinterpret_cast<uint32_t *>(d.scratch + kScrTicket2), 1u);
+    __syncthreads();
+    const uint32_t g = s_g;
+    const uint64_t b = (uint64_t)g * kScanGroup + t;
+    uint32_t parked;
+    const uint64_t total = block_spill(reinterpret_cast<const UnitRec *>(d.scratch + scr_rec_offset(nblk)), b, nblk,
+                                       parked);
+    uint64_t agg;
+    const uint64_t inc = group_scan(total, s_wave, agg);
     if (t < 64) {
-        uint64_t *flags = reinterpret_cast<uint64_t *>(scratch + kScrFlags);
-        const uint64_t ex = lookback(flags, g, agg, status);
+        uint64_t *flags = reinterpret_cast<uint64_t *>(d.scratch + kScrFlags);
+        const uint64_t ex = lookback(flags, g, agg, d.status);
         if (t == 0) s_excl = ex;
     }
     __syncthreads();
     const uint64_t ex = s_excl + inc - total;
-    if (b < nblk) obase[b] = ex;
+    if (b < nblk) d.obase[b] = ex;
     if (b + 1 == nblk) {
-        obase[nblk] = ex + total;
-        if (ex + total > ovf_cap) atomicOr(status, LCT_ST_OVF_FULL);
+        d.obase[nblk] = ex + total;
+        if (ex + total > d.ovf_cap) atomicOr(d.status, LCT_ST_OVF_FULL);
     }
     // parked counts are put in place by the placing kernel: tell it
     if (__any(parked != 0) && lane() == 0)
-        atomicOr(reinterpret_cast<uint32_t *>(scratch + kScrParked), 1u);
+        atomicOr(reinterpret_cast<uint32_t *>(d.scratch + kScrParked), 1u);
 }
 
-// After the scan: every unit's spilled bytes go from the second staging area
-// to the overflow region at its block's offset plus the spills of the block's
-// earlier units, and parked counts go in place.  One wave per unit, the
-// workgroups taking units round-robin; nothing to do (no spills, nothing
-// parked) ends every wave at once.
-__global__ __launch_bounds__(256) void k_place(const uint8_t *scratch, uint64_t nblk, const uint64_t *obase,
-                                               uint8_t *ovf, uint64_t ovf_cap, uint16_t *cnt) {
-    const uint32_t parked = *reinterpret_cast<const uint32_t *>(scratch + kScrParked);
-    if (obase[nblk] == 0 && parked == 0) return;
+// After the scan: every unit's spilled bytes go to the overflow region at its
+// block's offset plus the spills of the block's earlier units, and parked
+// counts go in place.  One wave per unit, the workgroups taking units
+// round-robin; nothing to do (no spills, nothing parked) ends every wave at
+// once.
+__global__ __launch_bounds__(256) void k_place(const OutSides o) {
+    const OutSide &d = o.side[blockIdx.y];
+    const uint64_t nblk = o.nblk;
+    const uint32_t parked = *reinterpret_cast<const uint32_t *>(d.scratch + kScrParked);
+    if (d.obase[nblk] == 0 && parked == 0) return;
     const uint64_t nunits = nblk * kMaxUnits;
-    const UnitRec *rec = reinterpret_cast<const UnitRec *>(scratch + scr_rec_offset(nblk));
-    const uint8_t *stage2 = scratch + scr_stage2_offset(nblk, ovf_cap);
-    const uint16_t *parked_cnt = reinterpret_cast<const uint16_t *>(scratch + scr_cnt_offset(nblk));
-    const uint32_t l = lane();
+    const UnitRec *rec = reinterpret_cast<const UnitRec *>(d.scratch + scr_rec_offset(nblk));
     for (uint64_t u = (uint64_t)blockIdx.x * 4 + wave_id(); u < nunits; u += (uint64_t)gridDim.x * 4) {
         const UnitRec r = rec[u];
         const uint64_t b = u / kMaxUnits;
-        if (r.flags & 1u) {
-            const uint64_t at = b * NS + (u % kMaxUnits) * US;
-            cnt[at + l] = parked_cnt[at + l];
-        }
-        if (r.total == 0) continue;
-        uint64_t to = obase[b];
-        for (uint64_t v = b * kMaxUnits; v < u; ++v) to += rec[v].total;
-        for (uint64_t i = l; i < r.total; i += 64)
-            if (r.base + i < ovf_cap && to + i < ovf_cap) ovf[to + i] = stage2[r.base + i];
+        uint64_t to = d.obase[b];
+        if (r.total)
+            for (uint64_t v = b * kMaxUnits; v < u; ++v) to += rec[v].total;
+        place_unit(d, r, u, nblk, to);
     }
+}
+
+// Both at once where one scan group holds every block: each workgroup scans
+// all totals for itself (16 KB of records at most) and places its own block's
+// units; the first writes obase and the status.
+__global__ __launch_bounds__(kScanGroup) void k_settle(const OutSides o) {
+    __shared__ uint64_t s_wave[kScanGroup / 64], s_excl;
+    const OutSide &d = o.side[blockIdx.y];
+    const uint64_t nblk = o.nblk, own = blockIdx.x;
+    const UnitRec *rec = reinterpret_cast<const UnitRec *>(d.scratch + scr_rec_offset(nblk));
+    const uint64_t b = threadIdx.x;
+    const uint64_t u = own * kMaxUnits + wave_id();
+    const UnitRec r = rec[u];
+    uint32_t parked;
+    const uint64_t total = block_spill(rec, b, nblk, parked);
+    uint64_t agg;
+    const uint64_t ex = group_scan(total, s_wave, agg) - total;
+    if (own == 0) {
+        if (b < nblk) d.obase[b] = ex;
+        if (b == 0) {
+            d.obase[nblk] = agg;
+            if (agg > d.ovf_cap) atomicOr(d.status, LCT_ST_OVF_FULL);
+        }
+    }
+    if (b == own) s_excl = ex;
+    __syncthreads();
+    uint64_t to = s_excl;
+    if (r.total)
+        for (uint64_t v = own * kMaxUnits; v < u; ++v) to += rec[v].total;
+    place_unit(d, r, u, nblk, to);
 }
 
 __device__ uint16_t g_sample[4096];
@@ -2902,24 +2956,24 @@ size_t decode_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * dec_wav
 size_t norm_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * norm_wave_bytes(cap); }
 size_t sgd_lds(uint32_t cap, uint32_t waves) { return kSgdWave0 + (size_t)waves * sgd_wave_bytes(cap); }
 
-int launch_clear(uint8_t *scratch, uint64_t nblk, uint32_t *status, void *stream) {
-    const uint64_t words = (scr_clear_bytes(nblk) + 7) / 8;
-    const uint32_t grid = (uint32_t)((words + 255) / 256);
-    hipLaunchKernelGGL(k_clear, dim3(grid), dim3(256), 0, (hipStream_t)stream,
-                       reinterpret_cast<uint64_t *>(scratch), words, status);
+int launch_clear(const OutSides &o, void *stream) {
+    const uint64_t words = (scr_clear_bytes(o.nblk) + 7) / 8;
+    const dim3 grid((uint32_t)((words + 255) / 256), o.count);
+    hipLaunchKernelGGL(k_clear, grid, dim3(256), 0, (hipStream_t)stream, o, words);
     return (int)hipGetLastError();
 }
 
-int launch_scan(uint8_t *scratch, uint64_t nblk, uint64_t *obase, uint8_t *ovf, uint64_t ovf_cap,
-                uint32_t *status, uint16_t *cnt, void *stream) {
-    const uint64_t groups = (nblk + kScanGroup - 1) / kScanGroup;
-    hipLaunchKernelGGL(k_scan, dim3((uint32_t)groups), dim3(kScanGroup), 0, (hipStream_t)stream,
-                       scratch, nblk, obase, ovf_cap, status);
+int launch_scan(const OutSides &o, void *stream) {
+    if (o.nblk <= kScanGroup) {
+        hipLaunchKernelGGL(k_settle, dim3((uint32_t)o.nblk, o.count), dim3(kScanGroup), 0, (hipStream_t)stream, o);
+        return (int)hipGetLastError();
+    }
+    const uint64_t groups = (o.nblk + kScanGroup - 1) / kScanGroup;
+    hipLaunchKernelGGL(k_scan, dim3((uint32_t)groups, o.count), dim3(kScanGroup), 0, (hipStream_t)stream, o);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    const uint32_t place = (uint32_t)std::min<uint64_t>(nblk, 2048);
-    hipLaunchKernelGGL(k_place, dim3(place), dim3(256), 0, (hipStream_t)stream, scratch, nblk, obase, ovf,
-                       ovf_cap, cnt);
+    const dim3 place((uint32_t)std::min<uint64_t>(o.nblk, 2048), o.count);
+    hipLaunchKernelGGL(k_place, place, dim3(256), 0, (hipStream_t)stream, o);
     return (int)hipGetLastError();
 }
 

@@ -357,10 +357,24 @@ constexpr int kMaxDevices = 64;
 // once per device (hipGetSymbolAddress).  Returns a hipError_t.
 int noalloc_scratch(uint8_t **out);
 
+// The overflow side of a call's outputs (the momentum step has two).
+struct OutSide {
+    uint8_t *scratch;
+    uint64_t *obase;
+    uint8_t *ovf;
+    uint64_t ovf_cap;
+    uint32_t *status;
+    uint16_t *cnt;
+};
+struct OutSides {
+    OutSide side[2];
+    uint32_t count;
+    uint64_t nblk;
+};
+
 // Host-side launchers (kernels.hip).  Each returns the hipError_t of the launch.
-int launch_clear(uint8_t *scratch, uint64_t nblk, uint32_t *status, void *stream);
-int launch_scan(uint8_t *scratch, uint64_t nblk, uint64_t *obase, uint8_t *ovf, uint64_t ovf_cap,
-                uint32_t *status, uint16_t *cnt, void *stream);
+int launch_clear(const OutSides &o, void *stream);
+int launch_scan(const OutSides &o, void *stream);
 int launch_encode(const EncodeParams &p, void *stream, bool group = false);
 int launch_decode(const DecodeParams &p, void *stream, bool group = false);
 int launch_sgd(const SgdParams &p, void *stream, bool group = false);
