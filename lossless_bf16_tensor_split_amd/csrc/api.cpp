@@ -389,28 +389,18 @@ lct_status check_norm(int32_t kind, double max_norm, double scale, const void *s
     return overlap(s, o) || overlap(s, e) || overlap(o, e) ? LCT_EALIAS : LCT_OK;
 }
 
-// The result from `count` part values (every stride-th double).  Many are
-// first folded into kFoldGrid (room for which `fold` gives).
-lct_status norm_join(const double *part, uint64_t count, uint64_t stride, bool squares, NormArgs args, double *fold,
+// The result from `count` part values (every stride-th double).
+lct_status norm_join(const double *part, uint64_t count, uint64_t stride, bool squares, NormArgs args,
                      lct_norm_t *out, void *stream) {
     NormJoinParams p;
     memset(&p, 0, sizeof p);
     p.part = part;
     p.count = count;
     p.stride = stride;
+    p.out = out;
     p.args = args;
     p.squares = squares;
-    if (fold && count > kFoldFrom) {
-        p.fold = fold;
-        const int e = launch_norm_join(p, kFoldGrid, stream);
-        if (e != hipSuccess) return hip_fail(e, "norm join launch");
-        p.part = fold;
-        p.count = kFoldGrid;
-        p.stride = 1;
-        p.fold = nullptr;
-    }
-    p.out = out;
-    const int e = launch_norm_join(p, 1, stream);
+    const int e = launch_norm_join(p, stream);
     return e == hipSuccess ? LCT_OK : hip_fail(e, "norm join launch");
 }
 
@@ -522,11 +512,20 @@ lct_status code_norm(CodeNormParams &p, const lct_tensor &t, uint64_t nb, const 
         const int e = launch_code_norm(p, g != nullptr, squares, stream);
         if (e != hipSuccess) return hip_fail(e, "code norm launch");
     }
-    if (each) {
-        const int e = launch_group_each(p.grp.ent, count, part, {max_norm, scale}, squares, each, stream);
-        if (e != hipSuccess) return hip_fail(e, "group norms launch");
-    }
-    return norm_join(part, nb, 1, squares, {max_norm, scale}, part + nb, out, stream);
+    CodeFinishParams q;
+    memset(&q, 0, sizeof q);
+    q.part = part;
+    q.nblk = nb;
+    q.fold = nb > kFoldFrom ? part + nb : nullptr;
+    q.out = out;
+    q.ent = p.grp.ent;
+    q.each = each;
+    q.args = {max_norm, scale};
+    q.count = count;
+    q.squares = squares;
+    const int e = launch_code_finish(q, stream);
+    if (e != hipSuccess) return hip_fail(e, "code norm launch");
+    return q.fold ? norm_join(q.fold, kFoldGrid, 1, squares, q.args, out, stream) : LCT_OK;
 }
 
 // One launch of the clip for tensors [k0, k0 + count).
@@ -1258,7 +1257,7 @@ lct_status lct_norm_join(const lct_norm_t *d_parts, uint32_t count, int32_t kind
     if (st != LCT_OK) return st;
     static_assert(sizeof(lct_norm_t) == 16 && offsetof(lct_norm_t, sum) == 0, "sums are every second double");
     return norm_join(reinterpret_cast<const double *>(d_parts), count, 2, kind == LCT_NORM_L2, {max_norm, scale},
-                     nullptr, d_out, stream);
+                     d_out, stream);
 }
 
 lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list *y, void *stream) {

@@ -124,6 +124,19 @@ __device__ __forceinline__ void st8(uint32_t off, uint32_t v) {
     *reinterpret_cast<lds_u8 *>(off) = (uint8_t)v;
 }
 
+// Eight rows of sign-fraction bytes, US bytes each, read transposed: lane l
+// gets its own stream's byte of each row, the first row's in byte 0 of x.
+// off: tr_offset(l) past the first row.  (The hardware transposes within 16
+// lanes: lanes 2r and 2r+1 of them name the halves of row r's 16 bytes.)
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+__device__ __forceinline__ u32x2 ld_tr8(uint32_t off) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2 *>(off)));
+}
+__device__ __forceinline__ uint32_t tr_offset(uint32_t l) {
+    return (l % 16 / 2) * kUnitStreams + l / 16 * 16 + l % 2 * 8;
+}
+
 constexpr uint32_t log2c(uint32_t v) { return v <= 1 ? 0 : 1 + log2c(v / 2); }
 
 __device__ __forceinline__ uint32_t lane() { return __lane_id(); }
@@ -297,7 +310,8 @@ struct Reader {
     // returned, and a caller that gets more than 30 must decode the same
     // fields again with next().  q is kept at most qmax so that a bad group
     // never addresses past the stream's zero row.
-    template <uint32_t N>
+    // Without CLAMP the caller knows that all N fields are the stream's.
+    template <uint32_t N, bool CLAMP = true>
     __device__ __forceinline__ uint32_t next_n(uint32_t tab, int32_t qmax, uint32_t (&e23)[N]) {
         const uint32_t win = window();
         uint32_t c = 0;
@@ -308,7 +322,7 @@ struct Reader {
             e23[k] = (wk << (en & 31u)) | en;
             c += (en >> 8) & 0xFFu;
         }
-        q = min(q + (int32_t)c, qmax);
+        q = CLAMP ? min(q + (int32_t)c, qmax) : q + (int32_t)c;
         return c;
     }
 };
@@ -1346,8 +1360,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_decode(const DecodeParams p)
 
 // The decoder's walk with every value joined into a norm in place of being
 // stored: a sum of squares in 64 bits, or the largest magnitude (its BF16 bits
-// without the sign, so that NaN is above infinity).  LDS as the decoder's; the
-// first 32 bytes take the waves' values at the block's end.
+// without the sign, so that NaN is above infinity).
 template <bool SQ>
 struct CodeAcc {
     double s = 0.0;
@@ -1361,24 +1374,53 @@ struct CodeAcc {
             m = max(m, f & 0x7FFF0000u);
         }
     }
+    // A step's CH values.  Their squares are summed in fp32 first and the sum
+    // joined in 64 bits: each square has 16 significant bits, so the sum is
+    // off by 15 * 2^-24 of itself at most (the conversions to 64 bits, at a
+    // quarter of the rate of the other instructions, are a third of the time
+    // otherwise).  A sum in [2^-96, 2^127) lost nothing to underflow (a
+    // square below 2^-126 is less than 2^-30 of it) or overflow; any other,
+    // zero and NaN included, is made again in 64 bits.
+    __device__ __forceinline__ void add_step(const uint32_t (&f)[CH]) {
+        if (!SQ) {
+#pragma unroll
+            for (uint32_t i = 0; i < CH; ++i) add(f[i]);
+            return;
+        }
+        float t = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < CH; ++i) t = __builtin_fmaf(__uint_as_float(f[i]), __uint_as_float(f[i]), t);
+        if (__builtin_expect(wave_all(t >= 0x1p-96f && t < 0x1p127f), 1)) {
+            s += (double)t;
+            return;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < CH; ++i) add(f[i]);
+    }
 };
 
-// Per wave: the decoder's rows, then two regions of sign-fraction bytes, one
-// half (CH positions of the unit's streams) each.
-constexpr uint32_t kNormRegB = CH * US;
-__host__ __device__ constexpr uint32_t norm_wave_bytes(uint32_t cap) { return dec_wave_bytes(cap) + 2 * kNormRegB; }
+// LDS: the decode table, the waves' rows with a zero row before, between and
+// after them (the row past one wave's last is the row before the next one's
+// first), then a region of sign-fraction bytes per wave, one half (CH
+// positions of the unit's streams).  At the CLEAN capacity 32,000 bytes, so
+// that five workgroups share a CU.
+constexpr uint32_t kNormTab = 0, kNormRows = 1024, kNormRegB = CH * US;
+__host__ __device__ constexpr uint32_t norm_row0(uint32_t cap, uint32_t wave) {
+    return kNormRows + (wave * (cap + 1) + 1) * ROWB;
+}
+__host__ __device__ constexpr uint32_t norm_slab(uint32_t cap, uint32_t wave) {
+    return norm_row0(cap, kDecWaves) + wave * kNormRegB;
+}
 
 // Positions [0, CH * nh) of every stream, none of them spilled.  The
-// sign-fraction bytes move by 16-byte loads through the wave's LDS regions (a
-// byte load per position and lane keeps the address unit busy for as long as
-// the arithmetic takes).
+// sign-fraction bytes move by 16-byte loads through the wave's LDS regions and
+// come out of them transposed, a lane's next eight in one read.
 template <uint32_t CAPT, bool SQ>
 __device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t row0, uint32_t slab, uint32_t nh,
                                             const uint8_t *sfu, CodeAcc<SQ> &acc) {
     const uint32_t l = lane();
     const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap - 2;
-    const uint32_t lw = l & ~3u;
-    const uint32_t jsel = (l & 3u) * 0x01010000u | 0x0C0Cu;
+    const uint32_t tr = tr_offset(l);
     constexpr uint32_t kNone = 0x80000000u;
     constexpr uint32_t kHalfB = CH * NS;
     const uint32_t piece = (l >> 2) * NS + 16 * (l & 3);
@@ -1387,33 +1429,35 @@ __device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t r
         return __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, h < nh ? h * kHalfB + piece : kNone, 0, 0));
     };
-    auto region = [&](uint32_t h) { return slab + (h & 1u) * kNormRegB; };
-    st128(region(0) + 16 * l, load(0));
-    u32x4 next = load(1);
+    st128(slab + 16 * l, load(0));
+    u32x4 a = load(1), b = load(2);
     for (uint32_t h = 0; h < nh; ++h) {
-        uint32_t w[CH];
-#pragma unroll
-        for (uint32_t i = 0; i < CH; ++i) w[i] = ld32(region(h) + i * US + lw);
-        st128(region(h + 1) + 16 * l, next);
-        next = load(h + 2);
+        // (a wave's LDS accesses run in order: the store follows the reads)
+        const u32x2 w[2] = {ld_tr8(slab + tr), ld_tr8(slab + 8 * US + tr)};
+        st128(slab + 16 * l, a);
+        a = b;
+        b = load(h + 3);
         // four fields per window, as the decoder reads them; a window that
         // ran out is read again one field at a time
+        uint32_t f[CH];
 #pragma unroll
         for (uint32_t g = 0; g < CH; g += 4) {
             const int32_t q0 = rd.q;
             uint32_t e23[4];
-            const uint32_t c = rd.next_n<4>(kDecTab, qmax, e23);
-            if (__builtin_expect(!__all(c <= 30), 0)) {
+            const uint32_t c = rd.next_n<4, false>(kNormTab, qmax, e23);
+            if (__builtin_expect(!wave_all(c <= 30), 0)) {
                 rd.q = q0;
 #pragma unroll
                 for (uint32_t k = 0; k < 4; ++k) {
-                    e23[k] = rd.next(kDecTab);
+                    e23[k] = rd.next(kNormTab);
                     rd.q = min(rd.q, qmax);
                 }
             }
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) acc.add(join32s(w[g + k], e23[k], jsel));
+            for (uint32_t k = 0; k < 4; ++k)
+                f[g + k] = join32s(w[g / 8][g / 4 % 2], e23[k], k * 0x01010000u | 0x0C0Cu);
         }
+        acc.add_step(f);
     }
 }
 
@@ -1432,7 +1476,7 @@ __device__ __forceinline__ void norm_rest(const CodeNormParams &p, Reader &rd, u
 #pragma unroll
         for (uint32_t i = 0; i < CH; ++i) {
             const uint32_t j = j0 + i;
-            uint32_t e23 = rd.next(kDecTab);
+            uint32_t e23 = rd.next(kNormTab);
             rd.q = min(rd.q, qmax);
             if (j >= c_s && j < n_s) {
                 const uint64_t k = sp0 + (j - c_s);
@@ -1447,13 +1491,12 @@ template <uint32_t CAPT, bool GROUP, bool SQ>
 __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p) {
     const uint32_t b = blockIdx.x, h = wave_id();   // a workgroup is a block's four units
     const uint32_t k = GROUP ? p.grp.blk_tensor[b] : 0u;
-    stage_dec(GROUP ? p.grp.dec[k] : p.dec, kDecTab);
+    stage_dec(GROUP ? p.grp.dec[k] : p.dec, kNormTab);
     __syncthreads();
     const uint32_t l = lane();
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
-    const uint32_t base = kDecWave0 + wave_id() * norm_wave_bytes(cap);
-    const uint32_t row0 = base + ROWB;
-    st32(base + 4 * l, 0);                      // row -1
+    const uint32_t row0 = norm_row0(cap, h);
+    st32(row0 - ROWB + 4 * l, 0);               // row -1
     st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
     rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
     const BlockSpan sp = GROUP ? group_span(p.grp, k, p.block_elems, b) : flat_span(nullptr, p.n, p.block_elems, b);
@@ -1465,7 +1508,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p)
     rd.init(row0, l);
     const bool spills = ob0 != ob1;
     const uint32_t nh = spills ? 0u : halves(nb);
-    if (nh) norm_halves<CAPT, SQ>(rd, cap, row0, base + dec_wave_bytes(cap), nh, sfu, acc);
+    if (nh) norm_halves<CAPT, SQ>(rd, cap, row0, norm_slab(cap, h), nh, sfu, acc);
     if (nh * CH < walk_end(nb)) {
         const uint32_t n_s = stream_len(nb, h * US + l);
         uint32_t c_s = n_s, excl = 0;
@@ -1482,21 +1525,21 @@ __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p)
         else
             m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
     }
-    if (l == 0) {
+    if (l == 0) {   // in the wave's own region, which it has done with
         const uint64_t bits = SQ ? (uint64_t)__double_as_longlong(v) : m;
-        st32(8 * h, (uint32_t)bits);
-        st32(8 * h + 4, (uint32_t)(bits >> 32));
+        st32(norm_slab(cap, h), (uint32_t)bits);
+        st32(norm_slab(cap, h) + 4, (uint32_t)(bits >> 32));
     }
     __syncthreads();
     if (threadIdx.x != 0) return;
     if (SQ) {
         v = 0.0;
         for (uint32_t j = 0; j < kDecWaves; ++j)
-            v += __longlong_as_double((long long)(((uint64_t)ld32(8 * j + 4) << 32) | ld32(8 * j)));
+            v += __longlong_as_double((long long)(((uint64_t)ld32(norm_slab(cap, j) + 4) << 32) | ld32(norm_slab(cap, j))));
         p.part[b] = v;
     } else {
         m = 0;
-        for (uint32_t j = 0; j < kDecWaves; ++j) m = max(m, ld32(8 * j));
+        for (uint32_t j = 0; j < kDecWaves; ++j) m = max(m, ld32(norm_slab(cap, j)));
         p.part[b] = (double)__uint_as_float(m);
     }
 }
@@ -2953,7 +2996,7 @@ int launch_update(P p, const void *full, uint32_t full_waves, size_t full_lds, s
 
 size_t encode_lds(uint32_t cap) { return kEncWave0 + (size_t)kEncWaves * enc_wave_bytes(cap); }
 size_t decode_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * dec_wave_bytes(cap); }
-size_t norm_lds(uint32_t cap) { return kDecWave0 + (size_t)kDecWaves * norm_wave_bytes(cap); }
+size_t norm_lds(uint32_t cap) { return norm_slab(cap, kDecWaves); }
 size_t sgd_lds(uint32_t cap, uint32_t waves) { return kSgdWave0 + (size_t)waves * sgd_wave_bytes(cap); }
 
 int launch_clear(const OutSides &o, void *stream) {

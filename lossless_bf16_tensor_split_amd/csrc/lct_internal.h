@@ -309,14 +309,24 @@ struct ListFinishParams {
     bool squares;
     uint32_t chunk0[kListMax + 1];
 };
-// Part values (every `stride`-th double) joined by the launch's workgroups,
-// into a value each (fold) or, by a single one, into the result (out).
+// Part values (every `stride`-th double) joined into the result.
 struct NormJoinParams {
     const double *part;
     uint64_t count, stride;
-    double *fold;
     lct_norm_t *out;
     NormArgs args;
+    bool squares;
+};
+// What follows the norm of codes (a value per block in part).
+struct CodeFinishParams {
+    const double *part;
+    uint64_t nblk;
+    double *fold;         // many blocks: kFoldGrid values first (null: the result)
+    lct_norm_t *out;
+    const GroupEntry *ent;
+    float *each;          // null: not wanted
+    NormArgs args;
+    uint32_t count;       // a group's tensors
     bool squares;
 };
 template <uint32_t N>
@@ -390,9 +400,8 @@ int launch_list_norm(const ListNormParams<N> &p, uint32_t grid, bool squares, vo
 template <uint32_t N>
 int launch_list_one(const ListOneParams<N> &p, bool squares, void *stream);
 int launch_list_finish(const ListFinishParams &p, void *stream);
-int launch_norm_join(const NormJoinParams &p, uint32_t grid, void *stream);
-int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part, const NormArgs &args, bool squares,
-                      float *each, void *stream);
+int launch_norm_join(const NormJoinParams &p, void *stream);
+int launch_code_finish(const CodeFinishParams &p, void *stream);
 template <uint32_t N>
 int launch_list_clip(const ListClipParams<N> &p, void *stream);
 int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *stream);

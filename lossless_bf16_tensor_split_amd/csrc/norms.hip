@@ -292,34 +292,42 @@ __global__ __launch_bounds__(kOneThreads) void k_list_one(const ListOneParams<N>
     }
 }
 
-// Part values joined by G workgroups into G values (G = 1: the result).
+// The result from part values (every stride-th double), by one workgroup.
 template <class A>
 __global__ __launch_bounds__(1024) void k_norm_join(const NormJoinParams p) {
     __shared__ double slots[16];
-    const uint64_t G = gridDim.x, i = blockIdx.x;
-    const uint64_t lo = i * p.count / G, hi = (i + 1) * p.count / G;
     double v = 0.0;
-    for (uint64_t j = lo + threadIdx.x; j < hi; j += blockDim.x) v = A::join(v, p.part[j * p.stride]);
+    for (uint64_t j = threadIdx.x; j < p.count; j += 1024) v = A::join(v, p.part[j * p.stride]);
+    v = group_join<A>(v, slots);
+    if (threadIdx.x == 0) *p.out = result(v, p.args, p.squares);
+}
+
+// After the blocks' values of a compressed tensor or group: the first F
+// workgroups join them all, into the result (F = 1) or a value each (fold),
+// and each of the others makes the norm of a tensor of the group.
+template <class A>
+__global__ __launch_bounds__(1024) void k_code_finish(const CodeFinishParams p) {
+    __shared__ double slots[16];
+    const uint32_t F = p.fold ? kFoldGrid : 1u, i = blockIdx.x;
+    uint64_t lo, hi;
+    if (i < F) {
+        lo = i * p.nblk / F;
+        hi = (i + 1) * p.nblk / F;
+    } else {
+        const GroupEntry e = p.ent[i - F];
+        lo = e.blk0;
+        hi = lo + e.nblk;
+    }
+    double v = 0.0;
+    for (uint64_t j = lo + threadIdx.x; j < hi; j += 1024) v = A::join(v, p.part[j]);
     v = group_join<A>(v, slots);
     if (threadIdx.x != 0) return;
-    if (p.fold)
+    if (i >= F)
+        p.each[i - F] = result(v, p.args, p.squares).norm;
+    else if (p.fold)
         p.fold[i] = v;
     else
         *p.out = result(v, p.args, p.squares);
-}
-
-// The norm of each tensor of a group from its blocks' values.
-template <class A>
-__global__ __launch_bounds__(kNormThreads) void k_group_each(const GroupEntry *ent, uint32_t count, const double *part,
-                                                             const NormArgs args, bool squares, float *each) {
-    __shared__ double slots[kWaves];
-    for (uint32_t k = blockIdx.x; k < count; k += gridDim.x) {
-        const GroupEntry e = ent[k];
-        double v = 0.0;
-        for (uint32_t j = threadIdx.x; j < e.nblk; j += kNormThreads) v = A::join(v, part[(uint64_t)e.blk0 + j]);
-        v = group_join<A>(v, slots);
-        if (threadIdx.x == 0) each[k] = result(v, args, squares).norm;
-    }
 }
 
 // ------------------------------------------------------------------ clip
@@ -483,25 +491,22 @@ int launch_list_finish(const ListFinishParams &p, void *stream) {
     });
 }
 
-int launch_norm_join(const NormJoinParams &p, uint32_t grid, void *stream) {
+int launch_norm_join(const NormJoinParams &p, void *stream) {
     return launched([&] {
         if (p.squares)
-            hipLaunchKernelGGL(k_norm_join<SumSq>, dim3(grid), dim3(1024), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL(k_norm_join<SumSq>, dim3(1), dim3(1024), 0, (hipStream_t)stream, p);
         else
-            hipLaunchKernelGGL(k_norm_join<MaxAbs>, dim3(grid), dim3(1024), 0, (hipStream_t)stream, p);
+            hipLaunchKernelGGL(k_norm_join<MaxAbs>, dim3(1), dim3(1024), 0, (hipStream_t)stream, p);
     });
 }
 
-int launch_group_each(const GroupEntry *ent, uint32_t count, const double *part, const NormArgs &args, bool squares,
-                      float *each, void *stream) {
-    const dim3 grid(std::min<uint32_t>(count, 4096));
+int launch_code_finish(const CodeFinishParams &p, void *stream) {
+    const dim3 grid((p.fold ? kFoldGrid : 1u) + (p.each ? p.count : 0u));
     return launched([&] {
-        if (squares)
-            hipLaunchKernelGGL(k_group_each<SumSq>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, ent, count, part,
-                               args, squares, each);
+        if (p.squares)
+            hipLaunchKernelGGL(k_code_finish<SumSq>, grid, dim3(1024), 0, (hipStream_t)stream, p);
         else
-            hipLaunchKernelGGL(k_group_each<MaxAbs>, grid, dim3(kNormThreads), 0, (hipStream_t)stream, ent, count,
-                               part, args, squares, each);
+            hipLaunchKernelGGL(k_code_finish<MaxAbs>, grid, dim3(1024), 0, (hipStream_t)stream, p);
     });
 }
 
