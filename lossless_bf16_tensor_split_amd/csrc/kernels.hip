@@ -248,6 +248,9 @@ __device__ __forceinline__ uint32_t join32s(uint32_t w, uint32_t e23, uint32_t s
     return r;
 }
 
+// join32s's selector of byte k.
+__device__ __forceinline__ constexpr uint32_t byte_sel(uint32_t k) { return k * 0x01010000u | 0x0C0Cu; }
+
 // ------------------------------------------------------------------ code tables in LDS
 
 // Decode table at byte offset `tab`, indexed by peek*4 (see the bit reader).
@@ -1455,7 +1458,7 @@ __device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t r
             }
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
-                f[g + k] = join32s(w[g / 8][g / 4 % 2], e23[k], k * 0x01010000u | 0x0C0Cu);
+                f[g + k] = join32s(w[g / 8][g / 4 % 2], e23[k], byte_sel(k));
         }
         acc.add_step(f);
     }
@@ -1863,8 +1866,7 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
     int32_t qmmax;
     const uint32_t mine = 16 * l;                 // this lane's 16 bytes of a region
-    const uint32_t lw = l & ~3u;                  // its sign-fraction byte's word in a region row
-    const uint32_t jsel = (l & 3u) * 0x01010000u | 0x0C0Cu;
+    const uint32_t tr = tr_offset(l);             // its place in a transposed read of eight region rows
     // The unit's sign-fraction bytes of W, M and the result through buffer
     // resources spanning them: 32-bit offsets, and an offset past the range
     // makes a load that returns nothing (no traffic) or a store that is
@@ -1909,7 +1911,8 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
     // fields) of the group the writer codes next, the result bytes of the
     // half that leaves next.  Before the first group they stand for a group
     // that codes to nothing.
-    uint32_t wsP[4] = {0, 0, 0, 0}, msP[4] = {0, 0, 0, 0}, ewP[4] = {0, 0, 0, 0}, emP[4] = {0, 0, 0, 0};
+    u32x2 ws8 = {0u, 0u}, ms8 = {0u, 0u};         // bytes of two groups, a group a word
+    uint32_t wsP = 0, msP = 0, ewP[4] = {0, 0, 0, 0}, emP[4] = {0, 0, 0, 0};
     u32x2 wc[4] = {{0u, 0u}, {0u, 0u}, {0u, 0u}, {0u, 0u}};
     uint32_t ew8[4] = {kSgdNoField, kSgdNoField, kSgdNoField, kSgdNoField};
     uint32_t jw = 0;                              // position of the writer's group
@@ -1945,16 +1948,15 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
         const uint32_t rc = region(h) + GS * 4 * US;                       // group s's rows
         const uint32_t rcm = region_m(h) + GS * 4 * US;
         const uint32_t rp = (GS ? region(h) : region(h + 1)) + ((GS + 3) % 4) * 4 * US;   // group s-1's rows
-        uint32_t wsC[4], msC[4], ewC[4], emC[4];
+        uint32_t ewC[4], emC[4];
         uint32_t winw = 0, winm = 0, cw = 0, cm = 0;
         const int32_t qw0 = rw.q, qm0 = rm.q;
         if (DEC) {
             winw = rw.window();
             winm = rm.window();
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                wsC[k] = ld32(lay.sw + rc + k * US + lw);
-                msC[k] = ld32(lay.sm + rcm + k * US + lw);
+            if (GS % 2 == 0) {
+                ws8 = ld_tr8(lay.sw + rc + tr);
+                ms8 = ld_tr8(lay.sm + rcm + tr);
             }
         }
         // the writer's group, with checks when some stream is near its end
@@ -1972,8 +1974,8 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
                 wkm = winm >> cm;
                 enm = ld32(tabM + (wkm & 0x3FCu));
             }
-            r[k] = __builtin_fmaf(mul, __uint_as_float(join32s(msP[k], emP[k], jsel)),
-                                  __uint_as_float(join32s(wsP[k], ewP[k], jsel)));
+            r[k] = __builtin_fmaf(mul, __uint_as_float(join32s(msP, emP[k], byte_sel(k))),
+                                  __uint_as_float(join32s(wsP, ewP[k], byte_sel(k))));
             nan |= r[k] != r[k];
             if (k & 1) {
                 uint32_t hh = cvt_bf16x2(r[k - 1], r[k]);
@@ -2021,9 +2023,9 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
 #pragma unroll
             for (uint32_t k = 0; k < 4; k += 2) {
                 const uint32_t R0 =
-                    sgd_round(join32s(wsP[k], ewP[k], jsel), join32s(msP[k], emP[k], jsel), mul);
-                const uint32_t R1 = sgd_round(join32s(wsP[k + 1], ewP[k + 1], jsel),
-                                              join32s(msP[k + 1], emP[k + 1], jsel), mul);
+                    sgd_round(join32s(wsP, ewP[k], byte_sel(k)), join32s(msP, emP[k], byte_sel(k)), mul);
+                const uint32_t R1 = sgd_round(join32s(wsP, ewP[k + 1], byte_sel(k + 1)),
+                                              join32s(msP, emP[k + 1], byte_sel(k + 1)), mul);
                 const uint32_t hh = (R0 >> 16) | (R1 & 0xFFFF0000u);
                 ep[k] = (hh >> 4) & 0x7F8u;
                 ep[k + 1] = (hh >> 20) & 0x7F8u;
@@ -2043,11 +2045,11 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
         if (DEC) {
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
-                wsP[k] = wsC[k];
-                msP[k] = msC[k];
                 ewP[k] = ewC[k];
                 emP[k] = emC[k];
             }
+            wsP = ws8[GS % 2];
+            msP = ms8[GS % 2];
         }
     };
     // Half h: its four stages.  At the end of its first stage the last group
@@ -2533,8 +2535,7 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
     const int32_t qwmax = Reader::bias(lay.w0) + (int32_t)capbits - 2;
     const int32_t qmmax = Reader::bias(lay.m0) + (int32_t)capbits - 2;
     const uint32_t mine = 16 * l;
-    const uint32_t lw = l & ~3u;
-    const uint32_t jsel = (l & 3u) * 0x01010000u | 0x0C0Cu;
+    const uint32_t tr = tr_offset(l);
     const uint32_t span = (nh * CH - 1) * NS + US;
     const __amdgpu_buffer_rsrc_t rws = wave_rsrc(p.w_sf + r0, span);
     const __amdgpu_buffer_rsrc_t rms = wave_rsrc(p.m_sf + r0, span);
@@ -2573,7 +2574,8 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
             gv[k] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rg, o + 2 * k * NS, 0, 0);
     };
 
-    uint32_t wsP[4] = {0, 0, 0, 0}, msP[4] = {0, 0, 0, 0}, ewP[4] = {0, 0, 0, 0}, emP[4] = {0, 0, 0, 0};
+    u32x2 ws8 = {0u, 0u}, ms8 = {0u, 0u};
+    uint32_t wsP = 0, msP = 0, ewP[4] = {0, 0, 0, 0}, emP[4] = {0, 0, 0, 0};
     uint32_t gP[4] = {0, 0, 0, 0}, gC[4] = {0, 0, 0, 0};
     u32x2 wcw[4] = {{0u, 0u}, {0u, 0u}, {0u, 0u}, {0u, 0u}}, wcm[4] = {{0u, 0u}, {0u, 0u}, {0u, 0u}, {0u, 0u}};
     uint32_t ew8[4] = {kMWNoField, kMWNoField, kMWNoField, kMWNoField};
@@ -2610,16 +2612,15 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
         constexpr uint32_t GS = decltype(GS_)::value;
         const uint32_t rc = region(h) + GS * 4 * US;
         const uint32_t rp = (GS ? region(h) : region(h + 1)) + ((GS + 3) % 4) * 4 * US;
-        uint32_t wsC[4], msC[4], ewC[4], emC[4];
+        uint32_t ewC[4], emC[4];
         uint32_t winw = 0, winm = 0, cw = 0, cm = 0;
         const int32_t qw0 = rw.q, qm0 = rm.q;
         if (DEC) {
             winw = rw.window();
             winm = rm.window();
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                wsC[k] = ld32(lay.sw + rc + k * US + lw);
-                msC[k] = ld32(lay.sm + rc + k * US + lw);
+            if (GS % 2 == 0) {
+                ws8 = ld_tr8(lay.sw + rc + tr);
+                ms8 = ld_tr8(lay.sm + rc + tr);
             }
             gload(4 * h + GS, gC);
         }
@@ -2639,16 +2640,16 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
                 wkm = winm >> cm;
                 enm = ld32(kMMD + (wkm & 0x3FCu));
             }
-            rmv[k] = __builtin_fmaf(p.mu, __uint_as_float(join32s(msP[k], emP[k], jsel)),
+            rmv[k] = __builtin_fmaf(p.mu, __uint_as_float(join32s(msP, emP[k], byte_sel(k))),
                                     __uint_as_float(gradient<CLIP>(gP[k], c)));
             if (k & 1) {
                 // M' of the pair, rounded; W' from M' as rounded
                 uint32_t hm = cvt_bf16x2(rmv[k - 1], rmv[k]);
                 asm volatile("" : "+v"(hm));
                 rwv[k - 1] = __builtin_fmaf(p.neg_eta, __uint_as_float(hm << 16),
-                                            __uint_as_float(join32s(wsP[k - 1], ewP[k - 1], jsel)));
+                                            __uint_as_float(join32s(wsP, ewP[k - 1], byte_sel(k - 1))));
                 rwv[k] = __builtin_fmaf(p.neg_eta, __uint_as_float(hm & 0xFFFF0000u),
-                                        __uint_as_float(join32s(wsP[k], ewP[k], jsel)));
+                                        __uint_as_float(join32s(wsP, ewP[k], byte_sel(k))));
                 uint32_t hw = cvt_bf16x2(rwv[k - 1], rwv[k]);
                 asm volatile("" : "+v"(hw));
                 nan |= (rmv[k - 1] != rmv[k - 1]) | (rmv[k] != rmv[k]) | (rwv[k - 1] != rwv[k - 1]) |
@@ -2700,11 +2701,11 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
             // becomes the canonical one's)
 #pragma unroll
             for (uint32_t k = 0; k < 4; k += 2) {
-                const uint32_t Rm0 = sgd_round(gradient<CLIP>(gP[k], c), join32s(msP[k], emP[k], jsel), p.mu);
-                const uint32_t Rm1 = sgd_round(gradient<CLIP>(gP[k + 1], c), join32s(msP[k + 1], emP[k + 1], jsel),
+                const uint32_t Rm0 = sgd_round(gradient<CLIP>(gP[k], c), join32s(msP, emP[k], byte_sel(k)), p.mu);
+                const uint32_t Rm1 = sgd_round(gradient<CLIP>(gP[k + 1], c), join32s(msP, emP[k + 1], byte_sel(k + 1)),
                                                p.mu);
-                const uint32_t Rw0 = sgd_round(join32s(wsP[k], ewP[k], jsel), Rm0 & 0xFFFF0000u, p.neg_eta);
-                const uint32_t Rw1 = sgd_round(join32s(wsP[k + 1], ewP[k + 1], jsel), Rm1 & 0xFFFF0000u,
+                const uint32_t Rw0 = sgd_round(join32s(wsP, ewP[k], byte_sel(k)), Rm0 & 0xFFFF0000u, p.neg_eta);
+                const uint32_t Rw1 = sgd_round(join32s(wsP, ewP[k + 1], byte_sel(k + 1)), Rm1 & 0xFFFF0000u,
                                                p.neg_eta);
                 const uint32_t hm = (Rm0 >> 16) | (Rm1 & 0xFFFF0000u);
                 const uint32_t hw = (Rw0 >> 16) | (Rw1 & 0xFFFF0000u);
@@ -2732,12 +2733,12 @@ __device__ __forceinline__ void mom_stream_full(const MomParams &p, const SgdLay
         if (DEC) {
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
-                wsP[k] = wsC[k];
-                msP[k] = msC[k];
                 ewP[k] = ewC[k];
                 emP[k] = emC[k];
                 gP[k] = gC[k];
             }
+            wsP = ws8[GS % 2];
+            msP = ms8[GS % 2];
         }
     };
     auto half = [&](uint32_t h, Halves &next) {
