@@ -260,11 +260,12 @@ struct NormArgs {
     double max_norm, scale;
 };
 
-// Lists of dense tensors: cut into chunks of kListChunk elements, numbered
+// Lists of dense tensors: cut into chunks of 2^shift elements, numbered
 // through a launch's tensors (chunk0[k]: tensor k's first; chunk0[count]: all
 // of them).  A size travels with its element types above kListTypeShift.
 constexpr uint32_t kNormThreads = 256;
-constexpr uint32_t kListChunk = 16384;
+constexpr uint32_t kListChunkMax = 14, kListChunkMin = 11;   // shifts
+constexpr uint32_t kListSpread = 512;     // chunks that a cut should make
 constexpr uint32_t kListMax = 192;        // tensors per launch of the norm
 constexpr uint32_t kListFew = 16;         // short lists take kernels with shorter arguments
 constexpr uint32_t kClipMax = 128;        // and of the clip
@@ -273,13 +274,13 @@ constexpr uint32_t kListTypeShift = 48;
 constexpr uint64_t kListElems = (1ull << kListTypeShift) - 1;
 constexpr uint64_t kListMaxElems = 1ull << 44;   // of a whole list: chunk numbers stay within 32 bits
 // Short lists in one launch: a workgroup of kOneThreads does every chunk of
-// kOneChunk elements, a wave each.
+// 2^kOneShift elements, a wave each.
 constexpr uint32_t kOneThreads = 1024;
-constexpr uint32_t kOneChunk = 2048;
+constexpr uint32_t kOneShift = 11;
 constexpr uint32_t kOneMax = 64;          // chunks
 template <uint32_t N>
 struct ListArgs {
-    uint32_t count, chunks;
+    uint32_t count, chunks, shift;
     const void *x[N];
     uint64_t n[N];
     uint32_t chunk0[N + 1];

@@ -1,7 +1,7 @@
 // norms.hip -- norms of many dense tensors, the clip coefficient, and the
 // scaling of many tensors by it, for CDNA4 (gfx950, wave64).
 //
-// A list's tensors are cut into chunks of kListChunk elements, numbered
+// A list's tensors are cut into chunks of 2^11 to 2^14 elements, numbered
 // through the list; a launch covers at most kListMax tensors, whose pointers
 // and sizes travel as kernel arguments (no table to upload, so tensors may
 // move from step to step).  Sums of squares are kept in 64 bits from the
@@ -174,17 +174,17 @@ __device__ __forceinline__ lct_norm_t result(double v, const NormArgs &a, bool s
 }
 
 // The last tensor that starts at or before chunk c (tensors of no elements
-// have no chunks, so it is the one that holds c).
-__device__ __forceinline__ uint32_t tensor_of(const uint32_t *chunk0, uint32_t count, uint32_t c) {
-    uint32_t lo = 0, hi = count;   // chunk0[lo] <= c < chunk0[hi]
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (chunk0[mid] <= c)
-            lo = mid;
-        else
-            hi = mid;
+// have no chunks, so it is the one that holds c): every lane looks at a few
+// tensors, one round trip for all (a search by halves takes eight).
+template <uint32_t N>
+__device__ __forceinline__ uint32_t tensor_of(const ListArgs<N> &li, uint32_t c) {
+    uint32_t k = 0;
+#pragma unroll
+    for (uint32_t b = 0; b < N; b += 64) {
+        const uint32_t j = b + (threadIdx.x & 63);
+        k += __popcll(__ballot(j < li.count && li.chunk0[min(j, N)] <= c));
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(k) - 1;
 }
 
 // Workgroup i of G takes chunks [first(i), first(i + 1)); chunk c belongs to
@@ -209,17 +209,17 @@ __global__ __launch_bounds__(kNormThreads) void k_list_norm(const ListNormParams
     const uint32_t i = blockIdx.x, G = gridDim.x;
     uint32_t c = run_first(i, li.chunks, G);
     const uint32_t end = run_first(i + 1, li.chunks, G);
-    uint32_t k = tensor_of(li.chunk0, li.count, c);
+    uint32_t k = tensor_of(li, c);
     double run = 0.0;
     A acc;
     while (c < end) {
-        while (li.chunk0[k + 1] <= c) ++k;
+        while (li.chunk0[k + 1] <= c) ++k;   // (the first is at hand)
         const uint32_t stop = min(end, li.chunk0[k + 1]);
         const uint64_t n = li.n[k] & kListElems;
         const uint32_t type = (uint32_t)(li.n[k] >> kListTypeShift);
         for (; c < stop; ++c) {
-            const uint64_t at = (uint64_t)(c - li.chunk0[k]) * kListChunk;
-            add_typed(type, li.x[k], at, (uint32_t)min<uint64_t>(kListChunk, n - at), threadIdx.x, kNormThreads, acc);
+            const uint64_t at = (uint64_t)(c - li.chunk0[k]) << li.shift;
+            add_typed(type, li.x[k], at, (uint32_t)min<uint64_t>(1u << li.shift, n - at), threadIdx.x, kNormThreads, acc);
         }
         if (p.piece) {
             const double v = group_join<A>(acc.value(), slots);
@@ -268,11 +268,11 @@ __global__ __launch_bounds__(kOneThreads) void k_list_one(const ListOneParams<N>
     const ListArgs<N> &li = p.list;
     const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
     for (uint32_t c = w; c < li.chunks; c += kOneThreads / 64) {
-        const uint32_t k = tensor_of(li.chunk0, li.count, c);
-        const uint64_t n = li.n[k] & kListElems, at = (uint64_t)(c - li.chunk0[k]) * kOneChunk;
+        const uint32_t k = tensor_of(li, c);
+        const uint64_t n = li.n[k] & kListElems, at = (uint64_t)(c - li.chunk0[k]) << kOneShift;
         A acc;
-        add_typed((uint32_t)(li.n[k] >> kListTypeShift), li.x[k], at, (uint32_t)min<uint64_t>(kOneChunk, n - at), l, 64,
-                  acc);
+        add_typed((uint32_t)(li.n[k] >> kListTypeShift), li.x[k], at, (uint32_t)min<uint64_t>(1u << kOneShift, n - at), l,
+                  64, acc);
         const double v = wave_join<A>(acc.value());
         if (l == 0) vals[c] = v;
     }
@@ -433,13 +433,13 @@ __global__ __launch_bounds__(kNormThreads) void k_list_clip(const ListClipParams
     const float c = *p.coef;
     const ListArgs<N> &li = p.list;
     const uint32_t at = blockIdx.x;
-    const uint32_t k = tensor_of(li.chunk0, li.count, at);
+    const uint32_t k = tensor_of(li, at);
     const uint32_t types = (uint32_t)(li.n[k] >> kListTypeShift);
     const uint32_t from = types & 3u, to = types >> 2;
     // in place, a coefficient of 1 leaves every value as it is
     if (c == 1.0f && li.x[k] == p.y[k]) return;
-    const uint64_t e0 = (uint64_t)(at - li.chunk0[k]) * kListChunk;
-    const uint32_t m = (uint32_t)min<uint64_t>(kListChunk, (li.n[k] & kListElems) - e0);
+    const uint64_t e0 = (uint64_t)(at - li.chunk0[k]) << li.shift;
+    const uint32_t m = (uint32_t)min<uint64_t>(1u << li.shift, (li.n[k] & kListElems) - e0);
     if (from == LCT_BF16)
         clip_from<LCT_BF16>(to, li.x[k], p.y[k], e0, m, c);
     else if (from == LCT_FP16)
