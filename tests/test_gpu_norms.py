@@ -754,3 +754,175 @@ def test_another_current_device_is_refused(L, monkeypatch):
         L.lct_list_norm(lst, out)
     with pytest.raises(ValueError, match="current device"):
         L.lct_list_clip(lst, torch.ones(1, device=x.device))
+
+
+# ------------------------------------------------------------------ where the updates' kernels meet
+
+def update_case(L, orc, w, m, gr, B, cw, c, eta, inplace, what):
+    """The clipped and the plain update and momentum step of one tensor against
+    the oracle's bytes; (W', M', update's W') as device tensors."""
+    n = w.size
+    lay = L.layout(B, cw)
+    cbw, ocw = check_codebook(L, orc, synth.Model(0, 0.02), w)
+    cbm, ocm = check_codebook(L, orc, synth.Model(0, 1e-3), m)
+    rw, rm = orc.encode(ocw, w, B, cw), orc.encode(ocm, m, B, cw)
+    outs = []
+    for clip in (True, False):
+        coef = torch.tensor([c if clip else 1.0], device="cuda")
+        cc = float(np.float32(c)) if clip else 1.0
+
+        def fresh():
+            tw, tm = L.encode(cbw, dev(w), lay), L.encode(cbm, dev(m), lay)
+            ow, om = L.alloc_tensor(n, lay), L.alloc_tensor(n, lay)
+            if inplace:
+                ow.sf, ow.pay, ow.cnt, ow.obase = tw.sf, tw.pay, tw.cnt, tw.obase
+            return tw, tm, ow, om
+
+        tw, tm, ow, om = fresh()
+        if inplace:
+            om.sf, om.pay, om.cnt, om.obase = tm.sf, tm.pay, tm.cnt, tm.obase
+        if clip:
+            L.lct_momentum_step_clip(cbw, tw, cbm, tm, dev(gr), coef, 0.9, eta, ow, om)
+        else:
+            L.lct_momentum_step(cbw, tw, cbm, tm, dev(gr), 0.9, eta, ow, om)
+        wo, mo = orc.momentum_clip_dense(w, m, gr, cc, 0.9, eta)
+        ref_w, ref_m = orc.encode(ocw, wo, B, cw), orc.encode(ocm, mo, B, cw)
+        assert_same(host_parts(ow), ref_w, what + " W'")
+        assert_same(host_parts(om), ref_m, what + " M'")
+        tw, tm, os_, _ = fresh()
+        if clip:
+            L.lct_sgd_step_clip(cbw, tw, cbm, tm, eta, coef, os_)
+        else:
+            L.lct_sgd_step(cbw, tw, cbm, tm, eta, os_)
+        assert_same(host_parts(os_), orc.sgd(ocw, rw, ocm, rm, float(np.float32(eta) * np.float32(cc))), what + " sgd")
+        outs.append((ow, om, os_, ref_w, ref_m))
+        for cb, t, x in ((cbw, os_, None), (cbw, ow, wo), (cbm, om, mo)):
+            y = L.decode(cb, t)
+            torch.cuda.synchronize()
+            if x is not None:
+                assert np.array_equal(y.view(torch.int16).cpu().numpy().view(np.uint16), x), what
+    return outs
+
+
+def three(n, seed, sg=1e-3):
+    g = np.random.default_rng(seed)
+    return [synth.to_bf16_bits(g.normal(0, s, n)) for s in (0.02, 1e-3, sg)]
+
+
+LAST = [1, 255, 256, 257, 4095, 4096, 4097, 5 * 4096 + 300, 8192, 30000, 32767]
+
+
+@pytest.mark.parametrize("B,cw", [(65536, 25), (32768, 12), (32768, 11)])
+def test_partial_blocks_of_every_kind(L, orc, B, cw):
+    """A whole block and a last one of many lengths: shorter than a step, whole
+    steps, whole steps and a rest, one element short of a block."""
+    for last in LAST + ([B - 256, B - 1] if B == 65536 else []):
+        n = B + last
+        w, m, gr = three(n, last)
+        update_case(L, orc, w, m, gr, B, cw, 0.37, 0.1, last % 2 == 0, "last=%d cw=%d" % (last, cw))
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("B,cw,last", [(65536, 25, 40000), (65536, 25, 65535), (32768, 11, 20001), (32768, 12, 4097)])
+def test_partial_blocks_whose_outputs_spill(L, orc, B, cw, last, inplace):
+    """No input field spilled, so a partial block takes the full-block path,
+    whose outputs run out of room midway and go on spilling in its rest."""
+    g = np.random.default_rng(last + cw)
+    n = B + last
+    # inputs from a narrow band of exponents (short codes), a gradient far
+    # outside M's codes and a rate that carries W outside its own
+    w = synth.to_bf16_bits(np.sign(g.normal(size=n)) * g.uniform(0.016, 0.031, n))
+    m = synth.to_bf16_bits(np.sign(g.normal(size=n)) * g.uniform(0.8e-3, 1.5e-3, n))
+    gr = synth.to_bf16_bits(g.normal(0, 0.5, n))
+    outs = update_case(L, orc, w, m, gr, B, cw, 0.9, 40.0, inplace, "spills last=%d cw=%d" % (last, cw))
+    assert all(o[4].spilled > n // 8 for o in outs)
+
+
+@pytest.mark.parametrize("B,cw", [(4096, 25), (8192, 25), (4096, 12), (4096, 11), (4096, 7)])
+def test_more_blocks_than_workgroups(L, orc, B, cw):
+    """More blocks than the general kernels have workgroups: full blocks run in
+    the kernels of their own (the ring kernel at 25 words), the last, partial
+    one and those with spilled inputs in the general ones."""
+    n = 700 * B + 1234
+    w, m, gr = three(n, B + cw)
+    if cw >= 11:
+        w[5 * B:5 * B + 3000] = synth.to_bf16_bits(np.full(3000, 1e-25))    # spills one block's inputs
+    outs = update_case(L, orc, w, m, gr, B, cw, 0.37, 0.1, False, "700 blocks of %d, cw=%d" % (B, cw))
+    full = outs[0][2].full_path_units()
+    assert full == outs[1][2].full_path_units() and full <= 4 * 700
+    if cw == 25:
+        assert full >= 4 * 690
+    update_case(L, orc, w, m, gr, B, cw, 0.37, 0.1, True, "in place, 700 blocks of %d, cw=%d" % (B, cw))
+
+
+def test_around_one_workgroup_per_block(L, orc):
+    """Numbers of blocks about the size from which one scan, and from which one
+    kernel, no longer does all of them."""
+    for nblk in (255, 256, 257, 511, 512, 513):
+        n = (nblk - 1) * 4096 + 77
+        w, m, gr = three(n, nblk)
+        update_case(L, orc, w, m, gr, 4096, 25, 0.5, 0.1, nblk % 2 == 0, "%d blocks" % nblk)
+
+
+def test_norm_scratch_is_not_passed(L):
+    """Guards after the scratch and around the results stay, for every form of
+    the norms."""
+    def guarded(need):
+        buf = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[:need]
+
+    r = np.random.default_rng(2)
+    for ns in ([3], [100, 0, 5000], [3_000_000], [int(v) for v in r.integers(1, 70000, 401)], [50] * 193):
+        xs = [torch.randn(n, device="cuda").to(BF) for n in ns]
+        lst = L.LctList(xs)
+        for each in (True, False):
+            buf, scr = guarded(lst.need)
+            out = L.alloc_norm(len(ns), each, scratch=scr)
+            L.lct_list_norm(lst, out, 1.0)
+            check_norm(out, [f64(x) for x in xs], "l2", 1.0, 1.0, "%d tensors" % len(ns))
+            assert (buf[lst.need:] == 0xA5).all()
+    for n in (100, 4096 * 4200 + 5):
+        x = (torch.randn(n, device="cuda") * 0.02).to(BF)
+        cb = L.lct_codebook_build(L.Model(0, 0.02, 0.0), x)
+        t = L.encode(cb, x, L.layout(4096, 4))
+        need = L._norm_scratch(0, t.sizes.nblk)
+        buf, scr = guarded(need)
+        out = L.alloc_norm(scratch=scr, nblk=t.sizes.nblk)
+        L.lct_tensor_norm(cb, t, out, 1.0)
+        check_norm(out, [f64(x)], "l2", 1.0, 1.0, "codes", CODES)
+        assert (buf[need:] == 0xA5).all()
+
+
+def test_short_norm_and_clip_replayed_from_a_graph(L):
+    """The one-launch norm and the clip in place captured together: each replay
+    scales what the one before left."""
+    xs = [torch.empty(n, device="cuda") for n in (1000, 1, 20000)]
+    ref = [torch.empty_like(x) for x in xs]
+    lst, rl = L.LctList(xs), L.LctList(ref)
+    out, ro = L.alloc_norm(3, True), L.alloc_norm(3, True)
+
+    def fill(seed):
+        g = torch.Generator().manual_seed(seed)
+        for x, y in zip(xs, ref):
+            v = torch.randn(x.numel(), generator=g)
+            x.copy_(v)
+            y.copy_(v)
+
+    fill(0)
+    L.lct_list_norm(lst, out, 5.0)
+    L.lct_list_clip(lst, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.lct_list_norm(lst, out, 5.0)
+        L.lct_list_clip(lst, out)
+    for rep in range(4):
+        fill(rep)
+        L.lct_list_norm(rl, ro, 5.0)
+        L.lct_list_clip(rl, ro)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.buf, ro.buf) and torch.equal(out.each, ro.each), rep
+        assert all(torch.equal(a, b) for a, b in zip(xs, ref)), rep
+        assert abs(float(L.grad_norm(xs).norm) - 5.0) < 5.0 * 2.0 ** -20
