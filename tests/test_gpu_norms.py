@@ -926,3 +926,34 @@ def test_short_norm_and_clip_replayed_from_a_graph(L):
         assert torch.equal(out.buf, ro.buf) and torch.equal(out.each, ro.each), rep
         assert all(torch.equal(a, b) for a, b in zip(xs, ref)), rep
         assert abs(float(L.grad_norm(xs).norm) - 5.0) < 5.0 * 2.0 ** -20
+
+
+def test_a_kept_descriptor_follows_its_buffers(L):
+    """A tensor's descriptor is kept from call to call: a buffer that is
+    replaced (by a right one, a short one, none) is seen, and not held."""
+    import weakref
+    n = 70000
+    x = (torch.randn(n, device="cuda") * 0.02).to(BF)
+    cb = L.lct_codebook_build(L.Model(0, 0.02, 0.0), x)
+    t = L.encode(cb, x, L.layout(65536, 25))
+    a = t.c()
+    assert t.c() is a and t.c(need_scratch=False) is a
+    old = weakref.ref(t.scratch)
+    t.scratch = torch.empty_like(t.scratch)
+    assert old() is None
+    b = t.c()
+    assert b is not a and b.scratch == t.scratch.data_ptr()
+    t.scratch = None
+    assert t.c().scratch is None
+    t.scratch = torch.empty(16, dtype=torch.uint8, device="cuda")
+    assert t.c(need_scratch=False).scratch == t.scratch.data_ptr()
+    with pytest.raises(ValueError, match="scratch"):
+        t.c()
+    t.sf = t.sf[:n - 1]
+    with pytest.raises(ValueError, match="sf"):
+        t.c(need_scratch=False)
+    t = L.encode(cb, x, L.layout(65536, 25))
+    t.c()
+    t.ovf_cap = t.ovf_cap * 2
+    with pytest.raises(ValueError, match="ovf"):
+        t.c()
