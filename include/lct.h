@@ -478,7 +478,8 @@ typedef struct {
 /* A list of dense tensors: host arrays of the caller's, read during the call
  * only (tensors may move from call to call).  Tensor k has n[k] contiguous
  * elements (0 allowed) of type[k] (lct_dtype) from d_x[k], which needs the
- * alignment of its elements only.  A list holds at most 2^44 elements. */
+ * alignment of its elements only.  A list holds at most 2^24 tensors and 2^44
+ * elements. */
 typedef struct {
     uint32_t count;
     const uint64_t *n;
@@ -488,8 +489,8 @@ typedef struct {
 
 /* Bytes of d_scratch of a norm: of a list of count tensors (nblk 0), or of a
  * compressed tensor or group of nblk blocks (lct_sizes, lct_group_sizes);
- * given both, enough for either.  Errors: LCT_EINVAL (null out, or nblk past
- * 2^32 - 1). */
+ * given both, enough for either.  Errors: LCT_EINVAL (null out, count past
+ * 2^24, or nblk past 2^32 - 1). */
 lct_status lct_norm_scratch(uint32_t count, uint64_t nblk, uint64_t *bytes);
 
 /* Norm of a list (a tensor that is listed twice counts twice).  d_each: count

@@ -671,7 +671,8 @@ class LctList:
 
 
 class LctNorm:
-    """A norm's result on the device, and the working memory of the call.
+    """A norm's result on the device (unset before the first call), and the
+    working memory of the call.
 
     ``sum`` (float64), ``norm`` and ``coef`` (float32) are 0-d views of one
     buffer; ``each`` holds every tensor's norm, or is None.  ``scratch`` may be
@@ -681,11 +682,12 @@ class LctNorm:
         dev = torch.device(device)
         if scratch is None:
             scratch = torch.empty(_norm_scratch(members, nblk), dtype=torch.uint8, device=dev)
-        self.buf = torch.zeros(16, dtype=torch.uint8, device=dev)
+        # (not filled: a call on another stream would race with that)
+        self.buf = torch.empty(16, dtype=torch.uint8, device=dev)
         self.sum = self.buf[0:8].view(torch.float64)[0]
         self.norm = self.buf[8:12].view(torch.float32)[0]
         self.coef = self.buf[12:16].view(torch.float32)[0]
-        self.each = torch.zeros(members, dtype=torch.float32, device=dev) if each else None
+        self.each = torch.empty(members, dtype=torch.float32, device=dev) if each else None
         self.members = members
         self.dev = self.buf.device.index
         self.buf_ptr = self.buf.data_ptr()
@@ -760,7 +762,8 @@ def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: fl
     """Norm of the union of the sets behind several results: a sequence of
     LctNorm, or their ``buf`` bytes gathered in one uint8 tensor [k, 16]."""
     if not torch.is_tensor(parts):
-        parts = torch.stack([p.buf for p in parts]) if len(parts) else out.buf[:0]
+        with torch.cuda.stream(stream):      # gathered where they are joined
+            parts = torch.stack([p.buf for p in parts]) if len(parts) else out.buf[:0]
     if parts.dtype != torch.uint8 or not parts.is_contiguous() or parts.numel() % 16:
         raise ValueError("parts must be a contiguous uint8 tensor of 16 bytes per result")
     _current(parts.device, "parts")

@@ -358,7 +358,7 @@ uint64_t type_bytes(int32_t type) { return type == LCT_FP32 ? 4 : 2; }
 Range member(const lct_list &x, uint32_t k) { return rng(x.d_x[k], x.n[k] * type_bytes(x.type[k])); }
 
 lct_status check_list(const lct_list *x) {
-    if (!x || (x->count > 0 && (!x->n || !x->d_x || !x->type))) return LCT_EINVAL;
+    if (!x || x->count > kListMaxCount || (x->count > 0 && (!x->n || !x->d_x || !x->type))) return LCT_EINVAL;
     uint64_t total = 0;
     for (uint32_t k = 0; k < x->count; ++k) {
         if (x->type[k] != LCT_BF16 && x->type[k] != LCT_FP16 && x->type[k] != LCT_FP32) return LCT_EINVAL;
@@ -446,8 +446,7 @@ lct_status list_one(const lct_list &x, bool squares, NormArgs args, float *each,
     return e == hipSuccess ? LCT_OK : hip_fail(e, "list norm launch");
 }
 
-// One launch for tensors [k0, k0 + count); *grid gets its workgroups and q
-// the list's cut.
+// One launch for tensors [k0, k0 + count); q gets its cut and workgroups.
 template <uint32_t N>
 int list_part(const lct_list &x, uint32_t k0, uint32_t count, bool squares, double *run, double *piece,
               ListFinishParams &q, void *stream) {
@@ -475,6 +474,7 @@ lct_status list_norm(const lct_list &x, bool squares, NormArgs args, double *run
     q.args = args;
     q.squares = squares;
     q.run = run;
+    // the launches' runs, one after another; then a place per launch for pieces
     double *piece = run + list_launches(x.count) * kListGrid;
     for (uint32_t k0 = 0; k0 < x.count; k0 += kListMax) {
         const uint32_t count = std::min(kListMax, x.count - k0);
@@ -558,13 +558,12 @@ int clip_part(const lct_list &x, const lct_list &y, uint32_t k0, uint32_t count,
     return p.list.chunks ? launch_list_clip(p, stream) : (int)hipSuccess;
 }
 
-// The clip's aliasing rules.  Every range sorted by its start; an overlap of
-// neighbours in that order (against the furthest end so far) is one of the
-// list's, and only x_k with y_k in place, or x with x, may be.
+// The clip's aliasing rules: with every range sorted by its start, none may
+// begin inside a written one before it, and a written one inside none.  In
+// place, x_k and y_k are one range; inputs may overlap each other.
 lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list &y) {
     struct Span {
         Range r;
-        uint32_t k;
         bool written;
     };
     try {
@@ -574,10 +573,10 @@ lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list
             if (x.n[k] == 0) continue;
             const Range rx = member(x, k), ry = member(y, k);
             const bool inplace = rx.lo == ry.lo && x.type[k] == y.type[k];
-            if (!inplace) v.push_back({rx, k, false});
-            v.push_back({ry, k, true});
+            if (!inplace) v.push_back({rx, false});
+            v.push_back({ry, true});
         }
-        v.push_back({rng(coef, 4), 0, false});
+        v.push_back({rng(coef, 4), false});
         std::sort(v.begin(), v.end(), [](const Span &a, const Span &b) { return a.r.lo < b.r.lo; });
         uintptr_t any = 0, written = 0;   // furthest end of all spans so far, of the written ones
         for (const Span &s : v) {
@@ -1216,7 +1215,7 @@ lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w
 // ---- norms and clipping
 
 lct_status lct_norm_scratch(uint32_t count, uint64_t nblk, uint64_t *bytes) {
-    if (!bytes || nblk > 0xFFFFFFFFull) return LCT_EINVAL;
+    if (!bytes || count > kListMaxCount || nblk > 0xFFFFFFFFull) return LCT_EINVAL;
     *bytes = norm_scratch_bytes(count, nblk);
     return LCT_OK;
 }

@@ -273,6 +273,7 @@ constexpr uint32_t kListGrid = 2048;      // workgroups per launch at most: eigh
 constexpr uint32_t kListTypeShift = 48;
 constexpr uint64_t kListElems = (1ull << kListTypeShift) - 1;
 constexpr uint64_t kListMaxElems = 1ull << 44;   // of a whole list: chunk numbers stay within 32 bits
+constexpr uint32_t kListMaxCount = 1u << 24;     // tensors of a list
 // Short lists in one launch: a workgroup of kOneThreads does every chunk of
 // 2^kOneShift elements, a wave each.
 constexpr uint32_t kOneThreads = 1024;

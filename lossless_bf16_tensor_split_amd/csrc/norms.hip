@@ -198,6 +198,10 @@ __device__ __forceinline__ uint32_t run_owner(uint32_t c, uint32_t chunks, uint3
 
 // ------------------------------------------------------------------ the list's norm
 
+// Bound by reading: 8 GB of BF16 in 398 tensors take 1.21 ms (6.6 TB/s, 83 % of
+// the memory's peak; a device copy reaches 4.8), 0.65 GB of FP32 105 us.  The
+// 64-bit conversions and products hide behind the loads.
+//
 // Each workgroup walks its run of chunks and leaves the run's value in
 // p.run[i]; where the tensors' own norms are wanted, the part of the run that
 // lies in tensor k goes to p.piece[i + k] (runs and tensors both ascend, so no
@@ -261,7 +265,9 @@ __global__ __launch_bounds__(1024) void k_list_finish(const ListFinishParams p) 
 }
 
 // A short list in one launch: every wave of a single workgroup takes chunks
-// in turn and leaves their values in LDS.
+// in turn and leaves their values in LDS.  Up to 64 chunks (131,072 elements):
+// there a call takes 7.4 us among others and 20 alone, in the two-launch form
+// 9.1 and 20; twice as many elements take 12.5 us in one workgroup.
 template <class A, uint32_t N>
 __global__ __launch_bounds__(kOneThreads) void k_list_one(const ListOneParams<N> p, bool squares) {
     __shared__ double vals[kOneMax];

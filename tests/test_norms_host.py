@@ -50,6 +50,7 @@ def test_scratch_grows_with_tensors_and_blocks(L):
     assert scratch(L, 0, 0xFFFFFFFF) >= 8 * 0xFFFFFFFF
     assert L.lib.lct_norm_scratch(1, 1 << 32, C.byref(C.c_uint64())) == L.EINVAL
     assert L.lib.lct_norm_scratch(1, 1, None) == L.EINVAL
+    assert L.lib.lct_norm_scratch((1 << 24) + 1, 0, C.byref(C.c_uint64())) == L.EINVAL
 
 
 class FakeList:
@@ -92,6 +93,10 @@ def test_list_norm_refusals(L):
     assert call(FakeList(L, [(1 << 44) + 1], [A], [0])) == L.EINVAL
     assert call(FakeList(L, [1 << 43, 1 << 43, 1], [A, A, A], [0, 0, 0])) == L.EINVAL
     assert call(FakeList(L, [(1 << 64) - 1, 1], [A, A], [0, 0])) == L.EINVAL
+    many = FakeList(L, [4], [A], [0])
+    for count in ((1 << 24) + 1, 0xFFFFFFFF):
+        many.s.count = count                 # refused before its arrays are read
+        assert call(many) == L.EINVAL
     assert call(FakeList(L, [4], [A + 1], [L.BF16])) == L.EALIGN
     assert call(FakeList(L, [4], [A + 2], [L.FP32])) == L.EALIGN
     # outputs and scratch on an input or each other
