@@ -938,6 +938,9 @@ def test_a_kept_descriptor_follows_its_buffers(L):
     t = L.encode(cb, x, L.layout(65536, 25))
     a = t.c()
     assert t.c() is a and t.c(need_scratch=False) is a
+    t.status.set_(torch.zeros(4, dtype=torch.int32, device="cuda"))      # the same tensor over other memory
+    assert t.c() is not a and t.c().status == t.status.data_ptr()
+    a = t.c()
     old = weakref.ref(t.scratch)
     t.scratch = torch.empty_like(t.scratch)
     assert old() is None
