@@ -1492,7 +1492,7 @@ __device__ __forceinline__ void norm_rest(const CodeNormParams &p, Reader &rd, u
     }
 }
 
-// A workgroup is a block.  At 4.02B elements the kernel takes 1.22 ms (4.6 TB/s
+// A workgroup is a block.  At 4.02B elements the kernel takes 1.24 ms (4.5 TB/s
 // of codes, where dense norms read 6.6): its lanes issue 9.3 vector
 // instructions a value, nine tenths of the cycles, and the decode table's reads
 // fill two thirds of the LDS's.  Squares in 64 bits all through take 6 % more,

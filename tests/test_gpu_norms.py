@@ -960,3 +960,34 @@ def test_a_kept_descriptor_follows_its_buffers(L):
     t.ovf_cap = t.ovf_cap * 2
     with pytest.raises(ValueError, match="ovf"):
         t.c()
+
+
+def test_offsets_past_32_bits(L):
+    """A tensor of more than 2^32 elements: the norm finds what lies at its far
+    end, the clip scales it there and nothing else."""
+    n = (1 << 32) + 70001
+    x = torch.zeros(n, dtype=BF, device="cuda")
+    at = torch.tensor([7, (1 << 32) + 5, n - 1], device="cuda")
+    x[at] = torch.tensor([12.0, 4.0, -3.0], dtype=BF, device="cuda")
+    lst = L.LctList([x[1:], x[:1]])
+    out = L.alloc_norm(2, True)
+    L.lct_list_norm(lst, out, 6.5)
+    torch.cuda.synchronize()
+    assert float(out.norm) == 13.0 and float(out.sum) == 169.0 and float(out.each[1]) == 0.0
+    L.lct_list_norm(lst, out, kind=L.NORM_MAX)
+    L.lct_list_clip(lst, torch.tensor(0.25, device="cuda"))
+    torch.cuda.synchronize()
+    assert float(out.norm) == 12.0
+    assert x[at].tolist() == [3.0, 1.0, -0.75]
+    L.lct_list_norm(lst, out)
+    torch.cuda.synchronize()
+    assert float(out.sum) == 9.0 + 1.0 + 0.5625
+    # FP32 to FP16 over the same border
+    del x, lst
+    y = torch.zeros((1 << 32) + 3, device="cuda")
+    y[-1] = 1.5
+    z = torch.empty(y.numel(), dtype=HF, device="cuda")
+    L.lct_list_clip(L.LctList([y]), torch.tensor(2.0, device="cuda"), L.LctList([z]))
+    torch.cuda.synchronize()
+    assert float(z[-1]) == 3.0 and float(z[-2]) == 0.0
+    assert float(L.grad_norm([z]).norm) == 3.0
