@@ -635,13 +635,15 @@ def _norm_scratch(count: int, nblk: int) -> int:
 
 class LctList:
     """Dense tensors (BF16, FP16 or FP32, contiguous, on one GPU) for
-    ``lct_list_norm`` and ``lct_list_clip``.  Keeps the tensors and the
-    addresses they have now; makes host arrays only, so a new list for tensors
-    that moved costs no device work."""
+    ``lct_list_norm`` and ``lct_list_clip``.  Keeps the memory that the tensors
+    have now: one that is given other memory later (``t.data = ...``) needs a
+    new list, and until then the calls work on what it had, which the list
+    holds.  Makes host arrays only, so a new list costs no device work."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
         count = len(self.tensors)
+        self.held = [t.untyped_storage() for t in self.tensors]
         self.device = None
         types = []
         for k, t in enumerate(self.tensors):

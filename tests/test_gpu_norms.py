@@ -991,3 +991,20 @@ def test_offsets_past_32_bits(L):
     torch.cuda.synchronize()
     assert float(z[-1]) == 3.0 and float(z[-2]) == 0.0
     assert float(L.grad_norm([z]).norm) == 3.0
+
+
+def test_a_list_holds_the_memory_it_was_made_for(L):
+    """A tensor that is given other memory after the list was made: the calls
+    reach neither that nor what is allocated next."""
+    x = torch.ones(1 << 20, device="cuda")
+    lst, old = L.LctList([x]), x.data_ptr()
+    x.data = torch.ones(1 << 20, device="cuda")
+    z = [torch.ones(1 << 20, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != old for t in z + [x])
+    L.lct_list_clip(lst, torch.tensor(0.5, device="cuda"))
+    out = L.alloc_norm(1)
+    L.lct_list_norm(lst, out)
+    assert out.sum.item() == (1 << 18)
+    assert all(bool((t == 1).all()) for t in z + [x])
+    L.lct_list_norm(L.LctList([x]), out)
+    assert out.sum.item() == (1 << 20)
