@@ -755,6 +755,7 @@ def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float =
     """Norm of a compressed group and of each member where out has room."""
     a = all_.c(need_scratch=False)
     _current(all_.sf.device, "the group")
+    _current(g.table.device, "the group's table")
     out._check(g.count, _norm_scratch(0, all_.sizes.nblk))
     _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, out.scratch_ptr, out.each_ptr,
                               out.buf_ptr, _stream(stream)), "lct_group_norm")
@@ -785,6 +786,17 @@ def _coef(coef) -> torch.Tensor:
     return coef
 
 
+def _step_coef(coef, *bufs) -> torch.Tensor:
+    """The coefficient, once it and a step's buffers (a tensor's stand for the
+    rest of it) are on the current device."""
+    coef = _coef(coef)
+    dev = coef.device
+    for b in bufs:
+        if b is not None and b.device != dev:
+            raise ValueError("a buffer of the step is on %s, the current device is %s" % (b.device, dev))
+    return coef
+
+
 def lct_list_clip(x: LctList, coef, y: LctList | None = None, stream=None) -> None:
     """y_k = coef * x_k (in place without y), rounded to y_k's type."""
     y = x if y is None else y
@@ -799,7 +811,7 @@ def lct_list_clip(x: LctList, coef, y: LctList | None = None, stream=None) -> No
 def lct_sgd_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m: LctTensor, eta: float, coef,
                       w_out: LctTensor, stream=None) -> None:
     """lct_sgd_step with M scaled by coef."""
-    coef = _coef(coef)
+    coef = _step_coef(coef, w_in.sf, m.sf, w_out.sf)
     a, b, o = w_in.c(), m.c(), w_out.c()
     _check(lib.lct_sgd_step_clip(C.byref(cw), C.byref(a), C.byref(cm), C.byref(b), eta, _ptr(coef), C.byref(o),
                                  _stream(stream)), "lct_sgd_step_clip")
@@ -808,7 +820,7 @@ def lct_sgd_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m: LctTensor,
 def lct_sgd_step_clip_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all: LctTensor, eta: float, coef,
                             w_out: LctTensor, stream=None) -> None:
     """lct_sgd_step_group with M scaled by coef."""
-    coef = _coef(coef)
+    coef = _step_coef(coef, gw.table, w_all.sf, gm.table, m_all.sf, w_out.sf)
     a, b, o = w_all.c(), m_all.c(), w_out.c()
     _check(lib.lct_sgd_step_clip_group(C.byref(gw.g), C.byref(a), C.byref(gm.g), C.byref(b), eta, _ptr(coef),
                                        C.byref(o), _stream(stream)), "lct_sgd_step_clip_group")
@@ -818,7 +830,7 @@ def lct_momentum_step_clip(cw: Codebook, w_in: LctTensor, cm: Codebook, m_in: Lc
                            mu: float, eta: float, w_out: LctTensor, m_out: LctTensor, stream=None) -> None:
     """lct_momentum_step with the gradient scaled by coef."""
     _gradient(g, w_in.n)
-    coef = _coef(coef)
+    coef = _step_coef(coef, w_in.sf, m_in.sf, g, w_out.sf, m_out.sf)
     a, b, ow, om = w_in.c(), m_in.c(), w_out.c(), m_out.c()
     _check(lib.lct_momentum_step_clip(C.byref(cw), C.byref(a), C.byref(cm), C.byref(b), _ptr(g), _ptr(coef), mu,
                                       eta, C.byref(ow), C.byref(om), _stream(stream)), "lct_momentum_step_clip")
@@ -828,7 +840,7 @@ def lct_momentum_step_clip_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m
                                  coef, mu: float, eta: float, w_out: LctTensor, m_out: LctTensor,
                                  stream=None) -> None:
     """lct_momentum_step_group with the gradients scaled by coef."""
-    coef = _coef(coef)
+    coef = _step_coef(coef, gw.table, w_all.sf, gm.table, m_all.sf, gg.table, w_out.sf, m_out.sf)
     a, b, ow, om = w_all.c(), m_all.c(), w_out.c(), m_out.c()
     _check(lib.lct_momentum_step_clip_group(C.byref(gw.g), C.byref(a), C.byref(gm.g), C.byref(b), C.byref(gg.g),
                                             _ptr(coef), mu, eta, C.byref(ow), C.byref(om), _stream(stream)),

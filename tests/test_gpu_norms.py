@@ -1008,3 +1008,40 @@ def test_a_list_holds_the_memory_it_was_made_for(L):
     assert all(bool((t == 1).all()) for t in z + [x])
     L.lct_list_norm(L.LctList([x]), out)
     assert out.sum.item() == (1 << 20)
+
+
+def test_clipped_steps_refuse_buffers_elsewhere(L):
+    """Every buffer that stands for a step's operand, on the CPU or absent from
+    the current device, is refused before a kernel could read it."""
+    lay = L.layout(4096, 12)
+    x = (0.02 * torch.randn(5000, device="cuda")).to(torch.bfloat16)
+    cb = L.lct_codebook_build(L.Model(L.GAUSSIAN, 0.02, 0.0), x)
+    t = [L.encode(cb, x, lay) for _ in range(4)]
+    c = torch.ones(1, device="cuda")
+    for k in range(4):
+        sf = t[k].sf
+        t[k].sf = sf.cpu()
+        with pytest.raises(ValueError):
+            L.lct_momentum_step_clip(cb, t[0], cb, t[1], x, c, 0.9, 0.1, t[2], t[3])
+        if k < 3:
+            with pytest.raises(ValueError):
+                L.lct_sgd_step_clip(cb, t[0], cb, t[1], 0.1, c, t[2])
+        t[k].sf = sf
+    with pytest.raises((ValueError, TypeError)):
+        L.lct_momentum_step_clip(cb, t[0], cb, t[1], x.cpu(), c, 0.9, 0.1, t[2], t[3])
+    with pytest.raises(ValueError):
+        L.lct_sgd_step_clip(cb, t[0], cb, t[1], 0.1, c.cpu(), t[2])
+    g = L.LctGroup([5000], lay, [cb], [x])
+    a, b, o = (g.alloc_storage(5000) for _ in range(3))
+    L.lct_encode_group(g, a)
+    L.lct_encode_group(g, b)
+    table = g.table
+    g.table = table.cpu()
+    with pytest.raises(ValueError, match="current device"):
+        L.lct_sgd_step_clip_group(g, a, g, b, 0.1, c, o)
+    with pytest.raises(ValueError, match="the group's table"):
+        L.lct_group_norm(g, a, L.alloc_norm(1, nblk=a.sizes.nblk))
+    g.table = table
+    L.lct_sgd_step_clip_group(g, a, g, b, 0.1, c, o)
+    torch.cuda.synchronize()
+    assert o.status_word() == 0
