@@ -643,7 +643,6 @@ class LctList:
     def __init__(self, tensors):
         self.tensors = list(tensors)
         count = len(self.tensors)
-        self.held = [t.untyped_storage() for t in self.tensors]
         self.device = None
         types = []
         for k, t in enumerate(self.tensors):
@@ -659,6 +658,7 @@ class LctList:
             elif t.device != self.device:
                 raise ValueError("tensor %d is on %s, tensor 0 on %s" % (k, t.device, self.device))
             types.append(ty)
+        self.held = [t.untyped_storage() for t in self.tensors]
         self.ns = (C.c_uint64 * count)(*[t.numel() for t in self.tensors])
         self.ptrs = (C.c_void_p * count)(*[t.data_ptr() for t in self.tensors])
         self.types = (C.c_int32 * count)(*types)
