@@ -677,25 +677,52 @@ class LctNorm:
     """A norm's result on the device (unset before the first call), and the
     working memory of the call.
 
-    ``sum`` (float64), ``norm`` and ``coef`` (float32) are 0-d views of one
-    buffer; ``each`` holds every tensor's norm, or is None.  ``scratch`` may be
-    replaced; it is checked when it is set and its size at every call."""
+    ``buf`` (16 bytes) is the result; ``sum`` (float64), ``norm`` and ``coef``
+    (float32) are its 0-d views.  ``each`` holds every tensor's norm, or is
+    None; it and ``scratch`` may be replaced.  A call writes to the memory that
+    they have when it is made, once it is found large enough.  Copies and
+    pickles have memory of their own."""
 
     def __init__(self, members: int, nblk: int, each: bool, device, scratch=None):
         dev = torch.device(device)
         if scratch is None:
             scratch = torch.empty(_norm_scratch(members, nblk), dtype=torch.uint8, device=dev)
         # (not filled: a call on another stream would race with that)
-        self.buf = torch.empty(16, dtype=torch.uint8, device=dev)
-        self.sum = self.buf[0:8].view(torch.float64)[0]
-        self.norm = self.buf[8:12].view(torch.float32)[0]
-        self.coef = self.buf[12:16].view(torch.float32)[0]
-        self.each = torch.empty(members, dtype=torch.float32, device=dev) if each else None
-        self.members = members
-        self.dev = self.buf.device.index
-        self.buf_ptr = self.buf.data_ptr()
-        self.each_ptr = self.each.data_ptr() if each else None
-        self.scratch = scratch
+        self._make(torch.empty(16, dtype=torch.uint8, device=dev),
+                   torch.empty(members, dtype=torch.float32, device=dev) if each else None, members, scratch)
+
+    def _make(self, buf, each, members, scratch):
+        self._buf, self._each, self._scratch, self.members = buf, each, scratch, members
+        self.dev = buf.device.index
+        self.sum = buf[0:8].view(torch.float64)[0]
+        self.norm = buf[8:12].view(torch.float32)[0]
+        self.coef = buf[12:16].view(torch.float32)[0]
+        self._buf_at, self._buf_held = buf.data_ptr(), buf.untyped_storage()
+        self._look()
+
+    def __getstate__(self):
+        return {"buf": self._buf, "each": self._each, "members": self.members, "scratch": self._scratch}
+
+    def __setstate__(self, state):
+        self._make(**state)
+
+    @property
+    def buf(self):
+        return self._buf
+
+    @property
+    def each(self):
+        return self._each
+
+    @each.setter
+    def each(self, t):
+        if t is not None:
+            if t.dtype != torch.float32 or t.dim() != 1:
+                raise TypeError("each must be a float32 vector or None")
+            self._bytes(t, "each")
+            self.members = t.numel()
+        self._each = t
+        self._look()
 
     @property
     def scratch(self):
@@ -703,21 +730,49 @@ class LctNorm:
 
     @scratch.setter
     def scratch(self, t):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("scratch must be a contiguous tensor on the GPU")
-        if t.device.index != self.dev:
-            raise ValueError("scratch is on %s, the result on cuda:%s" % (t.device, self.dev))
+        self._bytes(t, "scratch")
         self._scratch = t
-        self.scratch_ptr = t.data_ptr()
-        self.scratch_bytes = t.numel() * t.element_size()
+        self._look()
 
-    def _check(self, members: int, need: int) -> None:
-        """Fit for a norm of so many tensors that needs so much scratch."""
+    def _bytes(self, t, what: str) -> int:
+        """The bytes of memory behind a tensor that a call may write."""
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor on the GPU" % what)
+        if t.device.index != self.dev:
+            raise ValueError("%s is on %s, the result on cuda:%s" % (what, t.device, self.dev))
+        size = t.numel() * t.element_size()
+        if t.untyped_storage().nbytes() < t.storage_offset() * t.element_size() + size:
+            raise ValueError("the memory of %s was taken from it" % what)
+        return size
+
+    def _look(self) -> None:
+        """Take the addresses and sizes of each and scratch.  Their memory is
+        held with them: an address that a call finds unchanged is that memory
+        still."""
+        e, s = self._each, self._scratch
+        self._each_bytes = 0 if e is None else self._bytes(e, "each")
+        self._scratch_bytes = self._bytes(s, "scratch")
+        self._held = (None if e is None else e.untyped_storage(), s.untyped_storage())
+        self._at = (None if e is None else e.data_ptr(), s.data_ptr())
+
+    def _result(self) -> int:
+        """The result's address."""
         _current(self.dev, "the result")
-        if self.scratch_bytes < need:
-            raise ValueError("scratch holds %d bytes; the norm needs %d" % (self.scratch_bytes, need))
-        if self.each is not None and self.members != members:
-            raise ValueError("each has room for %d norms, the set has %d tensors" % (self.members, members))
+        if self._buf.data_ptr() != self._buf_at:
+            raise ValueError("buf has other memory than sum, norm and coef")
+        return self._buf_at
+
+    def _args(self, members: int, need: int):
+        """(scratch, each, result): addresses for a norm of so many tensors
+        that needs so much scratch, once all are found fit for it."""
+        res, e = self._result(), self._each
+        if self._at != (None if e is None else e.data_ptr(), self._scratch.data_ptr()):
+            self._look()                     # given other memory
+        if self._scratch_bytes < need:
+            raise ValueError("scratch holds %d bytes; the norm needs %d" % (self._scratch_bytes, need))
+        if e is not None and (self.members != members or self._each_bytes < 4 * members):
+            raise ValueError("each has room for %d norms, the set has %d tensors" % (self._each_bytes // 4, members))
+        return self._at[1], self._at[0], res
 
 
 def alloc_norm(members: int = 0, each: bool = False, nblk: int = 0, device="cuda", scratch=None) -> LctNorm:
@@ -733,9 +788,8 @@ def lct_list_norm(x: LctList, out: LctNorm, max_norm: float = float("inf"), scal
     room for them, and the coefficient that clips to max_norm."""
     if x.dev is not None:
         _current(x.dev, "the list")
-    out._check(x.count, x.need)
-    _check(lib.lct_list_norm(x.ref, kind, max_norm, scale, out.scratch_ptr, out.each_ptr, out.buf_ptr,
-                             _stream(stream)), "lct_list_norm")
+    scratch, each, res = out._args(x.count, x.need)
+    _check(lib.lct_list_norm(x.ref, kind, max_norm, scale, scratch, each, res, _stream(stream)), "lct_list_norm")
 
 
 def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
@@ -745,9 +799,9 @@ def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = 
     _current(t.sf.device, "the tensor")
     if out.each is not None:
         raise ValueError("each is for lists and groups")
-    out._check(1, _norm_scratch(0, t.sizes.nblk))
-    _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, out.scratch_ptr, out.buf_ptr,
-                               _stream(stream)), "lct_tensor_norm")
+    scratch, _, res = out._args(1, _norm_scratch(0, t.sizes.nblk))
+    _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, scratch, res, _stream(stream)),
+           "lct_tensor_norm")
 
 
 def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
@@ -756,9 +810,9 @@ def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float =
     a = all_.c(need_scratch=False)
     _current(all_.sf.device, "the group")
     _current(g.table.device, "the group's table")
-    out._check(g.count, _norm_scratch(0, all_.sizes.nblk))
-    _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, out.scratch_ptr, out.each_ptr,
-                              out.buf_ptr, _stream(stream)), "lct_group_norm")
+    scratch, each, res = out._args(g.count, _norm_scratch(0, all_.sizes.nblk))
+    _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, scratch, each, res, _stream(stream)),
+           "lct_group_norm")
 
 
 def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0, kind: int = NORM_L2,
@@ -771,8 +825,7 @@ def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: fl
     if parts.dtype != torch.uint8 or not parts.is_contiguous() or parts.numel() % 16:
         raise ValueError("parts must be a contiguous uint8 tensor of 16 bytes per result")
     _current(parts.device, "parts")
-    _current(out.buf.device, "buf")
-    _check(lib.lct_norm_join(_ptr(parts), parts.numel() // 16, kind, max_norm, scale, _ptr(out.buf),
+    _check(lib.lct_norm_join(_ptr(parts), parts.numel() // 16, kind, max_norm, scale, out._result(),
                              _stream(stream)), "lct_norm_join")
 
 
