@@ -341,6 +341,10 @@ class LctTensor:
                       self.ovf_cap, self.sizes, self.layout)
         return t
 
+    def __getstate__(self):
+        """Copies and pickles hold the buffers; a descriptor is made anew."""
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
     # host views (synchronise the current stream)
     def status_word(self) -> int:
         return int(self.status[0].item()) & 0xFFFFFFFF

@@ -174,3 +174,34 @@ def test_copies_of_a_result(L, calls, how):
     assert all((p != q) == own for p, q in zip(addresses(b), addresses(out)))
     b.buf.view(F32)[3] = 0.125                   # what a call would leave in coef
     assert float(b.coef) == 0.125 and (float(out.coef) == 0.125) == (not own)
+
+
+# ------------------------------------------------------------------ compressed tensors
+
+def coded(L, n=70000):
+    """A compressed tensor with made-up contents."""
+    t = L.alloc_tensor(n, L.layout(65536, 25), device="cpu")
+    for k, name in enumerate(("sf", "pay", "cnt", "obase", "ovf", "status", "scratch")):
+        b = getattr(t, name)
+        setattr(t, name, gpu(b.fill_(k)))
+    return t
+
+
+BUFFERS = ("sf", "pay", "cnt", "obase", "ovf", "status", "scratch")
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_copies_of_a_tensor_that_was_used(L, how):
+    """A tensor is copied and saved after a call as before its first one, and
+    the copy's descriptor is of the copy's buffers."""
+    t = coded(L)
+    a = t.c()
+    b = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda v: pickle.loads(pickle.dumps(v))}[how](t)
+    assert (b.n, b.ovf_cap) == (t.n, t.ovf_cap) and bytes(b.sizes) == bytes(t.sizes)
+    assert bytes(b.layout) == bytes(t.layout)
+    c = b.c()
+    for name in BUFFERS:
+        x, y = getattr(t, name), getattr(b, name)
+        assert torch.equal(x, y) and getattr(c, name) == y.data_ptr() and getattr(a, name) == x.data_ptr()
+        assert (x.data_ptr() == y.data_ptr()) == (how == "copy")
+    assert t.c() is a                            # the original's is kept still
