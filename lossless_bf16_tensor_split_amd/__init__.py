@@ -312,15 +312,17 @@ class LctTensor:
         """The C descriptor.  Every buffer must be a contiguous device tensor
         of at least the bytes lct_sizes gives (the library cannot see a
         buffer's size; a missing one is left to the call to refuse).  Kept
-        until a buffer is replaced or its memory moves: a step on a small
+        until a buffer is replaced, its memory or its size changes, or one of
+        the numbers does (the descriptor's own among them): a step on a small
         group would otherwise spend longer here than on the device."""
         bufs = (self.sf, self.pay, self.cnt, self.obase, self.ovf, self.status, self.scratch)
         kept = self.__dict__.get("_kept")
         if kept is not None:
-            refs, had_scratch, t, n, cap, sizes, lay = kept
+            refs, had_scratch, t, made, n, cap, sizes, lay = kept
             if ((had_scratch or not need_scratch) and n == self.n and cap == self.ovf_cap and sizes is self.sizes
-                    and lay is self.layout
-                    and all(r is None if b is None else r is not None and r[0]() is b and r[1] == b.data_ptr()
+                    and lay == bytes(self.layout) and made == bytes(t)
+                    and all(r is None if b is None
+                            else r is not None and r[0]() is b and r[1] == b.data_ptr() and r[2] == b.numel()
                             for r, b in zip(refs, bufs))):
                 return t
         sz = self.sizes
@@ -337,8 +339,8 @@ class LctTensor:
                     _ptr(self.obase), _ptr(self.ovf), self.ovf_cap, _ptr(self.status),
                     _ptr(self.scratch))
         # (weak references: a buffer that is replaced is not held)
-        self._kept = (tuple(b if b is None else (ref(b), b.data_ptr()) for b in bufs), need_scratch, t, self.n,
-                      self.ovf_cap, self.sizes, self.layout)
+        self._kept = (tuple(b if b is None else (ref(b), b.data_ptr(), b.numel()) for b in bufs), need_scratch, t,
+                      bytes(t), self.n, self.ovf_cap, self.sizes, bytes(self.layout))
         return t
 
     def __getstate__(self):

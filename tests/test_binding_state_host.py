@@ -205,3 +205,31 @@ def test_copies_of_a_tensor_that_was_used(L, how):
         assert torch.equal(x, y) and getattr(c, name) == y.data_ptr() and getattr(a, name) == x.data_ptr()
         assert (x.data_ptr() == y.data_ptr()) == (how == "copy")
     assert t.c() is a                            # the original's is kept still
+
+
+def test_a_kept_descriptor_follows_the_tensors_numbers(L):
+    """Changed in place, they reach the next call, as they did before
+    descriptors were kept; an edited descriptor is not given out again."""
+    t = coded(L)
+    a = t.c()
+    assert t.c() is a
+    t.layout.cap_words = 12
+    assert t.c().layout.cap_words == 12 and t.c() is t.c()
+    t.layout.block_elems = 32768
+    assert t.c().layout.block_elems == 32768
+    t.c().ovf_cap = 0
+    t.c().pay = None
+    assert t.c().ovf_cap == t.ovf_cap and t.c().pay == t.pay.data_ptr()
+
+
+def test_a_kept_descriptor_follows_the_sizes_of_buffers(L):
+    t = coded(L)
+    t.c()
+    t.sf.resize_(t.n - 1)                        # the same memory, shorter
+    with pytest.raises(ValueError, match="sf"):
+        t.c()
+    t = coded(L)
+    t.c()
+    t.pay.set_(gpu(t.pay[:-4].clone()))
+    with pytest.raises(ValueError, match="pay"):
+        t.c()
