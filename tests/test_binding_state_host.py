@@ -160,6 +160,7 @@ def test_copies_of_a_result(L, calls, how):
     """A deep copy or a pickle writes to its own memory, and its views show
     it; a shallow copy shares the tensors."""
     out = result(L, 3)
+    out.buf.zero_()                              # (a result is unset until its first call)
     out.norm.fill_(2.5)
     if how == "copy":
         b = copy.copy(out)
