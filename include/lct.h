@@ -464,7 +464,8 @@ lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all,
  * norm above; d_out: device, 8-byte aligned.  They only enqueue work on
  * `stream`.  Unlike the codec's calls they write their result for an empty
  * set too.  Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS (an output or the
- * scratch overlapping an input or each other), LCT_EARCH, LCT_EHIP. */
+ * scratch overlapping an input, which a group's device table is too, or each
+ * other), LCT_EARCH, LCT_EHIP. */
 typedef enum { LCT_NORM_L2 = 0, LCT_NORM_MAX = 1 } lct_norm_kind;
 typedef enum { LCT_BF16 = 0, LCT_FP16 = 1, LCT_FP32 = 2 } lct_dtype;
 

@@ -503,12 +503,11 @@ lct_status code_norm(CodeNormParams &p, const lct_tensor &t, uint64_t nb, const 
     const uint64_t scr = norm_scratch_bytes(0, nb);
     lct_status st = check_norm(kind, max_norm, scale, scratch, scr, each, count, out);
     if (st != LCT_OK) return st;
-    if (nb > 0) {
-        const Parts in = parts(t, nb);
-        if (overlaps_any(rng(scratch, scr), in, false) || overlaps_any(rng(out, sizeof *out), in, false) ||
-            overlaps_any(rng(each, each ? 4ull * count : 0), in, false))
-            return LCT_EALIAS;
-    }
+    // what is read: the codes, and a group's table (codebooks, members, blocks)
+    const Range table = g ? rng(g->d_table, group_table_layout(count, nb).bytes) : Range{0, 0};
+    const Range written[] = {rng(scratch, scr), rng(out, sizeof *out), rng(each, each ? 4ull * count : 0)};
+    for (const Range &r : written)
+        if ((nb > 0 && overlaps_any(r, parts(t, nb), false)) || overlap(r, table)) return LCT_EALIAS;
     st = check_arch();
     if (st != LCT_OK) return st;
     const bool squares = kind == LCT_NORM_L2;
