@@ -315,8 +315,7 @@ struct Reader {
     // returned, and a caller that gets more than 30 must decode the same
     // fields again with next().  q is kept at most qmax so that a bad group
     // never addresses past the stream's zero row.
-    // Without CLAMP the caller knows that all N fields are the stream's.
-    template <uint32_t N, bool CLAMP = true>
+    template <uint32_t N>
     __device__ __forceinline__ uint32_t next_n(uint32_t tab, int32_t qmax, uint32_t (&e23)[N]) {
         const uint32_t win = window();
         uint32_t c = 0;
@@ -327,7 +326,7 @@ struct Reader {
             e23[k] = (wk << (en & 31u)) | en;
             c += (en >> 8) & 0xFFu;
         }
-        q = CLAMP ? min(q + (int32_t)c, qmax) : q + (int32_t)c;
+        q = min(q + (int32_t)c, qmax);
         return c;
     }
 };
@@ -1449,7 +1448,7 @@ __device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t r
         for (uint32_t g = 0; g < CH; g += 4) {
             const int32_t q0 = rd.q;
             uint32_t e23[4];
-            const uint32_t c = rd.next_n<4, false>(kNormTab, qmax, e23);
+            const uint32_t c = rd.next_n<4>(kNormTab, qmax, e23);
             if (__builtin_expect(!wave_all(c <= 30), 0)) {
                 rd.q = q0;
 #pragma unroll
