@@ -451,8 +451,7 @@ lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all,
  *   LCT_NORM_MAX:  S = largest |x|,         norm = |s| * S
  *   coef = s * min(1, max_norm / (norm + 1e-6))
  * S is summed and the rest computed in 64 bits; norm and coef are rounded to
- * fp32 once.  (Of a compressed tensor, the squares of 16 values are summed in
- * fp32 first, which leaves S within 15 * 2^-24 of itself.)  Equal calls give equal bits.  A NaN element makes norm and coef
+ * fp32 once.  Equal calls give equal bits.  A NaN element makes norm and coef
  * NaN, an infinite one makes norm infinite and coef 0 (NaN when max_norm is
  * infinite too).  An empty set has S = 0, norm 0.  max_norm = INFINITY with
  * finite elements gives coef = s.

@@ -1369,7 +1369,7 @@ template <bool SQ>
 struct CodeAcc {
     double s = 0.0;
     uint32_t m = 0;
-    // the value's fp32 bits
+    // f: the value's fp32 bits
     __device__ __forceinline__ void add(uint32_t f) {
         if (SQ) {
             const double d = (double)__uint_as_float(f);
@@ -1377,29 +1377,6 @@ struct CodeAcc {
         } else {
             m = max(m, f & 0x7FFF0000u);
         }
-    }
-    // A step's CH values.  Their squares are summed in fp32 first and the sum
-    // joined in 64 bits: each square has 16 significant bits, so the sum is
-    // off by 15 * 2^-24 of itself at most (the conversions to 64 bits, at a
-    // quarter of the rate of the other instructions, are a third of the time
-    // otherwise).  A sum in [2^-96, 2^127) lost nothing to underflow (a
-    // square below 2^-126 is less than 2^-30 of it) or overflow; any other,
-    // zero and NaN included, is made again in 64 bits.
-    __device__ __forceinline__ void add_step(const uint32_t (&f)[CH]) {
-        if (!SQ) {
-#pragma unroll
-            for (uint32_t i = 0; i < CH; ++i) add(f[i]);
-            return;
-        }
-        float t = 0.0f;
-#pragma unroll
-        for (uint32_t i = 0; i < CH; ++i) t = __builtin_fmaf(__uint_as_float(f[i]), __uint_as_float(f[i]), t);
-        if (__builtin_expect(wave_all(t >= 0x1p-96f && t < 0x1p127f), 1)) {
-            s += (double)t;
-            return;
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < CH; ++i) add(f[i]);
     }
 };
 
@@ -1461,7 +1438,8 @@ __device__ __forceinline__ void norm_halves(Reader &rd, uint32_t cap, uint32_t r
             for (uint32_t k = 0; k < 4; ++k)
                 f[g + k] = join32s(w[g / 8][g / 4 % 2], e23[k], byte_sel(k));
         }
-        acc.add_step(f);
+#pragma unroll
+        for (uint32_t i = 0; i < CH; ++i) acc.add(f[i]);
     }
 }
 
@@ -1491,13 +1469,14 @@ __device__ __forceinline__ void norm_rest(const CodeNormParams &p, Reader &rd, u
     }
 }
 
-// A workgroup is a block.  At 4.02B elements the kernel takes 1.24 ms (4.5 TB/s
-// of codes, where dense norms read 6.6): its lanes issue 9.3 vector
-// instructions a value, nine tenths of the cycles, and the decode table's reads
-// fill two thirds of the LDS's.  Squares in 64 bits all through take 6 % more,
-// four workgroups per CU (larger LDS rows) 5 %, a word read per value and
-// sign-fraction byte 5 %.  Few blocks are bound by one stream's chain of
-// lookups (18 us for 256 positions).
+// A workgroup is a block.  At 4.02B elements the kernel takes 1.30 ms (4.3 TB/s
+// of codes, where dense norms read 6.6), bound by issue: a value takes some
+// nine vector instructions beside its square's conversion to 64 bits, and the
+// decode table's reads fill two thirds of the LDS's cycles.  Sixteen squares
+// summed in fp32 before they go on in 64 bits take 1.21 ms, but leave the sum
+// with 24 bits.  Four workgroups per CU (larger LDS rows) take 5 % more, a word
+// read per value and sign-fraction byte 5 %.  Few blocks are bound by one
+// stream's chain of lookups (18 us for 256 positions).
 template <uint32_t CAPT, bool GROUP, bool SQ>
 __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p) {
     const uint32_t b = blockIdx.x, h = wave_id();   // a workgroup is a block's four units

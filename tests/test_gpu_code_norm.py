@@ -53,3 +53,31 @@ def test_a_tensor_read_with_another_codebook(L, lay):
     assert code_norm(L, other, t, L.NORM_MAX) == np.abs(y).max()
     # and its own codebook still reads the tensor
     assert code_norm(L, own, t, L.NORM_MAX) == np.abs(values(x)).max()
+
+
+@pytest.mark.parametrize("lay,heavy", [((65536, 25), False), ((32768, 12), True), ((32768, 11), True),
+                                       ((4096, 2), False)])
+def test_sums_hold_64_bits(L, lay, heavy):
+    """S is summed in 64 bits from the first square on: a square is exact (16
+    significant bits), and an addition is off by 2^-53 of a partial sum that
+    is at most S.  On its way a square meets one addition for each later
+    position of its stream, six joins of the lanes, three of a block's waves
+    and six of the blocks' values (38 blocks: one wave; the other waves' zeros
+    add exactly)."""
+    n = 37 * lay[0] + 1001
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, generator=g) * 0.02
+    if heavy:                                    # many fields spill
+        x *= torch.exp2(torch.randint(-20, 8, (n,), generator=g).float())
+    x = x.to(BF).cuda()
+    cb = L.lct_codebook_build(L.Model(L.GAUSSIAN, 0.02, 0.0), x)
+    t = L.encode(cb, x, L.layout(*lay))
+    if heavy:
+        assert t.spilled() > 0
+    v = values(x).astype(np.longdouble)
+    want = (v * v).sum()
+    adds = lay[0] // 256 + 6 + 3 + 6
+    assert abs(code_norm(L, cb, t, L.NORM_L2) - want) <= want * adds * 2.0 ** -53
+    # dense, of the same values: the two sums differ by their order only
+    out = L.grad_norm([x])
+    assert abs(float(out.sum) - want) <= want * (n + 64) * 2.0 ** -53
