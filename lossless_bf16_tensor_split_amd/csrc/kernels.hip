@@ -784,9 +784,16 @@ __device__ __forceinline__ void place_unit(const OutSide &d, const UnitRec &r, u
         const uint64_t at = u / kMaxUnits * NS + (u % kMaxUnits) * US;
         d.cnt[at + l] = parked_cnt[at + l];
     }
-    const uint8_t *stage2 = d.scratch + scr_stage2_offset(nblk, d.ovf_cap);
-    for (uint64_t i = l; i < r.total; i += 64)
-        if (r.base + i < d.ovf_cap && to + i < d.ovf_cap) d.ovf[to + i] = stage2[r.base + i];
+    if (r.total == 0) return;
+    // The bytes that both the staging area and the region have room for, so that
+    // the loop tests nothing else and reads no argument (131M elements with 76 MB
+    // of spills: an encode of 483 us; with both tests and the region's address
+    // read at every step 508).
+    const uint64_t past = max(r.base, to), room = d.ovf_cap - min(d.ovf_cap, past);
+    const uint32_t m = (uint32_t)min<uint64_t>(r.total, room);
+    const uint8_t *from = d.scratch + scr_stage2_offset(nblk, d.ovf_cap) + r.base;
+    uint8_t *out = d.ovf + to;
+    for (uint32_t i = l; i < m; i += 64) out[i] = from[i];
 }
 
 // Overflow offsets: an exclusive scan of the blocks' spill totals, one block
@@ -831,7 +838,7 @@ __global__ __launch_bounds__(kScanGroup) void k_scan(const OutSides o) {
 // round-robin; nothing to do (no spills, nothing parked) ends every wave at
 // once.
 __global__ __launch_bounds__(256) void k_place(const OutSides o) {
-    const OutSide &d = o.side[blockIdx.y];
+    const OutSide d = o.side[blockIdx.y];
     const uint64_t nblk = o.nblk;
     const uint32_t parked = *reinterpret_cast<const uint32_t *>(d.scratch + kScrParked);
     if (d.obase[nblk] == 0 && parked == 0) return;
@@ -840,9 +847,11 @@ __global__ __launch_bounds__(256) void k_place(const OutSides o) {
     for (uint64_t u = (uint64_t)blockIdx.x * 4 + wave_id(); u < nunits; u += (uint64_t)gridDim.x * 4) {
         const UnitRec r = rec[u];
         const uint64_t b = u / kMaxUnits;
-        uint64_t to = d.obase[b];
-        if (r.total)
+        uint64_t to = 0;
+        if (r.total) {
+            to = d.obase[b];
             for (uint64_t v = b * kMaxUnits; v < u; ++v) to += rec[v].total;
+        }
         place_unit(d, r, u, nblk, to);
     }
 }
