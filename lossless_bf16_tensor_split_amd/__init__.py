@@ -618,6 +618,7 @@ def lct_momentum_step_group(gw: LctGroup, w_all: LctTensor, gm: LctGroup, m_all:
 
 # ------------------------------------------------------------------ norms and clipping
 
+_KINDS = {NORM_L2: "an L2 norm", NORM_MAX: "a largest magnitude"}
 _LIST_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 
 
@@ -686,8 +687,9 @@ class LctNorm:
     ``buf`` (16 bytes) is the result; ``sum`` (float64), ``norm`` and ``coef``
     (float32) are its 0-d views.  ``each`` holds every tensor's norm, or is
     None; it and ``scratch`` may be replaced.  A call writes to the memory that
-    they have when it is made, once it is found large enough.  Copies and
-    pickles have memory of their own."""
+    they have when it is made, once it is found large enough.  ``kind`` is the
+    last call's (None before the first).  Copies and pickles have memory of
+    their own."""
 
     def __init__(self, members: int, nblk: int, each: bool, device, scratch=None):
         dev = torch.device(device)
@@ -695,10 +697,10 @@ class LctNorm:
             scratch = torch.empty(_norm_scratch(members, nblk), dtype=torch.uint8, device=dev)
         # (not filled: a call on another stream would race with that)
         self._make(torch.empty(16, dtype=torch.uint8, device=dev),
-                   torch.empty(members, dtype=torch.float32, device=dev) if each else None, members, scratch)
+                   torch.empty(members, dtype=torch.float32, device=dev) if each else None, members, scratch, None)
 
-    def _make(self, buf, each, members, scratch):
-        self._buf, self._each, self._scratch, self.members = buf, each, scratch, members
+    def _make(self, buf, each, members, scratch, kind):
+        self._buf, self._each, self._scratch, self.members, self.kind = buf, each, scratch, members, kind
         self.dev = buf.device.index
         self.sum = buf[0:8].view(torch.float64)[0]
         self.norm = buf[8:12].view(torch.float32)[0]
@@ -707,7 +709,8 @@ class LctNorm:
         self._look()
 
     def __getstate__(self):
-        return {"buf": self._buf, "each": self._each, "members": self.members, "scratch": self._scratch}
+        return {"buf": self._buf, "each": self._each, "members": self.members, "scratch": self._scratch,
+                "kind": self.kind}
 
     def __setstate__(self, state):
         self._make(**state)
@@ -796,6 +799,7 @@ def lct_list_norm(x: LctList, out: LctNorm, max_norm: float = float("inf"), scal
         _current(x.dev, "the list")
     scratch, each, res = out._args(x.count, x.need)
     _check(lib.lct_list_norm(x.ref, kind, max_norm, scale, scratch, each, res, _stream(stream)), "lct_list_norm")
+    out.kind = kind
 
 
 def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
@@ -808,6 +812,7 @@ def lct_tensor_norm(cb: Codebook, t: LctTensor, out: LctNorm, max_norm: float = 
     scratch, _, res = out._args(1, _norm_scratch(0, t.sizes.nblk))
     _check(lib.lct_tensor_norm(C.byref(cb), C.byref(ct), kind, max_norm, scale, scratch, res, _stream(stream)),
            "lct_tensor_norm")
+    out.kind = kind
 
 
 def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0,
@@ -819,13 +824,18 @@ def lct_group_norm(g: LctGroup, all_: LctTensor, out: LctNorm, max_norm: float =
     scratch, each, res = out._args(g.count, _norm_scratch(0, all_.sizes.nblk))
     _check(lib.lct_group_norm(C.byref(g.g), C.byref(a), kind, max_norm, scale, scratch, each, res, _stream(stream)),
            "lct_group_norm")
+    out.kind = kind
 
 
 def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: float = 1.0, kind: int = NORM_L2,
                   stream=None) -> None:
-    """Norm of the union of the sets behind several results: a sequence of
-    LctNorm, or their ``buf`` bytes gathered in one uint8 tensor [k, 16]."""
+    """Norm of the union of the sets behind several results of this kind: a
+    sequence of LctNorm, or their ``buf`` bytes gathered in one uint8 tensor
+    [k, 16] (whose kinds cannot be seen any more)."""
     if not torch.is_tensor(parts):
+        for k, p in enumerate(parts):
+            if p.kind is not None and p.kind != kind:
+                raise ValueError("part %d is %s, joined as %s" % (k, _KINDS[p.kind], _KINDS.get(kind, kind)))
         with torch.cuda.stream(stream):      # gathered where they are joined
             parts = torch.stack([p.buf for p in parts]) if len(parts) else out.buf[:0]
     if parts.dtype != torch.uint8 or not parts.is_contiguous() or parts.numel() % 16:
@@ -833,6 +843,7 @@ def lct_norm_join(parts, out: LctNorm, max_norm: float = float("inf"), scale: fl
     _current(parts.device, "parts")
     _check(lib.lct_norm_join(_ptr(parts), parts.numel() // 16, kind, max_norm, scale, out._result(),
                              _stream(stream)), "lct_norm_join")
+    out.kind = kind
 
 
 def _coef(coef) -> torch.Tensor:

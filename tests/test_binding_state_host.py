@@ -177,6 +177,25 @@ def test_copies_of_a_result(L, calls, how):
     assert float(b.coef) == 0.125 and (float(out.coef) == 0.125) == (not own)
 
 
+def test_results_of_another_kind_are_not_joined(L, calls, monkeypatch):
+    """A sum of squares and a largest magnitude have no norm together."""
+    joined = []
+    monkeypatch.setattr(L.lib, "lct_norm_join", lambda parts, count, kind, *a: joined.append((count, kind)) or 0)
+    a, b, c = result(L, 3), result(L, 3), result(L, 3)
+    L.lct_list_norm(listed(L, 3), a, kind=L.NORM_L2)
+    L.lct_list_norm(listed(L, 3), b, kind=L.NORM_MAX)
+    assert (a.kind, b.kind, c.kind) == (L.NORM_L2, L.NORM_MAX, None)
+    for parts, kind in (((a, b), L.NORM_L2), ((a, b), L.NORM_MAX), ((a,), L.NORM_MAX), ((c, b), L.NORM_L2)):
+        with pytest.raises(ValueError, match="part"):
+            L.lct_norm_join(parts, result(L, 0), kind=kind)
+    assert not joined
+    out = result(L, 0)
+    L.lct_norm_join([a, copy.deepcopy(a), c], out)       # (c was filled by other means)
+    L.lct_norm_join([b], out, kind=L.NORM_MAX)
+    L.lct_norm_join(torch.zeros(2, 16, dtype=U8), out)
+    assert joined == [(3, L.NORM_L2), (1, L.NORM_MAX), (2, L.NORM_L2)] and out.kind == L.NORM_L2
+
+
 # ------------------------------------------------------------------ compressed tensors
 
 def coded(L, n=70000):
