@@ -320,11 +320,15 @@ class LctTensor:
         if kept is not None:
             refs, had_scratch, t, made, n, cap, sizes, lay = kept
             if ((had_scratch or not need_scratch) and n == self.n and cap == self.ovf_cap and sizes is self.sizes
-                    and lay == bytes(self.layout) and made == bytes(t)
-                    and all(r is None if b is None
-                            else r is not None and r[0]() is b and r[1] == b.data_ptr() and r[2] == b.numel()
-                            for r, b in zip(refs, bufs))):
-                return t
+                    and lay == bytes(self.layout) and made == bytes(t)):
+                for b, (r, at, numel) in zip(bufs, refs):
+                    if b is None or r is None:
+                        if b is not r:           # one of them is not missing
+                            break
+                    elif r() is not b or at != b.data_ptr() or numel != b.numel():
+                        break
+                else:
+                    return t
         sz = self.sizes
         for name, need in (("sf", sz.sf), ("pay", sz.pay), ("cnt", sz.cnt), ("obase", sz.obase),
                            ("ovf", self.ovf_cap), ("status", 4), ("scratch", sz.scratch if need_scratch else 0)):
@@ -339,8 +343,8 @@ class LctTensor:
                     _ptr(self.obase), _ptr(self.ovf), self.ovf_cap, _ptr(self.status),
                     _ptr(self.scratch))
         # (weak references: a buffer that is replaced is not held)
-        self._kept = (tuple(b if b is None else (ref(b), b.data_ptr(), b.numel()) for b in bufs), need_scratch, t,
-                      bytes(t), self.n, self.ovf_cap, self.sizes, bytes(self.layout))
+        self._kept = (tuple((None, 0, 0) if b is None else (ref(b), b.data_ptr(), b.numel()) for b in bufs),
+                      need_scratch, t, bytes(t), self.n, self.ovf_cap, self.sizes, bytes(self.layout))
         return t
 
     def __getstate__(self):
@@ -797,9 +801,9 @@ def lct_list_norm(x: LctList, out: LctNorm, max_norm: float = float("inf"), scal
                   kind: int = NORM_L2, stream=None) -> None:
     """Norm of the list's tensors (times scale), each tensor's where out has
     room for them, and the coefficient that clips to max_norm."""
-    if x.dev is not None:
+    if x.dev != out.dev and x.dev is not None:
         _current(x.dev, "the list")
-    scratch, each, res = out._args(x.count, x.need)
+    scratch, each, res = out._args(x.count, x.need)      # (the result is on the current device)
     _check(lib.lct_list_norm(x.ref, kind, max_norm, scale, scratch, each, res, _stream(stream)), "lct_list_norm")
     out.kind = kind
 

@@ -253,3 +253,17 @@ def test_a_kept_descriptor_follows_the_sizes_of_buffers(L):
     t.pay.set_(gpu(t.pay[:-4].clone()))
     with pytest.raises(ValueError, match="pay"):
         t.c()
+
+
+def test_a_kept_descriptor_follows_replaced_and_missing_buffers(L):
+    t = coded(L)
+    for name in ("status", "scratch", "ovf"):
+        old = getattr(t, name)
+        assert getattr(t.c(), name) == old.data_ptr()
+        setattr(t, name, gpu(old.clone()))
+        assert getattr(t.c(), name) == getattr(t, name).data_ptr() != old.data_ptr()
+        del old
+        setattr(t, name, None)                   # (the last reference to it)
+        assert getattr(t.c(), name) is None and t.c() is t.c()
+        setattr(t, name, gpu(torch.zeros(t.sizes.scratch + t.ovf_cap, dtype=U8)))
+        assert getattr(t.c(), name) == getattr(t, name).data_ptr()
