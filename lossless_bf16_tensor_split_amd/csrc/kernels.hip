@@ -1478,14 +1478,14 @@ __device__ __forceinline__ void norm_rest(const CodeNormParams &p, Reader &rd, u
     }
 }
 
-// A workgroup is a block.  At 4.02B elements the kernel takes 1.30 ms (4.3 TB/s
-// of codes, where dense norms read 6.6), bound by issue: a value takes some
-// nine vector instructions beside its square's conversion to 64 bits, and the
-// decode table's reads fill two thirds of the LDS's cycles.  Sixteen squares
-// summed in fp32 before they go on in 64 bits take 1.21 ms, but leave the sum
-// with 24 bits.  Four workgroups per CU (larger LDS rows) take 5 % more, a word
-// read per value and sign-fraction byte 5 %.  Few blocks are bound by one
-// stream's chain of lookups (18 us for 256 positions).
+// A workgroup is a block.  A pass over 4.02B elements takes 1.30 ms (4.3 TB/s of
+// codes, where dense norms read 6.6; 1.38 on a slower card): 10.2 vector
+// instructions a value are nine tenths of the cycles, and the decode table's
+// reads fill two thirds of the LDS's.  Sixteen squares summed in fp32 before
+// they go on in 64 bits take 1.21 ms on the first card, but leave the sum with
+// 24 bits; four workgroups per CU (larger LDS rows) take 5 % more, a word read
+// per value and sign-fraction byte 5 %.  Few blocks are bound by one stream's
+// chain of lookups (18 us for 256 positions; the waves wait six tenths of it).
 template <uint32_t CAPT, bool GROUP, bool SQ>
 __global__ __launch_bounds__(64 * kDecWaves) void k_norm(const CodeNormParams p) {
     const uint32_t b = blockIdx.x, h = wave_id();   // a workgroup is a block's four units
