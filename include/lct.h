@@ -441,9 +441,10 @@ lct_status lct_momentum_step_group(const lct_group *gw, const lct_tensor *w_all,
 
 /* ---- norms and clipping ----------------------------------------------------
  * The global norm of a step's gradients, the coefficient that clips them to a
- * largest norm, and the ways to apply it, so that a step with clipping never
- * waits for the host: the norm calls leave their result in device memory, and
- * the clip and the clipped steps read the coefficient from there.
+ * largest norm, and the ways to apply it, without a wait for the host between
+ * them: the norm calls leave their result in device memory, and the clip and
+ * the clipped steps read the coefficient from there.  (Gradients of a group's
+ * momentum step that have moved need a new lct_group_bind, which does wait.)
  *
  * With x the elements of every tensor of a set and s the scale (the gradients
  * stand for s * x: 1 / loss scale, or 1 / accumulated batches):
@@ -506,8 +507,9 @@ lct_status lct_tensor_norm(const lct_codebook *cb, const lct_tensor *t, int32_t 
 lct_status lct_group_norm(const lct_group *g, const lct_tensor *all, int32_t kind, double max_norm,
                           double scale, void *d_scratch, float *d_each, lct_norm_t *d_out, void *stream);
 
-/* The norm of the union of the sets behind `count` results (their sums, of
- * the same kind): other ranks' gathered results, or a list's and a group's.
+/* The norm of the union of the sets behind `count` results (their sums, all of
+ * this kind, which a result does not hold and the call cannot check): other
+ * ranks' gathered results, or a list's and a group's.
  * d_out may be one of d_parts. */
 lct_status lct_norm_join(const lct_norm_t *d_parts, uint32_t count, int32_t kind, double max_norm,
                          double scale, lct_norm_t *d_out, void *stream);
