@@ -547,6 +547,35 @@ lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w
                                         float mu, float eta, const lct_tensor *w_out,
                                         const lct_tensor *m_out, void *stream);
 
+/* ---- orthogonalised updates -------------------------------------------------
+ * Newton-Schulz orthogonalisation of many matrices, as optimisers use it on a
+ * matrix's momentum: with X0 = x / (|x| + 1e-7) (the root of the sum of
+ * squares), `steps` times
+ *     A = X X',  B = b A + c A A,  X <- a X + B X
+ * (a matrix with more rows than columns is taken transposed), and y = s * X,
+ * rounded to BF16.  coef = {a, b, c}; s is the matrix's own factor.
+ *
+ * x: matrices as a list, of any lct_dtype; matrix k has rows[k] rows and n[k] /
+ * rows[k] columns, its elements row by row, at most 2^24 of either and 2^32
+ * elements (n[k] = 0: nothing is done).  y: a list of the same sizes, all BF16;
+ * y_k is x_k (same memory, BF16: in place) or overlaps no tensor of x, and no
+ * other of y.  scale: host array of a factor per matrix (null: 1).  steps 1..32.  The
+ * products are computed from FP16 numbers held in pairs where one would lose
+ * too much; the coefficients must keep every iterate's singular values below
+ * 1.9 (and those of B below 7.8) for starting values in [0, 1], which the call
+ * checks: (3.4445, -4.775, 2.0315) and (15, -10, 3) / 8 do.  A matrix whose norm
+ * is not finite in FP32 gives NaN, a matrix of zeros zeros.  Equal calls give
+ * equal bits.
+ * d_scratch: device working memory of lct_orthogonal_scratch() bytes (256-byte
+ * aligned), overlapping no tensor, shared only by calls that do not overlap in
+ * time.  Long lists are done in batches of consecutive matrices, whose memory
+ * it holds at a time: about 8 bytes per element of the largest batch (sides
+ * rounded up to whole tiles).  Enqueues only.  Errors: LCT_EINVAL, LCT_EALIGN,
+ * LCT_EALIAS, LCT_EARCH, LCT_EHIP. */
+lct_status lct_orthogonal_scratch(const lct_list *x, const uint64_t *rows, uint64_t *bytes);
+lct_status lct_list_orthogonalize(const lct_list *x, const uint64_t *rows, const lct_list *y, uint32_t steps,
+                                  const float coef[3], const float *scale, void *d_scratch, void *stream);
+
 /* Message for a status code (static string). */
 const char *lct_strerror(lct_status st);
 /* Text of the last HIP error seen on this thread (static per thread). */

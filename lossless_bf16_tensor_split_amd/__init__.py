@@ -64,6 +64,7 @@ EXPORTED = ["lct_layout_init", "lct_sizes", "lct_codebook_build", "lct_codebook_
             "lct_encode_group", "lct_decode_group", "lct_sgd_step_group", "lct_momentum_step_group",
             "lct_norm_scratch", "lct_list_norm", "lct_tensor_norm", "lct_group_norm", "lct_norm_join", "lct_list_clip",
             "lct_sgd_step_clip", "lct_sgd_step_clip_group", "lct_momentum_step_clip", "lct_momentum_step_clip_group",
+            "lct_orthogonal_scratch", "lct_list_orthogonalize",
             "lct_strerror", "lct_last_hip_error"]
 
 
@@ -156,6 +157,8 @@ def _load():
     L.lct_sgd_step_clip_group.argtypes = [G, T, G, T, f32, P, T, P]
     L.lct_momentum_step_clip.argtypes = [CB, T, CB, T, P, P, f32, f32, T, T, P]
     L.lct_momentum_step_clip_group.argtypes = [G, T, G, T, G, P, f32, f32, T, T, P]
+    L.lct_orthogonal_scratch.argtypes = [LI, P, C.POINTER(u64)]
+    L.lct_list_orthogonalize.argtypes = [LI, P, LI, C.c_uint32, P, P, P, P]
     L.lct_strerror.restype = C.c_char_p
     L.lct_strerror.argtypes = [i32]
     L.lct_last_hip_error.restype = C.c_char_p
@@ -938,4 +941,85 @@ def clip_grad_norm(tensors, max_norm: float, scale: float = 1.0, kind: int = NOR
     x = tensors if isinstance(tensors, LctList) else LctList(tensors)
     out = grad_norm(x, max_norm, scale, kind)
     lct_list_clip(x, out)
+    return out
+
+
+# ------------------------------------------------------------------ orthogonalised updates
+
+# the usual quintic's coefficients: a steep start, values near one after five steps
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+class LctMatrices(LctList):
+    """Dense matrices for ``lct_list_orthogonalize``: a list whose tensors have
+    two dimensions, or more (every matrix of the last two counts by itself, as
+    stacked experts' weights do).  Keeps the tensors' memory as a list does."""
+
+    def __init__(self, tensors):
+        mats = []
+        for k, t in enumerate(tensors):
+            if t.dim() < 2:
+                raise ValueError("tensor %d has %d dimensions; matrices have two or more" % (k, t.dim()))
+            if t.dim() == 2:
+                mats.append(t)
+            else:
+                if not t.is_contiguous():
+                    raise ValueError("tensor %d must be contiguous" % k)
+                mats.extend(t.view(-1, t.shape[-2], t.shape[-1]).unbind(0) if t.numel() else [])
+        super().__init__(mats)
+        self.shapes = [tuple(t.shape) for t in self.tensors]
+        self.rows = (C.c_uint64 * self.count)(*[r for r, _ in self.shapes])
+
+
+class OrthoWork:
+    """Working memory of ``lct_list_orthogonalize`` (kept between calls; shared
+    only by calls that do not overlap in time)."""
+
+    def __init__(self, scratch: torch.Tensor):
+        self.scratch = scratch
+
+
+def alloc_orthogonal(x: LctMatrices) -> OrthoWork:
+    """Working memory for matrices of x's shapes."""
+    need = C.c_uint64(0)
+    _check(lib.lct_orthogonal_scratch(x.ref, x.rows, C.byref(need)), "lct_orthogonal_scratch")
+    return OrthoWork(torch.empty(max(int(need.value), 256), dtype=torch.uint8, device=x.device or "cuda"))
+
+
+def lct_list_orthogonalize(x: LctMatrices, y: LctMatrices, work: OrthoWork, steps: int = 5, coef=NEWTON_SCHULZ,
+                           scale=None, stream=None) -> None:
+    """y_k = s_k * (x_k with its singular values driven towards one); scale: a
+    number, or one per matrix."""
+    if x.shapes != y.shapes:
+        raise ValueError("the lists' matrices have other shapes")
+    if len(coef) != 3:
+        raise ValueError("coef holds three numbers")
+    if scale is not None:
+        scale = [float(scale)] * x.count if isinstance(scale, (int, float)) else [float(v) for v in scale]
+        if len(scale) != x.count:
+            raise ValueError("%d factors for %d matrices" % (len(scale), x.count))
+        scale = (C.c_float * x.count)(*scale)
+    if not 0 <= steps < 2 ** 32:
+        raise ValueError("steps must be 1 to 32")
+    if x.dev is not None:
+        _current(x.dev, "the list")
+    if y.dev is not None:
+        _current(y.dev, "the output list")
+    scr = work.scratch
+    _current(scr.device, "the working memory")
+    need = C.c_uint64(0)
+    _check(lib.lct_orthogonal_scratch(x.ref, x.rows, C.byref(need)), "lct_orthogonal_scratch")
+    if not scr.is_contiguous() or scr.numel() * scr.element_size() < need.value:
+        raise ValueError("the working memory holds %d bytes; the matrices need %d"
+                         % (scr.numel() * scr.element_size(), need.value))
+    _check(lib.lct_list_orthogonalize(x.ref, x.rows, y.ref, steps, (C.c_float * 3)(*coef), scale, _ptr(scr),
+                                      _stream(stream)), "lct_list_orthogonalize")
+
+
+def orthogonalize(tensors, steps: int = 5, coef=NEWTON_SCHULZ, scale=None):
+    """Orthogonalised matrices, as new BF16 tensors of the same shapes."""
+    tensors = list(tensors)
+    x = LctMatrices(tensors)
+    out = [torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in tensors]
+    lct_list_orthogonalize(x, LctMatrices(out), alloc_orthogonal(x), steps, coef, scale)
     return out

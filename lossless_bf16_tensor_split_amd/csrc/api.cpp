@@ -557,10 +557,12 @@ int clip_part(const lct_list &x, const lct_list &y, uint32_t k0, uint32_t count,
     return p.list.chunks ? launch_list_clip(p, stream) : (int)hipSuccess;
 }
 
-// The clip's aliasing rules: with every range sorted by its start, none may
-// begin inside a written one before it, and a written one inside none.  In
-// place, x_k and y_k are one range; inputs may overlap each other.
-lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list &y) {
+// The aliasing rules of a call that reads the tensors of x and writes those
+// of y, and that reads or writes one range more: with every range sorted by its
+// start, none may begin inside a written one before it, and a written one
+// inside none.  In place, x_k and y_k are one range; inputs may overlap each
+// other.
+lct_status check_list_alias(const lct_list &x, Range also, bool also_written, const lct_list &y) {
     struct Span {
         Range r;
         bool written;
@@ -575,7 +577,7 @@ lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list
             if (!inplace) v.push_back({rx, false});
             v.push_back({ry, true});
         }
-        v.push_back({rng(coef, 4), false});
+        if (also.lo != also.hi) v.push_back({also, also_written});
         std::sort(v.begin(), v.end(), [](const Span &a, const Span &b) { return a.r.lo < b.r.lo; });
         uintptr_t any = 0, written = 0;   // furthest end of all spans so far, of the written ones
         for (const Span &s : v) {
@@ -584,9 +586,129 @@ lct_status check_clip_alias(const lct_list &x, const float *coef, const lct_list
             if (s.written) written = std::max(written, s.r.hi);
         }
     } catch (const std::bad_alloc &) {
-        return hip_fail(hipErrorOutOfMemory, "clip's table of ranges");
+        return hip_fail(hipErrorOutOfMemory, "table of ranges");
     }
     return LCT_OK;
+}
+
+// ---- orthogonalisation
+
+// A list of matrices: rows[k] divides n[k], and no side is too long.
+lct_status check_matrices(const lct_list *x, const uint64_t *rows) {
+    const lct_status st = check_list(x);
+    if (st != LCT_OK) return st;
+    if (x->count > 0 && !rows) return LCT_EINVAL;
+    for (uint32_t k = 0; k < x->count; ++k) {
+        const uint64_t n = x->n[k], r = rows[k];
+        if (n == 0) continue;
+        if (r == 0 || n % r || n > kOrthoMaxElems || r > kOrthoMaxSide || n / r > kOrthoMaxSide) return LCT_EINVAL;
+    }
+    return LCT_OK;
+}
+
+// The largest magnitude that p(s) = a s + b s^3 + c s^5 (odd), or with
+// `square` b s + c s^2 (for s of A), takes on [0, hi]: at the end or where the
+// derivative vanishes.
+double poly_most(const float (&coef)[3], double hi, bool square) {
+    const double a = coef[0], b = coef[1], c = coef[2];
+    auto at = [&](double s) { return std::fabs(square ? b * s + c * s * s : s * (a + s * s * (b + c * s * s))); };
+    double most = at(hi);
+    auto look = [&](double s) {
+        if (s > 0.0 && s < hi) most = std::max(most, at(s));
+    };
+    if (square) {
+        if (c != 0.0) look(-b / (2.0 * c));
+        return most;
+    }
+    // a + 3 b t + 5 c t^2 = 0 in t = s^2
+    if (c == 0.0) {
+        if (b != 0.0) look(std::sqrt(std::max(0.0, -a / (3.0 * b))));
+        return most;
+    }
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0)
+        for (const double sign : {-1.0, 1.0}) look(std::sqrt(std::max(0.0, (-3.0 * b + sign * std::sqrt(d)) / (10.0 * c))));
+    return most;
+}
+
+// Coefficients whose iterates stay within the range of the numbers that the
+// kernels hold them in.
+bool ortho_coef_ok(const float (&coef)[3], uint32_t steps) {
+    for (const float c : coef)
+        if (!std::isfinite(c)) return false;
+    double hi = 1.001;   // a norm rounded down leaves a singular value slightly above one
+    for (uint32_t s = 0; s < steps; ++s) {
+        if (!(poly_most(coef, hi * hi, true) <= kOrthoBoundB)) return false;
+        hi = poly_most(coef, hi, false) * 1.001;
+        if (s + 1 < steps && !(hi <= kOrthoBound)) return false;   // (the last result is not held in FP16)
+    }
+    return true;
+}
+
+uint64_t ortho_pad(uint64_t v) { return (v + kOrthoTile - 1) / kOrthoTile * kOrthoTile; }
+uint64_t ortho_bytes(uint64_t mp, uint64_t np) { return 2 * (4 * mp * np + 3 * mp * mp); }
+
+// Batches of matrices, in list order: f(p, b, bytes) with the matrices' sizes
+// and places in the working memory after `p.off`'s start; the list's other
+// fields are the caller's.  Stops at f's first failure.
+template <class F>
+lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
+    uint32_t k = 0;
+    while (k < x.count) {
+        OrthoParams p;
+        memset(&p, 0, sizeof p);
+        OrthoBatch b = {0, 0, 0};
+        uint64_t bytes = 0, elems = 0;
+        for (; k < x.count && p.count < kOrthoMax; ++k) {
+            if (x.n[k] == 0) continue;
+            const uint64_t r = rows[k], c = x.n[k] / r;
+            const uint64_t m = std::min(r, c), n = std::max(r, c);
+            const uint64_t mp = ortho_pad(m), np = ortho_pad(n);
+            if (p.count > 0 && elems + mp * np > kOrthoBatch) break;
+            elems += mp * np;
+            OrthoMat &o = p.mat[p.count++];
+            o.off = bytes;
+            o.m = (uint32_t)m;
+            o.n = (uint32_t)n;
+            o.mp = (uint32_t)mp;
+            o.np = (uint32_t)np;
+            o.type = (uint32_t)x.type[k];
+            o.tall = r > c;
+            o.index = k;
+            o.x = x.d_x[k];
+            o.prep0 = b.prep_tiles;
+            o.sym0 = b.sym_tiles;
+            o.next0 = b.next_tiles;
+            const uint64_t side = mp / kOrthoTile;
+            b.prep_tiles += (uint32_t)(mp / 64 * (np / 64));
+            b.sym_tiles += (uint32_t)(side * (side + 1) / 2);
+            b.next_tiles += (uint32_t)(side * (np / kOrthoTile));
+            bytes += ortho_bytes(mp, np);
+        }
+        if (p.count == 0) break;
+        const lct_status st = f(p, b, bytes);
+        if (st != LCT_OK) return st;
+    }
+    return LCT_OK;
+}
+
+// The working memory: every matrix's norm, the norms' result and scratch, then
+// the largest batch's.
+struct OrthoScratch {
+    uint64_t out, norm, batch, bytes;
+};
+OrthoScratch ortho_scratch(const lct_list &x, const uint64_t *rows) {
+    OrthoScratch s;
+    s.out = align256(4ull * x.count);
+    s.norm = s.out + 256;
+    s.batch = s.norm + norm_scratch_bytes(x.count, 0);
+    uint64_t most = 0;
+    (void)ortho_batches(x, rows, [&](OrthoParams &, OrthoBatch &, uint64_t bytes) {
+        most = std::max(most, bytes);
+        return LCT_OK;
+    });
+    s.bytes = s.batch + most;
+    return s;
 }
 
 }  // namespace
@@ -1282,7 +1404,7 @@ lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list 
     if (!aligned(d_coef, 4)) return LCT_EALIGN;
     for (uint32_t k = 0; k < x->count; ++k)
         if (x->n[k] != y->n[k]) return LCT_EINVAL;
-    st = check_clip_alias(*x, d_coef, *y);
+    st = check_list_alias(*x, rng(d_coef, 4), false, *y);
     if (st != LCT_OK) return st;
     st = check_arch();
     if (st != LCT_OK) return st;
@@ -1293,6 +1415,58 @@ lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list 
         if (e != hipSuccess) return hip_fail(e, "clip launch");
     }
     return LCT_OK;
+}
+
+// ---- orthogonalisation
+
+lct_status lct_orthogonal_scratch(const lct_list *x, const uint64_t *rows, uint64_t *bytes) {
+    if (!bytes) return LCT_EINVAL;
+    const lct_status st = check_matrices(x, rows);
+    if (st != LCT_OK) return st;
+    *bytes = ortho_scratch(*x, rows).bytes;
+    return LCT_OK;
+}
+
+lct_status lct_list_orthogonalize(const lct_list *x, const uint64_t *rows, const lct_list *y, uint32_t steps,
+                                  const float coef[3], const float *scale, void *d_scratch, void *stream) {
+    lct_status st = check_matrices(x, rows);
+    if (st == LCT_OK) st = check_list(y);
+    if (st != LCT_OK) return st;
+    if (!coef || steps < 1 || steps > 32 || x->count != y->count || !d_scratch) return LCT_EINVAL;
+    for (uint32_t k = 0; k < x->count; ++k)
+        if (x->n[k] != y->n[k] || y->type[k] != LCT_BF16) return LCT_EINVAL;
+    const float cf[3] = {coef[0], coef[1], coef[2]};
+    if (!ortho_coef_ok(cf, steps)) return LCT_EINVAL;
+    if (!aligned(d_scratch, 256)) return LCT_EALIGN;
+    const OrthoScratch s = ortho_scratch(*x, rows);
+    st = check_list_alias(*x, rng(d_scratch, s.bytes), true, *y);
+    if (st != LCT_OK) return st;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    uint8_t *scr = static_cast<uint8_t *>(d_scratch);
+    float *norm = reinterpret_cast<float *>(scr);
+    if (x->count > 0) {
+        st = list_norm(*x, true, {INFINITY, 1.0}, reinterpret_cast<double *>(scr + s.norm), norm,
+                       reinterpret_cast<lct_norm_t *>(scr + s.out), stream);
+        if (st != LCT_OK) return st;
+    }
+    return ortho_batches(*x, rows, [&](OrthoParams &p, OrthoBatch &b, uint64_t) {
+        p.scratch = scr + s.batch;
+        p.norm = norm;
+        p.xscale = kOrthoX;
+        p.a = cf[0];
+        p.kx = (float)(kOrthoA / (kOrthoX * kOrthoX));
+        p.ka = (float)(cf[1] * kOrthoB / kOrthoA);
+        p.kaa = (float)(cf[2] * kOrthoB / (kOrthoA * kOrthoA));
+        p.kbx = (float)(1.0 / kOrthoB);
+        for (uint32_t j = 0; j < p.count; ++j) {
+            OrthoMat &o = p.mat[j];
+            o.y = const_cast<void *>(y->d_x[o.index]);
+            o.scale = (float)((scale ? (double)scale[o.index] : 1.0) / kOrthoX);
+        }
+        const int e = launch_ortho(p, b, steps, stream);
+        return e == hipSuccess ? LCT_OK : hip_fail(e, "orthogonalisation launch");
+    });
 }
 
 const char *lct_strerror(lct_status st) {

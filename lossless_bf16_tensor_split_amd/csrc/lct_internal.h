@@ -362,6 +362,44 @@ inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
     return align256(8 * ((list > nblk ? list : nblk) + kFoldGrid));
 }
 
+// Orthogonalising many matrices (ortho.hip): a launch's matrices travel as
+// kernel arguments.  A matrix has m rows and n >= m columns (`tall`: the
+// caller's is the transpose), padded to mp and np, whole tiles; its working
+// memory starts at byte `off`: X as a pair, two copies of its transpose, A as a
+// pair, B, all FP16.
+constexpr uint32_t kOrthoMax = 32;        // matrices per launch
+constexpr uint32_t kOrthoTile = 128;
+// Elements (padded) that a batch of matrices gathers: 1024 tiles of 256 x 256,
+// four per CU.
+constexpr uint64_t kOrthoBatch = 1ull << 26;
+// FP16 numbers stand for X, A and B times these powers of two.  Singular
+// values stay below kOrthoBound (checked for the coefficients), so X's
+// elements do, A's stay below its square and B's below kOrthoBoundB.
+constexpr double kOrthoX = 32768.0, kOrthoA = 16384.0, kOrthoB = 8192.0;
+constexpr double kOrthoBound = 1.9, kOrthoBoundB = 7.8;
+constexpr uint64_t kOrthoMaxElems = 1ull << 32;   // of one matrix: its root mean square stays in FP16's range
+constexpr uint32_t kOrthoMaxSide = 1u << 24;
+struct OrthoMat {
+    const void *x;
+    void *y;
+    uint64_t off;
+    uint32_t m, n, mp, np;
+    uint32_t type, tall, index;   // index: in the whole list (its norm's place)
+    float scale;
+    uint32_t prep0, sym0, next0;  // first tile of each kind of launch
+};
+struct OrthoParams {
+    uint8_t *scratch;
+    const float *norm;
+    double xscale;
+    float a, ka, kaa, kx, kbx;    // factors of a X, A, A A, X X' and B X for numbers as held
+    uint32_t count, turn, last;
+    OrthoMat mat[kOrthoMax];
+};
+struct OrthoBatch {
+    uint32_t prep_tiles, sym_tiles, next_tiles;
+};
+
 // The allocation-free update's static working memory (per device).
 constexpr uint64_t kNoAllocScratch = LCT_NOALLOC_SCRATCH_BYTES;
 constexpr int kMaxDevices = 64;
@@ -407,6 +445,8 @@ int launch_code_finish(const CodeFinishParams &p, void *stream);
 template <uint32_t N>
 int launch_list_clip(const ListClipParams<N> &p, void *stream);
 int launch_code_norm(const CodeNormParams &p, bool group, bool squares, void *stream);
+// Orthogonalising a batch of matrices (ortho.hip); changes p from step to step.
+int launch_ortho(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stream);
 
 // Host codebook construction (codebook.cpp).
 // The model's probability of each exponent field (its range of |x|).
