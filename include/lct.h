@@ -556,7 +556,7 @@ lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w
  * rounded to BF16.  coef = {a, b, c}; s is the matrix's own factor.
  *
  * x: matrices as a list, of any lct_dtype; matrix k has rows[k] rows and n[k] /
- * rows[k] columns, its elements row by row, at most 2^24 of either and 2^32
+ * rows[k] columns, its elements row by row, at most 2^22 of either and 2^32
  * elements (n[k] = 0: nothing is done).  y: a list of the same sizes, all BF16;
  * y_k is x_k (same memory, BF16: in place) or overlaps no tensor of x, and no
  * other of y.  scale: host array of a factor per matrix (null: 1).  steps 1..32.  The

@@ -645,47 +645,58 @@ bool ortho_coef_ok(const float (&coef)[3], uint32_t steps) {
     return true;
 }
 
-uint64_t ortho_pad(uint64_t v) { return (v + kOrthoTile - 1) / kOrthoTile * kOrthoTile; }
 uint64_t ortho_bytes(uint64_t mp, uint64_t np) { return 2 * (4 * mp * np + 3 * mp * mp); }
 
 // Batches of matrices, in list order: f(p, b, bytes) with the matrices' sizes
-// and places in the working memory after `p.off`'s start; the list's other
-// fields are the caller's.  Stops at f's first failure.
+// and places in the working memory; the other fields are the caller's.  Stops
+// at f's first failure.
 template <class F>
 lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
     uint32_t k = 0;
     while (k < x.count) {
         OrthoParams p;
         memset(&p, 0, sizeof p);
-        OrthoBatch b = {0, 0, 0};
-        uint64_t bytes = 0, elems = 0;
+        uint64_t elems = 0;
         for (; k < x.count && p.count < kOrthoMax; ++k) {
             if (x.n[k] == 0) continue;
             const uint64_t r = rows[k], c = x.n[k] / r;
-            const uint64_t m = std::min(r, c), n = std::max(r, c);
-            const uint64_t mp = ortho_pad(m), np = ortho_pad(n);
-            if (p.count > 0 && elems + mp * np > kOrthoBatch) break;
-            elems += mp * np;
+            if (p.count > 0 && elems + x.n[k] > kOrthoBatch) break;
+            elems += x.n[k];
             OrthoMat &o = p.mat[p.count++];
-            o.off = bytes;
-            o.m = (uint32_t)m;
-            o.n = (uint32_t)n;
-            o.mp = (uint32_t)mp;
-            o.np = (uint32_t)np;
+            o.m = (uint32_t)std::min(r, c);
+            o.n = (uint32_t)std::max(r, c);
             o.type = (uint32_t)x.type[k];
             o.tall = r > c;
             o.index = k;
             o.x = x.d_x[k];
+        }
+        if (p.count == 0) break;
+        // the longest products first: short ones fill what they leave
+        std::stable_sort(p.mat, p.mat + p.count,
+                         [](const OrthoMat &a, const OrthoMat &b) { return (uint64_t)a.m + a.n > (uint64_t)b.m + b.n; });
+        OrthoBatch b = {kOrthoLarge, 0, 0, 0};
+        uint64_t tiles = 0;
+        for (uint32_t j = 0; j < p.count; ++j) {
+            const uint64_t mt = (p.mat[j].m + kOrthoLarge - 1) / kOrthoLarge;
+            tiles += mt * ((p.mat[j].n + kOrthoLarge - 1) / kOrthoLarge);
+        }
+        if (tiles < kOrthoLargeFrom) b.tile = kOrthoSmall;
+        uint64_t bytes = 0;
+        for (uint32_t j = 0; j < p.count; ++j) {
+            OrthoMat &o = p.mat[j];
+            const uint64_t mt = (o.m + b.tile - 1) / b.tile, nt = (o.n + b.tile - 1) / b.tile;
+            o.mp = (uint32_t)(mt * b.tile);
+            o.np = (uint32_t)(nt * b.tile);
+            o.off = bytes;
             o.prep0 = b.prep_tiles;
             o.sym0 = b.sym_tiles;
             o.next0 = b.next_tiles;
-            const uint64_t side = mp / kOrthoTile;
-            b.prep_tiles += (uint32_t)(mp / 64 * (np / 64));
-            b.sym_tiles += (uint32_t)(side * (side + 1) / 2);
-            b.next_tiles += (uint32_t)(side * (np / kOrthoTile));
-            bytes += ortho_bytes(mp, np);
+            b.prep_tiles += o.mp / 64 * (o.np / 64);
+            const uint64_t r = b.tile / kOrthoSmall;   // a large tile is two wide ones
+            b.sym_tiles += (uint32_t)(mt * (mt + 1) / 2 * r);
+            b.next_tiles += (uint32_t)(mt * nt * r);
+            bytes += ortho_bytes(o.mp, o.np);
         }
-        if (p.count == 0) break;
         const lct_status st = f(p, b, bytes);
         if (st != LCT_OK) return st;
     }

@@ -368,17 +368,18 @@ inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
 // memory starts at byte `off`: X as a pair, two copies of its transpose, A as a
 // pair, B, all FP16.
 constexpr uint32_t kOrthoMax = 32;        // matrices per launch
-constexpr uint32_t kOrthoTile = 128;
-// Elements (padded) that a batch of matrices gathers: 1024 tiles of 256 x 256,
-// four per CU.
-constexpr uint64_t kOrthoBatch = 1ull << 26;
+constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;   // tiles
+constexpr uint32_t kOrthoLargeFrom = 200;                  // large tiles of a batch from which on they are taken
+// Elements that a batch of matrices gathers: 2048 tiles of 256 x 256, eight
+// per CU.
+constexpr uint64_t kOrthoBatch = 1ull << 27;
 // FP16 numbers stand for X, A and B times these powers of two.  Singular
 // values stay below kOrthoBound (checked for the coefficients), so X's
 // elements do, A's stay below its square and B's below kOrthoBoundB.
 constexpr double kOrthoX = 32768.0, kOrthoA = 16384.0, kOrthoB = 8192.0;
 constexpr double kOrthoBound = 1.9, kOrthoBoundB = 7.8;
 constexpr uint64_t kOrthoMaxElems = 1ull << 32;   // of one matrix: its root mean square stays in FP16's range
-constexpr uint32_t kOrthoMaxSide = 1u << 24;
+constexpr uint32_t kOrthoMaxSide = 1u << 22;      // a tile's rows span less than 2^32 bytes
 struct OrthoMat {
     const void *x;
     void *y;
@@ -393,11 +394,11 @@ struct OrthoParams {
     const float *norm;
     double xscale;
     float a, ka, kaa, kx, kbx;    // factors of a X, A, A A, X X' and B X for numbers as held
-    uint32_t count, turn, last;
+    uint32_t count, turn;         // turn: which copy of X' is read
     OrthoMat mat[kOrthoMax];
 };
 struct OrthoBatch {
-    uint32_t prep_tiles, sym_tiles, next_tiles;
+    uint32_t tile, prep_tiles, sym_tiles, next_tiles;
 };
 
 // The allocation-free update's static working memory (per device).

@@ -43,7 +43,7 @@ typedef __attribute__((address_space(1))) const uint8_t glb_u8;
 
 // Where a matrix's parts lie in the working memory (elements of FP16).
 struct Parts {
-    f16 *xh, *xl, *xt[2], *ah, *al, *bh;
+    f16 *xh, *xl, *xt0, *xt1, *ah, *al, *bh;
 };
 __device__ __forceinline__ Parts parts_of(uint8_t *scratch, const OrthoMat &o) {
     f16 *p = reinterpret_cast<f16 *>(scratch + o.off);
@@ -51,8 +51,8 @@ __device__ __forceinline__ Parts parts_of(uint8_t *scratch, const OrthoMat &o) {
     Parts r;
     r.xh = p;
     r.xl = p + x;
-    r.xt[0] = p + 2 * x;
-    r.xt[1] = p + 3 * x;
+    r.xt0 = p + 2 * x;
+    r.xt1 = p + 3 * x;
     r.ah = p + 4 * x;
     r.al = r.ah + a;
     r.bh = r.al + a;
@@ -107,223 +107,430 @@ __global__ __launch_bounds__(256) void k_ortho_prep(const OrthoParams p) {
         const uint64_t at = (uint64_t)(i0 + r) * o.np + j0 + c;
         w.xh[at] = h;
         w.xl[at] = (f16)(v - (float)h);
-        w.xt[0][(uint64_t)(j0 + r) * o.mp + i0 + c] = (f16)tile[c][r];
+        w.xt0[(uint64_t)(j0 + r) * o.mp + i0 + c] = (f16)tile[c][r];
     }
 }
 
 // ------------------------------------------------------------------ products
 
 // The product of P's rows with Q's rows over K (both read along their rows),
-// a T x T tile per workgroup of WM x WN waves.  K advances by 64 elements
-// (128 bytes of a row) a step; two LDS buffers alternate, filled by loads that
-// go to LDS directly.  A row's eight 16-byte pieces are stored rotated by an
-// exclusive-or with the row's number modulo 8: the fragments' reads (32 rows
-// of one column of pieces) then touch every bank equally.
-constexpr uint32_t kRowB = 128;
+// a TP x TQ tile per workgroup of four waves, a quarter each.  K advances by 32
+// elements (64 bytes of a row) a step through NB buffers in LDS, filled by
+// loads that go there directly.  A row's four 16-byte pieces are stored
+// exchanged by an exclusive-or with the row's number over 4, so that the
+// fragments' reads (32 rows of one column of pieces) touch every bank equally.
+//
+// The matrix units wait for nothing but the data: a wave reads the next
+// fragments while it multiplies the present ones, asks for one load at a
+// time among them (sixteen at once keep it from issuing products for half a
+// step), and has NB - 2 steps' loads under way when it waits for the one after
+// the present step.  The barrier lies between a step's halves: by then every
+// read of the step is done, so its buffer is free for the loads that follow.
+constexpr uint32_t kRowB = 64;
+constexpr uint32_t kStep = kRowB / 2;
+constexpr uint32_t kThreads = 256;
 
-template <uint32_t T, uint32_t WM, uint32_t WN>
+template <uint32_t TP, uint32_t TQ, uint32_t NB>
 struct Product {
-    static constexpr uint32_t kWaves = WM * WN;
-    static constexpr uint32_t FM = T / (32 * WM), FN = T / (32 * WN);
-    static constexpr uint32_t kSide = T * kRowB;        // LDS bytes of one operand's step
-    static constexpr uint32_t kBuf = 2 * kSide;
-    f32x16 acc[FM][FN];
+    static constexpr uint32_t FP = TP / 64, FQ = TQ / 64;   // fragments of 32 along the sides of a wave's part
+    static constexpr uint32_t SP = TP / 2, SQ = TQ / 2;     // its sides
+    static constexpr uint32_t kSide = TP * kRowB;           // LDS bytes of P's step; Q's follow
+    static constexpr uint32_t kBuf = (TP + TQ) * kRowB;
+    static constexpr uint32_t kLds = NB * kBuf;
+    static constexpr uint32_t kPart = 2 * SP * SQ;          // bytes of a wave's part as 16-bit numbers
+    static_assert(kLds >= 4 * kPart, "the waves' parts pass through LDS");
+    // acc[a][b][4 r + q]: row a 32 + 8 r + 4 (lane / 32) + q of P's part, row
+    // b 32 + lane % 32 of Q's
+    f32x16 acc[FP][FQ];
 
-    // Rows r0.. of g (a step's 128 bytes of each, at column byte c) to LDS.
-    __device__ __forceinline__ void fetch(const f16 *g, uint64_t ld, uint32_t c, uint8_t *lds) {
-        const uint32_t l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(g) + c + 16 * ((l & 7) ^ (l >> 3));
-#pragma unroll
-        for (uint32_t it = 0; it < T / (8 * kWaves); ++it) {
-            const uint32_t r = (it * kWaves + w) * 8;
-            __builtin_amdgcn_global_load_lds(
-                reinterpret_cast<glb_u8 *>(reinterpret_cast<uintptr_t>(src + 2 * ld * (r + (l >> 3)))),
-                (lds_u8 *)(lds + r * kRowB), 16, 0, 0);
-        }
+    // at most n loads outstanding, no LDS read
+    template <uint32_t N>
+    __device__ __forceinline__ static void wait() {
+        static_assert(N < 64, "six bits");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
-    // segs pairs of operands (p[s], q[s]), each of `steps` steps of 64.
-    __device__ __forceinline__ void run(const f16 *const *ps, const f16 *const *qs, uint32_t segs, uint32_t steps,
-                                        uint64_t ldp, uint64_t ldq, uint8_t *lds) {
-        const uint32_t l = threadIdx.x & 63, w = threadIdx.x >> 6;
-        const uint32_t wm = w / WN, wn = w % WN;
+    // Pairs of operands (p[s], q[s]), each of `steps` steps, summed.
+    template <uint32_t SEGS>
+    __device__ __forceinline__ void run(const f16 *const (&p)[SEGS], const f16 *const (&q)[SEGS], uint32_t steps,
+                                        uint64_t ld, uint8_t *lds) {
+        const uint32_t l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (uint32_t a = 0; a < FM; ++a)
+        for (uint32_t a = 0; a < FP; ++a)
 #pragma unroll
-            for (uint32_t b = 0; b < FN; ++b) acc[a][b] = f32x16{0.0f};
-        const uint32_t total = segs * steps;
-        const uint32_t pr = (wm * FM * 32 + (l & 31)) * kRowB, qr = (wn * FN * 32 + (l & 31)) * kRowB + kSide;
-        auto get = [&](uint32_t k, uint8_t *buf) {
-            const uint32_t s = k / steps, c = (k - s * steps) * kRowB;
-            fetch(ps[s], ldp, c, buf);
-            fetch(qs[s], ldq, c, buf + kSide);
+            for (uint32_t b = 0; b < FQ; ++b) acc[a][b] = f32x16{0.0f};
+        const uint32_t total = SEGS * steps;
+        // a load: 16 rows of 64 bytes, a lane's row and (exchanged) piece
+        const uint32_t ldb = 2 * (uint32_t)ld;   // (T rows span less than 2^32 bytes)
+        const uint32_t mine = (16 * w + (l >> 2)) * ldb + 16 * ((l & 3) ^ (l >> 4));
+        __amdgpu_buffer_rsrc_t rp = rsrc(p[0], ldb), rq = rsrc(q[0], ldb);
+        uint32_t at = 0, seg = 0;   // the next load's step of its segment, in bytes
+        auto load = [&](bool side, uint32_t it, uint8_t *buf) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(side ? rq : rp,
+                                                     (lds_u8 *)(buf + (side ? kSide : 0) + (it * 64 + 16 * w) * kRowB),
+                                                     16, mine, at + it * 64 * ldb, 0, 0);
         };
-        auto step = [&](const uint8_t *buf) {
-#pragma unroll
-            for (uint32_t ks = 0; ks < 4; ++ks) {
-                const uint32_t slot = 16 * ((2 * ks + (l >> 5)) ^ (l & 7));
-                f16x8 a[FM], b[FN];
-#pragma unroll
-                for (uint32_t f = 0; f < FM; ++f)
-                    a[f] = *reinterpret_cast<const f16x8 *>(buf + pr + f * 32 * kRowB + slot);
-#pragma unroll
-                for (uint32_t f = 0; f < FN; ++f)
-                    b[f] = *reinterpret_cast<const f16x8 *>(buf + qr + f * 32 * kRowB + slot);
-#pragma unroll
-                for (uint32_t f = 0; f < FM; ++f)
-#pragma unroll
-                    for (uint32_t g = 0; g < FN; ++g)
-                        acc[f][g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[f], b[g], acc[f][g], 0, 0, 0);
+        auto next_step = [&]() {
+            at += kRowB;
+            if (SEGS > 1 && at == steps * kRowB) {
+                at = 0;
+                ++seg;
+                rp = rsrc(p[seg == 1 ? 1 % SEGS : 2 % SEGS], ldb);
+                rq = rsrc(q[seg == 1 ? 1 % SEGS : 2 % SEGS], ldb);
             }
         };
-        get(0, lds);
-        for (uint32_t k = 0; k < total; ++k) {
-            __builtin_amdgcn_s_waitcnt(0x0F70);   // the step's loads are in LDS (vmcnt 0)
-            __syncthreads();
-            if (k + 1 < total) get(k + 1, lds + ((k + 1) & 1) * kBuf);
-            step(lds + (k & 1) * kBuf);
+        const uint32_t pr = ((w >> 1) * SP + (l & 31)) * kRowB, qr = ((w & 1) * SQ + (l & 31)) * kRowB + kSide;
+        struct Frags {
+            f16x8 p[FP], q[FQ];
+        };
+        auto read = [&](Frags &f, const uint8_t *buf, uint32_t ks) {
+            const uint32_t slot = 16 * ((2 * ks + (l >> 5)) ^ ((l >> 2) & 3));
+#pragma unroll
+            for (uint32_t k = 0; k < FP; ++k) f.p[k] = *reinterpret_cast<const f16x8 *>(buf + pr + k * 32 * kRowB + slot);
+#pragma unroll
+            for (uint32_t k = 0; k < FQ; ++k) f.q[k] = *reinterpret_cast<const f16x8 *>(buf + qr + k * 32 * kRowB + slot);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // FP * FQ products, with the loads of one operand among them
+        auto multiply = [&](const Frags &f, bool side, uint8_t *buf) {
+#pragma unroll
+            for (uint32_t a = 0; a < FP; ++a) {
+#pragma unroll
+                for (uint32_t b = 0; b < FQ; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[a], f.q[b], acc[a][b], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (!side)
+                    load(false, a, buf);
+                else if (a % (FP / FQ) == 0)
+                    load(true, a / (FP / FQ), buf);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto buffer = [&](uint32_t k) { return lds + (k % NB) * kBuf; };
+        Frags x, y;
+        // the first NB - 1 steps' loads (past the end the last step's again,
+        // so that the counts of what is outstanding hold)
+        for (uint32_t k = 0; k < NB - 1; ++k) {
+#pragma unroll
+            for (uint32_t it = 0; it < FP; ++it) load(false, it, buffer(k));
+#pragma unroll
+            for (uint32_t it = 0; it < FQ; ++it) load(true, it, buffer(k));
+            if (k + 1 < total) next_step();
         }
+        wait<(FP + FQ) * (NB - 2)>();
+        __syncthreads();
+        read(x, buffer(0), 0);
+        for (uint32_t k = 0; k < total; ++k) {
+            // (each wait is for fragments asked for half a step ago, before the
+            // next are: the compiler's own wait, behind them, is for all)
+            uint8_t *into = buffer(k + NB - 1);
+            wait<(FP + FQ) * (NB - 2)>();
+            read(y, buffer(k), 1);
+            multiply(x, false, into);
+            wait<(FP + FQ) * (NB - 3) + FP>();   // the next step's loads are in LDS
+            asm volatile("" ::: "memory");        // (a workgroup fence would wait for every load)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            read(x, buffer(k + 1), 0);
+            multiply(y, true, into);
+            if (k + NB < total) next_step();
+        }
+        wait<0>();
+        __syncthreads();   // LDS is free for what follows
+    }
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const f16 *g, uint32_t ldb) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16 *>(g), (short)0, (int)(max(TP, TQ) * ldb), 0x00020000);
     }
 
-    // f(i, j, v): v are the values of rows i..i+3 of column j of the tile
-    template <class F>
-    __device__ __forceinline__ void each(F f) {
-        const uint32_t l = threadIdx.x & 63, w = threadIdx.x >> 6;
-        const uint32_t wm = w / WN, wn = w % WN;
+    // Parts of matrices on their way between memory and a wave's sums, through
+    // the wave's own LDS, 16-byte pieces exchanged by row.  ALONG: the rows are
+    // Q's (SQ of SP elements; a lane has four neighbours of a row); otherwise
+    // P's (SP of SQ).
+    template <bool ALONG>
+    struct Rows {
+        static constexpr uint32_t kLen = ALONG ? SP : SQ, kCount = ALONG ? SQ : SP;
+        static constexpr uint32_t kPieces = kLen / 8, kPer = 64 / kPieces;   // of a row; rows a wave moves at once
+        __device__ __forceinline__ static uint32_t at(uint32_t row, uint32_t piece) {
+            return row * (2 * kLen) + 16 * (piece ^ (row & (kPieces - 1)));
+        }
+    };
+    __device__ __forceinline__ static uint8_t *mine(uint8_t *lds) { return lds + (threadIdx.x >> 6) * kPart; }
+    // The lane's number, anew for each pass over the sums: the compiler would
+    // otherwise keep every pass's addresses in registers, of which the sums
+    // take half, and spill.
+    __device__ __forceinline__ static uint32_t lane_anew() {
+        uint32_t l = threadIdx.x & 63;
+        asm volatile("" : "+v"(l));
+        return l;
+    }
+    template <class G>
+    __device__ __forceinline__ void quads(G g) {
+        const uint32_t l = lane_anew();
 #pragma unroll
-        for (uint32_t a = 0; a < FM; ++a)
+        for (uint32_t a = 0; a < FP; ++a)
 #pragma unroll
-            for (uint32_t b = 0; b < FN; ++b)
+            for (uint32_t b = 0; b < FQ; ++b) {
 #pragma unroll
-                for (uint32_t r = 0; r < 4; ++r) {
-                    const float v[4] = {acc[a][b][4 * r], acc[a][b][4 * r + 1], acc[a][b][4 * r + 2],
-                                        acc[a][b][4 * r + 3]};
-                    f((wm * FM + a) * 32 + 8 * r + 4 * (l >> 5), (wn * FN + b) * 32 + (l & 31), v);
+                for (uint32_t r = 0; r < 4; ++r) g(a, b, r, Rows<true>::at(b * 32 + (l & 31), 4 * a + r) + 8 * (l >> 5));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+    // acc <- acc + f * g, g's rows along
+    __device__ __forceinline__ void add_along(const f16 *g, uint64_t ld, float f, uint8_t *lds) {
+        using R = Rows<true>;
+        const uint32_t l = lane_anew();
+        uint8_t *own = mine(lds);
+#pragma unroll
+        for (uint32_t it = 0; it < R::kCount / R::kPer; ++it) {
+            const uint32_t v = it * R::kPer + l / R::kPieces, c = (l % R::kPieces) ^ (v & (R::kPieces - 1));
+            __builtin_amdgcn_global_load_lds(
+                reinterpret_cast<glb_u8 *>(reinterpret_cast<uintptr_t>(g + v * ld + 8 * c)),
+                (lds_u8 *)(own + it * 1024), 16, 0, 0);
+        }
+        wave_wait<true>();
+        quads([&](uint32_t a, uint32_t b, uint32_t r, uint32_t at) {
+            const f16x4 x = *reinterpret_cast<const f16x4 *>(own + at);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) acc[a][b][4 * r + q] += f * (float)x[q];
+        });
+        wave_wait();
+    }
+    // the wave's own LDS accesses (and, with LOADS, its loads to LDS) are done
+    template <bool LOADS = false>
+    __device__ __forceinline__ static void wave_wait() {
+        __builtin_amdgcn_s_waitcnt(LOADS ? 0x0070 : 0xC07F);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    // 16-bit numbers v(value) to LDS
+    template <bool ALONG, class V>
+    __device__ __forceinline__ void put(uint8_t *lds, V v) {
+        const uint32_t l = lane_anew();
+        uint8_t *own = mine(lds);
+        wave_wait();
+        if (ALONG) {
+            quads([&](uint32_t a, uint32_t b, uint32_t r, uint32_t at) {
+                uint16_t h[4];
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q) h[q] = v(acc[a][b][4 * r + q]);
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                *reinterpret_cast<u32x2 *>(own + at) =
+                    u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+            });
+        } else {
+#pragma unroll
+            for (uint32_t a = 0; a < FP; ++a)
+#pragma unroll
+                for (uint32_t b = 0; b < FQ; ++b) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e) {
+                        const uint32_t row = a * 32 + 8 * (e / 4) + 4 * (l >> 5) + e % 4;
+                        *reinterpret_cast<uint16_t *>(own + Rows<false>::at(row, 4 * b + (l & 31) / 8) + 2 * (l & 7)) =
+                            v(acc[a][b][e]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+        }
+        wave_wait();
+    }
+    // f(row, column, 16 bytes) for every piece of the part in LDS
+    template <bool ALONG, class G>
+    __device__ __forceinline__ static void pieces(uint8_t *lds, G g) {
+        using R = Rows<ALONG>;
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const uint32_t l = lane_anew();
+        uint8_t *own = mine(lds);
+#pragma unroll 8
+        for (uint32_t it = 0; it < R::kCount / R::kPer; ++it) {
+            const uint32_t row = it * R::kPer + l / R::kPieces, c = l % R::kPieces;
+            g(row, 8 * c, *reinterpret_cast<const u32x4 *>(own + R::at(row, c)));
+        }
+    }
+    // (the sums are hidden from the compiler between passes, or it keeps one
+    // pass's conversions for the next)
+    template <bool ALONG, class V>
+    __device__ __forceinline__ void store(f16 *g, uint64_t ld, uint8_t *lds, V v) {
+#pragma unroll
+        for (auto &ra : acc)
+#pragma unroll
+            for (auto &x : ra) asm volatile("" : "+a"(x));
+        put<ALONG>(lds, v);
+        pieces<ALONG>(lds, [&](uint32_t row, uint32_t c, auto x) {
+            *reinterpret_cast<decltype(x) *>(g + row * ld + c) = x;
+        });
     }
 };
 
-// Tile t of the upper triangle of a square of s x s tiles, row by row.
+__device__ __forceinline__ uint16_t high(float x) { return __builtin_bit_cast(uint16_t, (f16)x); }
+__device__ __forceinline__ uint16_t low(float x) { return __builtin_bit_cast(uint16_t, (f16)(x - (float)(f16)x)); }
+
+// Workgroups go to the eight XCDs in turn: of every 64 tiles an XCD gets eight
+// consecutive ones, which share rows of their operands in its L2.  (A longer
+// run each would give one XCD all of a batch's largest products.)
+__device__ __forceinline__ uint32_t tile_number() {
+    const uint32_t g = blockIdx.x;
+    if ((g | 63) >= gridDim.x) return g;
+    return (g & ~63u) + (g & 7) * 8 + (g >> 3 & 7);
+}
+
+// Tile t of the upper triangle of a square of s x s tiles: groups of four
+// rows, a group column by column.
 __device__ __forceinline__ void triangle(uint32_t t, uint32_t s, uint32_t &i, uint32_t &j) {
-    i = 0;
-    uint32_t len = s;
-    while (t >= len) {
-        t -= len;
-        --len;
-        ++i;
+    uint32_t r0 = 0, rows, head;
+    while (true) {
+        rows = min(4u, s - r0);
+        head = rows * (rows + 1) / 2;                  // the columns that the diagonal cuts
+        const uint32_t n = head + (s - r0 - rows) * rows;
+        if (t < n) break;
+        t -= n;
+        r0 += rows;
     }
-    j = i + t;
+    if (t >= head) {
+        i = r0 + (t - head) % rows;
+        j = r0 + rows + (t - head) / rows;
+        return;
+    }
+    uint32_t c = 0;
+    while (t > c) t -= ++c;
+    i = r0 + t;
+    j = r0 + c;
 }
 
 // A = X X' (SQUARE false) or B = b A + c A A: the tiles on and above the
 // diagonal, each written to its mirror image too.
-template <uint32_t T, uint32_t WM, uint32_t WN, bool SQUARE>
-__global__ __launch_bounds__(64 * WM * WN) void k_ortho_sym(const OrthoParams p) {
+template <uint32_t TP, uint32_t TQ, uint32_t NB, bool SQUARE>
+__global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const OrthoParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t k = matrix_of(p, blockIdx.x, [](const OrthoMat &o) { return o.sym0; });
+    const uint32_t t = tile_number();
+    const uint32_t k = matrix_of(p, t, [](const OrthoMat &o) { return o.sym0; });
     const OrthoMat &o = p.mat[k];
     const Parts w = parts_of(p.scratch, o);
     uint32_t ti, tj;
-    triangle(blockIdx.x - o.sym0, o.mp / T, ti, tj);
-    const uint32_t i0 = ti * T, j0 = tj * T;
-    Product<T, WM, WN> pr;
-    const uint64_t ld = SQUARE ? o.mp : o.np;
-    if (SQUARE) {
-        const f16 *ps[3] = {w.ah + i0 * ld, w.ah + i0 * ld, w.al + i0 * ld};
-        const f16 *qs[3] = {w.ah + j0 * ld, w.al + j0 * ld, w.ah + j0 * ld};
-        pr.run(ps, qs, 3, o.mp / 64, ld, ld, smem);
-    } else {
-        const f16 *ps[1] = {w.xh + i0 * ld}, *qs[1] = {w.xh + j0 * ld};
-        pr.run(ps, qs, 1, o.np / 64, ld, ld, smem);
-    }
-    pr.each([&](uint32_t i, uint32_t j, const float (&v)[4]) {
-        const uint64_t at = (uint64_t)(i0 + i) * o.mp + j0 + j, mirror = (uint64_t)(j0 + j) * o.mp + i0 + i;
-        f16x4 h, lo;
+    constexpr uint32_t R = TP / TQ;   // tiles to a square one
+    const uint32_t square = (t - o.sym0) / R;
+    triangle(square, o.mp / TP, ti, tj);
+    const bool mirror = ti != tj;
+    tj = tj * R + (t - o.sym0) % R;
+    const uint64_t ld = SQUARE ? o.mp : o.np, i0 = ti * TP * ld, j0 = tj * TQ * ld;
+    Product<TP, TQ, NB> pr;
+    if constexpr (SQUARE)
+        pr.template run<3>({w.ah + i0, w.ah + i0, w.al + i0}, {w.ah + j0, w.al + j0, w.ah + j0}, o.mp / kStep, ld, smem);
+    else
+        pr.template run<1>({w.xh + i0}, {w.xh + j0}, o.np / kStep, ld, smem);
+    // this wave's part: rows pi.. of P (of A), pj.. of Q
+    const uint32_t wv = threadIdx.x >> 6;
+    const uint64_t pi = ti * TP + (wv >> 1) * (TP / 2), pj = tj * TQ + (wv & 1) * (TQ / 2);
+    const uint64_t along = pj * o.mp + pi, across = pi * o.mp + pj;
+    const float f = SQUARE ? p.kaa : p.kx;
 #pragma unroll
-        for (uint32_t r = 0; r < 4; ++r) {
-            if (SQUARE) {
-                const uint64_t e = at + (uint64_t)r * o.mp;
-                h[r] = (f16)(p.ka * ((float)w.ah[e] + (float)w.al[e]) + p.kaa * v[r]);
-                w.bh[e] = h[r];
-            } else {
-                const float f = p.kx * v[r];
-                h[r] = (f16)f;
-                lo[r] = (f16)(f - (float)h[r]);
-                w.ah[at + (uint64_t)r * o.mp] = h[r];
-                w.al[at + (uint64_t)r * o.mp] = lo[r];
-            }
+    for (auto &ra : pr.acc)
+#pragma unroll
+        for (auto &v : ra) v *= f;
+    if (SQUARE) {
+        pr.add_along(w.ah + along, o.mp, p.ka, smem);
+        pr.add_along(w.al + along, o.mp, p.ka, smem);
+        pr.template store<true>(w.bh + along, o.mp, smem, high);
+        if (mirror) pr.template store<false>(w.bh + across, o.mp, smem, high);
+    } else {
+        pr.template store<true>(w.ah + along, o.mp, smem, high);
+        pr.template store<true>(w.al + along, o.mp, smem, low);
+        if (mirror) {
+            pr.template store<false>(w.ah + across, o.mp, smem, high);
+            pr.template store<false>(w.al + across, o.mp, smem, low);
         }
-        if (ti != tj) {
-            if (SQUARE) {
-                *reinterpret_cast<f16x4 *>(w.bh + mirror) = h;
-            } else {
-                *reinterpret_cast<f16x4 *>(w.ah + mirror) = h;
-                *reinterpret_cast<f16x4 *>(w.al + mirror) = lo;
-            }
-        }
-    });
+    }
 }
 
 // X <- a X + B X; the last step writes y in its place.
-template <uint32_t T, uint32_t WM, uint32_t WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_ortho_next(const OrthoParams p) {
+template <uint32_t TP, uint32_t TQ, uint32_t NB, bool LAST>
+__global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_next(const OrthoParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t k = matrix_of(p, blockIdx.x, [](const OrthoMat &o) { return o.next0; });
+    const uint32_t tile = tile_number();
+    const uint32_t k = matrix_of(p, tile, [](const OrthoMat &o) { return o.next0; });
     const OrthoMat &o = p.mat[k];
     const Parts w = parts_of(p.scratch, o);
-    const uint32_t t = blockIdx.x - o.next0, mt = o.mp / T;
-    const uint32_t i0 = t % mt * T, j0 = t / mt * T;
-    Product<T, WM, WN> pr;
-    const f16 *ps[1] = {w.bh + (uint64_t)i0 * o.mp}, *qs[1] = {w.xt[p.turn] + (uint64_t)j0 * o.mp};
-    pr.run(ps, qs, 1, o.mp / 64, o.mp, o.mp, smem);
-    const bool last = p.last;
-    pr.each([&](uint32_t i, uint32_t j, const float (&v)[4]) {
-        const uint64_t at = (uint64_t)(i0 + i) * o.np + j0 + j;
-        f16x4 h;
+    const uint32_t t = tile - o.next0, mt = o.mp / TQ;
+    const uint64_t i0 = t % mt * TQ, j0 = t / mt * TP;
+    Product<TP, TQ, NB> pr;
+    pr.template run<1>({(p.turn ? w.xt1 : w.xt0) + j0 * o.mp}, {w.bh + i0 * o.mp}, o.mp / kStep, o.mp, smem);
+    const uint32_t wv = threadIdx.x >> 6;
+    const uint64_t pj = j0 + (wv >> 1) * (TP / 2), pi = i0 + (wv & 1) * (TQ / 2);
+    const uint64_t along = pi * o.np + pj, across = pj * o.mp + pi;
 #pragma unroll
-        for (uint32_t r = 0; r < 4; ++r) {
-            const uint64_t e = at + (uint64_t)r * o.np;
-            const float x = p.a * ((float)w.xh[e] + (float)w.xl[e]) + p.kbx * v[r];
-            if (!last) {
-                h[r] = (f16)x;
-                w.xh[e] = h[r];
-                w.xl[e] = (f16)(x - (float)h[r]);
-            } else if (i0 + i + r < o.m && j0 + j < o.n) {
-                const uint64_t ye = o.tall ? (uint64_t)(j0 + j) * o.m + i0 + i + r : (uint64_t)(i0 + i + r) * o.n + j0 + j;
-                static_cast<__bf16 *>(o.y)[ye] = (__bf16)(o.scale * x);
-            }
+    for (auto &ra : pr.acc)
+#pragma unroll
+        for (auto &v : ra) v *= p.kbx;
+    pr.add_along(w.xh + along, o.np, p.a, smem);
+    pr.add_along(w.xl + along, o.np, p.a, smem);
+    if (!LAST) {
+        pr.template store<true>(w.xh + along, o.np, smem, high);
+        pr.template store<true>(w.xl + along, o.np, smem, low);
+        pr.template store<false>((p.turn ? w.xt0 : w.xt1) + across, o.mp, smem, high);
+        return;
+    }
+    const float scale = o.scale;
+    auto rounded = [&](float x) { return __builtin_bit_cast(uint16_t, (__bf16)(scale * x)); };
+    if (o.tall)
+        pr.template put<false>(smem, rounded);
+    else
+        pr.template put<true>(smem, rounded);
+    // rows and columns of y as the caller has it
+    const uint32_t rows = o.tall ? o.n : o.m, cols = o.tall ? o.m : o.n;
+    const uint64_t r0 = o.tall ? pj : pi, c0 = o.tall ? pi : pj;
+    uint16_t *y = static_cast<uint16_t *>(o.y);
+    const bool whole = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+    auto out = [&](uint32_t row, uint32_t c, auto x) {
+        const uint64_t r = r0 + row, q = c0 + c;
+        if (r >= rows || q >= cols) return;
+        uint16_t *to = y + r * cols + q;
+        if (whole) {
+            *reinterpret_cast<decltype(x) *>(to) = x;
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (q + e < cols) to[e] = (uint16_t)(x[e / 2] >> (16 * (e % 2)));
         }
-        if (!last) *reinterpret_cast<f16x4 *>(w.xt[p.turn ^ 1] + (uint64_t)(j0 + j) * o.mp + i0 + i) = h;
-    });
+    };
+    if (o.tall)
+        pr.template pieces<false>(smem, out);
+    else
+        pr.template pieces<true>(smem, out);
 }
 
-std::atomic<size_t> g_granted[8];
+// Dynamic LDS beyond 64 KiB must be requested per kernel, once.
+std::atomic<bool> g_granted[8];
 
-int launch_tiles(const void *fn, uint32_t grid, uint32_t threads, size_t lds, const OrthoParams &p, void *stream,
-                 std::atomic<size_t> &granted) {
-    if (lds > 64 * 1024 && lds > granted.load()) {
+int launch_tiles(const void *fn, uint32_t grid, size_t lds, const OrthoParams &p, void *stream,
+                 std::atomic<bool> &granted) {
+    if (lds > 64 * 1024 && !granted.load()) {
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return (int)e;
-        granted.store(lds);
+        granted.store(true);
     }
     void *args[] = {const_cast<OrthoParams *>(&p)};
-    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(threads), args, lds, (hipStream_t)stream);
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kThreads), args, lds, (hipStream_t)stream);
     return (int)(e != hipSuccess ? e : hipGetLastError());
 }
 
-template <uint32_t T, uint32_t WM, uint32_t WN>
+template <uint32_t TP, uint32_t TQ, uint32_t NB>
 int run_batch(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stream) {
-    const void *gram = reinterpret_cast<const void *>(&k_ortho_sym<T, WM, WN, false>);
-    const void *square = reinterpret_cast<const void *>(&k_ortho_sym<T, WM, WN, true>);
-    const void *next = reinterpret_cast<const void *>(&k_ortho_next<T, WM, WN>);
-    const size_t lds = 2 * Product<T, WM, WN>::kBuf;
-    const uint32_t threads = 64 * WM * WN;
+    const void *gram = reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, false>);
+    const void *square = reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, true>);
+    const void *next = reinterpret_cast<const void *>(&k_ortho_next<TP, TQ, NB, false>);
+    const void *last = reinterpret_cast<const void *>(&k_ortho_next<TP, TQ, NB, true>);
+    constexpr size_t lds = Product<TP, TQ, NB>::kLds;
+    std::atomic<bool> *granted = g_granted + (TP == 256 ? 4 : 0);
     for (uint32_t s = 0; s < steps; ++s) {
         p.turn = s & 1;
-        p.last = s + 1 == steps;
-        int e = launch_tiles(gram, b.sym_tiles, threads, lds, p, stream, g_granted[0]);
-        if (e == hipSuccess) e = launch_tiles(square, b.sym_tiles, threads, lds, p, stream, g_granted[1]);
-        if (e == hipSuccess) e = launch_tiles(next, b.next_tiles, threads, lds, p, stream, g_granted[2]);
+        const bool end = s + 1 == steps;
+        int e = launch_tiles(gram, b.sym_tiles, lds, p, stream, granted[0]);
+        if (e == hipSuccess) e = launch_tiles(square, b.sym_tiles, lds, p, stream, granted[1]);
+        if (e == hipSuccess)
+            e = end ? launch_tiles(last, b.next_tiles, lds, p, stream, granted[3])
+                    : launch_tiles(next, b.next_tiles, lds, p, stream, granted[2]);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -335,7 +542,7 @@ int launch_ortho(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stre
     hipLaunchKernelGGL(k_ortho_prep, dim3(b.prep_tiles), dim3(256), 0, (hipStream_t)stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    return run_batch<kOrthoTile, 2, 2>(p, b, steps, stream);
+    return b.tile == 256 ? run_batch<256, 128, 3>(p, b, steps, stream) : run_batch<128, 128, 4>(p, b, steps, stream);
 }
 
 }  // namespace lct
