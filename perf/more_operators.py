@@ -258,7 +258,8 @@ def keep(s, case):
         s["xl"], s["yl"] = L.LctMatrices(s["xs"]), L.LctMatrices(s["ys"])
         s["work"] = L.alloc_orthogonal(s["xl"])
     elif op == "mix":
-        lay, ns = L.lct_layout_init(L.CLEAN), sizes_of(case)
+        # each member with the padding behind it, over which the plain form goes too
+        lay, ns = L.lct_layout_init(L.CLEAN), [-(-n // 256) * 256 for n in sizes_of(case)]
         sigma = 0.02 if case["dense"] == "none" else 1e-3
         cb = L.lct_codebook_build(L.Model(L.GAUSSIAN, sigma, 0.0), s["y"])
         bind = lambda t: L.LctGroup(ns, lay, [cb] * len(ns), parts(t, ns))  # noqa: E731
