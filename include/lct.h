@@ -547,6 +547,61 @@ lct_status lct_momentum_step_clip_group(const lct_group *gw, const lct_tensor *w
                                         float mu, float eta, const lct_tensor *w_out,
                                         const lct_tensor *m_out, void *stream);
 
+/* ---- mixes of a compressed tensor with a dense one ---------------------------
+ * y' = rne_bf16(fmaf(a, y, bx)) with bx = (b * c) * x, both products rounded to
+ * fp32, c = *d_coef (a device float read when the step runs, such as a norm's
+ * coef; null: 1); a NaN result is written as 0x7FC0.  y is decoded with cb, y'
+ * encoded with cb_out (cb itself, or one from lct_codebook_reshift); x is dense,
+ * BF16, n elements.  With d_dense (BF16, n elements; may be null) a dense result
+ * too: y' as rounded, or, with ahead, rne_bf16(fmaf(a, y', bx)).
+ * A momentum step whose momentum is wanted dense: a = mu, b = 1, x the gradient
+ * (ahead: looked ahead by a step, after Nesterov).  A weight step from a dense
+ * update: a = 1 - eta * decay, b = -eta.
+ * d_x and d_dense: 16-byte aligned.  y_out's sf, pay, cnt and obase may be y_in's
+ * own (in place); its ovf, status and scratch overlap no part of y_in.  d_x
+ * overlaps no output but d_dense, which may be d_x itself and otherwise overlaps
+ * nothing; d_coef overlaps no output.  After a mix in place whose output
+ * overflowed, y is lost, as for the other updates.
+ * Group form: per tensor, with g's codebooks for y and y', and gx's and gd's
+ * dense buffers (their codebooks are not used; gd may be null, or gx); the groups
+ * have the same layout and sizes.
+ * Enqueues only.  Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS, LCT_EARCH,
+ * LCT_EHIP. */
+lct_status lct_mix_step(const lct_codebook *cb, const lct_tensor *y_in, float a, const uint16_t *d_x, float b,
+                        const float *d_coef, const lct_codebook *cb_out, const lct_tensor *y_out,
+                        uint16_t *d_dense, int32_t ahead, void *stream);
+lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float a, const lct_group *gx, float b,
+                              const float *d_coef, const lct_tensor *y_out, const lct_group *gd, int32_t ahead,
+                              void *stream);
+
+/* ---- tables looked up by rows ------------------------------------------------
+ * A token table kept compressed: rows of cols elements, read by number, and the
+ * gradient that its rows get from the tokens that looked them up.
+ *
+ * Common: d_index holds count indices, int64 (wide) or int32; an index outside
+ * 0 .. rows - 1 (a padding token's) gives a row of zeros and no gradient.  At
+ * most 2^30 indices, 2^31 rows and 2^24 columns.  Matrices are dense, row by
+ * row, of any lct_dtype, with the alignment of their elements.  Enqueue only.
+ * Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS, LCT_EARCH, LCT_EHIP.
+ *
+ * lct_tensor_rows: y_t = scale * W[index_t] (the product in fp32, rounded to y's
+ * type), W a compressed tensor of n = rows * cols elements (or a group's member,
+ * lct_group_tensor) decoded with cb.  A code is found only through its stream
+ * from the start, so a row costs the decoding of its block up to the row.
+ *
+ * lct_rows_grad: G[v] = scale * (sum of dy_t over the t with index_t = v), for
+ * every row of G, those without a token becoming zero; with add, added to what
+ * the rows with tokens hold and the others left alone.  Sums are FP32 in a fixed
+ * order (equal calls give equal bits), rounded once to G's type.  d_scratch:
+ * lct_rows_scratch(count, cols) bytes of device memory, 256-byte aligned, shared
+ * only by calls that do not overlap in time. */
+lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t cols, const void *d_index,
+                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *stream);
+lct_status lct_rows_scratch(uint64_t count, uint64_t cols, uint64_t *bytes);
+lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, const void *d_dy, int32_t dy_type,
+                         uint64_t rows, uint64_t cols, float scale, int32_t add, void *d_g, int32_t g_type,
+                         void *d_scratch, void *stream);
+
 /* ---- orthogonalised updates -------------------------------------------------
  * Newton-Schulz orthogonalisation of many matrices, as optimisers use it on a
  * matrix's momentum: with X0 = x / (|x| + 1e-7) (the root of the sum of

@@ -64,6 +64,7 @@ EXPORTED = ["lct_layout_init", "lct_sizes", "lct_codebook_build", "lct_codebook_
             "lct_encode_group", "lct_decode_group", "lct_sgd_step_group", "lct_momentum_step_group",
             "lct_norm_scratch", "lct_list_norm", "lct_tensor_norm", "lct_group_norm", "lct_norm_join", "lct_list_clip",
             "lct_sgd_step_clip", "lct_sgd_step_clip_group", "lct_momentum_step_clip", "lct_momentum_step_clip_group",
+            "lct_mix_step", "lct_mix_step_group", "lct_tensor_rows", "lct_rows_scratch", "lct_rows_grad",
             "lct_orthogonal_scratch", "lct_list_orthogonalize",
             "lct_strerror", "lct_last_hip_error"]
 
@@ -157,6 +158,11 @@ def _load():
     L.lct_sgd_step_clip_group.argtypes = [G, T, G, T, f32, P, T, P]
     L.lct_momentum_step_clip.argtypes = [CB, T, CB, T, P, P, f32, f32, T, T, P]
     L.lct_momentum_step_clip_group.argtypes = [G, T, G, T, G, P, f32, f32, T, T, P]
+    L.lct_mix_step.argtypes = [CB, T, f32, P, f32, P, CB, T, P, i32, P]
+    L.lct_mix_step_group.argtypes = [G, T, f32, G, f32, P, T, G, i32, P]
+    L.lct_tensor_rows.argtypes = [CB, T, u64, P, i32, u64, f32, P, i32, P]
+    L.lct_rows_scratch.argtypes = [u64, u64, C.POINTER(u64)]
+    L.lct_rows_grad.argtypes = [P, i32, u64, P, i32, u64, u64, f32, i32, P, i32, P, P]
     L.lct_orthogonal_scratch.argtypes = [LI, P, C.POINTER(u64)]
     L.lct_list_orthogonalize.argtypes = [LI, P, LI, C.c_uint32, P, P, P, P]
     L.lct_strerror.restype = C.c_char_p
@@ -942,6 +948,118 @@ def clip_grad_norm(tensors, max_norm: float, scale: float = 1.0, kind: int = NOR
     out = grad_norm(x, max_norm, scale, kind)
     lct_list_clip(x, out)
     return out
+
+
+# ------------------------------------------------------------------ mixes with a dense tensor
+
+def lct_mix_step(cb: Codebook, y_in: LctTensor, a: float, x: torch.Tensor, b: float, y_out: LctTensor, coef=None,
+                 dense: torch.Tensor | None = None, ahead: bool = False, cb_out: Codebook | None = None,
+                 stream=None) -> None:
+    """y' = a * y + (b * coef) * x, y compressed and x dense; dense (may be x)
+    gets y', or a * y' + (b * coef) * x with ahead."""
+    _gradient(x, y_in.n)
+    if dense is not None:
+        _bits16(dense)
+        if dense.numel() != y_in.n:
+            raise ValueError("dense has %d elements, the tensors %d" % (dense.numel(), y_in.n))
+    coef = None if coef is None else _coef(coef)
+    for t, what in ((y_in.sf, "the tensor"), (x, "x"), (y_out.sf, "the output"), (dense, "dense")):
+        if t is not None:
+            _current(t.device, what)
+    i, o = y_in.c(need_scratch=False), y_out.c()
+    _check(lib.lct_mix_step(C.byref(cb), C.byref(i), a, _ptr(x), b, _ptr(coef),
+                            C.byref(cb if cb_out is None else cb_out), C.byref(o), _ptr(dense), bool(ahead),
+                            _stream(stream)), "lct_mix_step")
+
+
+def lct_mix_step_group(g: LctGroup, y_all: LctTensor, a: float, gx: LctGroup, b: float, y_out: LctTensor, coef=None,
+                       dense: LctGroup | None = None, ahead: bool = False, stream=None) -> None:
+    """lct_mix_step on groups: x and the dense results are the dense buffers of
+    gx and of dense (which may be gx)."""
+    coef = None if coef is None else _coef(coef)
+    for t, what in ((g.table, "the group's table"), (y_all.sf, "the group"), (gx.table, "x's table"),
+                    (y_out.sf, "the output"), (dense and dense.table, "dense's table")):
+        if t is not None:
+            _current(t.device, what)
+    i, o = y_all.c(need_scratch=False), y_out.c()
+    _check(lib.lct_mix_step_group(C.byref(g.g), C.byref(i), a, C.byref(gx.g), b, _ptr(coef), C.byref(o),
+                                  None if dense is None else C.byref(dense.g), bool(ahead), _stream(stream)),
+           "lct_mix_step_group")
+
+
+# ------------------------------------------------------------------ tables looked up by rows
+
+class RowsWork:
+    """Working memory of ``lct_rows_grad`` (kept between calls; shared only by
+    calls that do not overlap in time)."""
+
+    def __init__(self, scratch: torch.Tensor):
+        self.scratch = scratch
+
+
+def alloc_rows(count: int, cols: int = 0, device="cuda") -> RowsWork:
+    """Working memory for up to ``count`` indices; cols: the columns of the
+    gradient (0: for lookups only)."""
+    need = C.c_uint64(0)
+    _check(lib.lct_rows_scratch(count, cols, C.byref(need)), "lct_rows_scratch")
+    return RowsWork(torch.empty(max(int(need.value), 256), dtype=torch.uint8, device=device))
+
+
+def _index(index: torch.Tensor) -> int:
+    """1 for 64-bit indices, 0 for 32-bit ones."""
+    if index.dtype not in (torch.int64, torch.int32):
+        raise TypeError("indices must be int64 or int32, got %s" % index.dtype)
+    if not index.is_contiguous():
+        raise ValueError("the indices must be contiguous")
+    _current(index.device, "the indices")
+    return int(index.dtype == torch.int64)
+
+
+def _matrix(t: torch.Tensor, rows: int | None, what: str) -> int:
+    """A dense matrix's lct_dtype."""
+    ty = _LIST_TYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError("%s is %s; expected bfloat16, float16 or float32" % (what, t.dtype))
+    if t.dim() < 2 or (rows is not None and t.numel() != rows * t.shape[-1]):
+        raise ValueError("%s has the shape %s%s" % (what, tuple(t.shape),
+                                                    "" if rows is None else ", not one row for each of %d" % rows))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    _current(t.device, what)
+    return ty
+
+
+def lct_tensor_rows(cb: Codebook, t: LctTensor, index: torch.Tensor, y: torch.Tensor, work: RowsWork | None = None,
+                    scale: float = 1.0, stream=None) -> None:
+    """y[k] = scale * row index[k] of the table t (rows of y's last dimension;
+    zeros for an index outside it)."""
+    wide, ty = _index(index), _matrix(y, index.numel(), "y")
+    cols = y.shape[-1]
+    if cols == 0 or t.n % cols:
+        raise ValueError("the table's %d elements are no whole rows of %d" % (t.n, cols))
+    _current(t.sf.device, "the table")
+    ct = t.c(need_scratch=False)
+    _check(lib.lct_tensor_rows(C.byref(cb), C.byref(ct), cols, _ptr(index), wide, index.numel(), scale, _ptr(y), ty,
+                               _stream(stream)), "lct_tensor_rows")
+
+
+def lct_rows_grad(index: torch.Tensor, dy: torch.Tensor, g: torch.Tensor, work: RowsWork, scale: float = 1.0,
+                  add: bool = False, stream=None) -> None:
+    """g[v] = scale * the sum of dy's rows whose index is v (added to g's rows
+    with add)."""
+    wide = _index(index)
+    ty, tg = _matrix(dy, index.numel(), "dy"), _matrix(g, None, "g")
+    if g.dim() != 2 or g.shape[1] != dy.shape[-1]:
+        raise ValueError("g has the shape %s, dy's rows %d columns" % (tuple(g.shape), dy.shape[-1]))
+    scr = work.scratch
+    _current(scr.device, "the working memory")
+    need = C.c_uint64(0)
+    _check(lib.lct_rows_scratch(index.numel(), g.shape[1], C.byref(need)), "lct_rows_scratch")
+    if not scr.is_contiguous() or scr.numel() * scr.element_size() < need.value:
+        raise ValueError("the working memory holds %d bytes; the gradient needs %d"
+                         % (scr.numel() * scr.element_size(), need.value))
+    _check(lib.lct_rows_grad(_ptr(index), wide, index.numel(), _ptr(dy), ty, g.shape[0], g.shape[1], scale, bool(add),
+                             _ptr(g), tg, _ptr(scr), _stream(stream)), "lct_rows_grad")
 
 
 # ------------------------------------------------------------------ orthogonalised updates

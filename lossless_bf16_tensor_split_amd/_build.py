@@ -26,7 +26,7 @@ def build(verbose: bool = False, save_temps: str | None = None) -> str:
         save_temps = os.path.abspath(save_temps)
     with tempfile.TemporaryDirectory(prefix="lct_build_") as tmp:
         objs = []
-        for src in ["kernels.hip", "norms.hip", "ortho.hip", "api.cpp", "codebook.cpp"]:
+        for src in ["kernels.hip", "norms.hip", "ortho.hip", "rows.hip", "api.cpp", "codebook.cpp"]:
             obj = os.path.join(tmp, src + ".o")
             cmd = [hipcc(), "--offload-arch=" + ARCH] + COMMON + ["-c", os.path.join(CSRC, src), "-o", obj]
             if src.endswith(".hip"):

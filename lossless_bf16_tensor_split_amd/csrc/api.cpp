@@ -351,6 +351,63 @@ lct_status sgd_run(SgdParams &p, const lct_tensor &w_in, const lct_tensor &m, co
     return sgd_launch(p, nb, group, stream);
 }
 
+// ---- mix
+
+// Aliasing rules of a mix (nb: the block count, ~0 for n's): the output's
+// fixed side is the input's own buffers, exactly, or disjoint from it; its
+// overflow, status and scratch overlap no part of the input.
+bool mix_alias_ok(const lct_tensor &in, const lct_tensor &out, uint64_t nb) {
+    const Parts pi = parts(in, nb), po = parts(out, nb);
+    const Range fi[] = {pi.sf, pi.pay, pi.cnt, pi.obase}, fo[] = {po.sf, po.pay, po.cnt, po.obase};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (!(i == j && fi[i].lo == fo[j].lo) && overlap(fi[i], fo[j])) return false;
+        if (overlap(pi.ovf, fo[i])) return false;
+    }
+    for (const Range &r : {po.ovf, po.status, po.scratch})
+        if (overlaps_any(r, pi, false)) return false;
+    return true;
+}
+
+void mix_params(MixParams &p, const lct_tensor &in, const lct_tensor &out, uint64_t nb, float a, float b,
+                const float *coef, bool dense, int32_t ahead) {
+    p.sf = in.sf;
+    p.pay = in.pay;
+    p.cnt = in.cnt;
+    p.obase = in.obase;
+    p.ovf = in.ovf;
+    p.ovf_cap = in.ovf_cap;
+    p.o_sf = out.sf;
+    p.o_pay = out.pay;
+    p.o_cnt = out.cnt;
+    p.o_obase = out.obase;
+    p.o_ovf = out.ovf;
+    p.o_ovf_cap = out.ovf_cap;
+    p.status = out.status;
+    p.scratch = (uint8_t *)out.scratch;
+    p.n = in.n;
+    p.block_elems = in.layout.block_elems;
+    p.cap_words = in.layout.cap_words;
+    p.nblk = (uint32_t)nb;
+    p.a = a;
+    p.b = b;
+    p.coef = coef;
+    p.park_cnt = out.cnt == in.cnt;
+    p.dense = dense;
+    p.ahead = ahead != 0;
+}
+
+lct_status mix_launch(const MixParams &p, uint64_t nb, bool group, void *stream) {
+    const OutSides o{{{p.scratch, p.o_obase, p.o_ovf, p.o_ovf_cap, p.status, p.o_cnt}}, 1, nb};
+    int e = launch_clear(o, stream);
+    if (e != hipSuccess) return hip_fail(e, "clear launch");
+    e = launch_mix(p, stream, group);
+    if (e != hipSuccess) return hip_fail(e, "mix launch");
+    e = launch_scan(o, stream);
+    if (e != hipSuccess) return hip_fail(e, "scan launch");
+    return LCT_OK;
+}
+
 // ---- norms and clipping
 
 uint64_t type_bytes(int32_t type) { return type == LCT_FP32 ? 4 : 2; }
@@ -1426,6 +1483,185 @@ lct_status lct_list_clip(const lct_list *x, const float *d_coef, const lct_list 
         if (e != hipSuccess) return hip_fail(e, "clip launch");
     }
     return LCT_OK;
+}
+
+// ---- mix of a compressed tensor with a dense one
+
+lct_status lct_mix_step(const lct_codebook *cb, const lct_tensor *y_in, float a, const uint16_t *d_x, float b,
+                        const float *d_coef, const lct_codebook *cb_out, const lct_tensor *y_out,
+                        uint16_t *d_dense, int32_t ahead, void *stream) {
+    if (!cb || !y_in || !y_out || !cb_out || !tables_ok(*cb) || !tables_ok(*cb_out)) return LCT_EINVAL;
+    if (y_in->n != y_out->n || y_in->layout.block_elems != y_out->layout.block_elems ||
+        y_in->layout.cap_words != y_out->layout.cap_words || (ahead && !d_dense))
+        return LCT_EINVAL;
+    if (y_in->n == 0) return layout_ok(y_in->layout) ? LCT_OK : LCT_EINVAL;
+    lct_status st = check_tensor(y_in, false);
+    if (st == LCT_OK) st = check_tensor(y_out, true);
+    if (st != LCT_OK) return st;
+    if (!d_x) return LCT_EINVAL;
+    if (!aligned(d_x, 16) || !aligned(d_dense, 16)) return LCT_EALIGN;
+    const uint64_t nb = nblocks(y_in->n, y_in->layout);
+    const Parts pi = parts(*y_in), po = parts(*y_out);
+    const Range x = rng(d_x, 2 * y_in->n), d = rng(d_dense, d_dense ? 2 * y_in->n : 0);
+    if (!mix_alias_ok(*y_in, *y_out, nb) || overlaps_any(x, po)) return LCT_EALIAS;
+    if (overlaps_any(d, pi, false) || overlaps_any(d, po) || (overlap(d, x) && d.lo != x.lo)) return LCT_EALIAS;
+    st = check_coef(d_coef, po);
+    if (st != LCT_OK) return st;
+    if (d_coef && overlap(rng(d_coef, 4), d)) return LCT_EALIAS;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    MixParams p;
+    memset(&p, 0, sizeof p);
+    mix_params(p, *y_in, *y_out, nb, a, b, d_coef, d_dense != nullptr, ahead);
+    p.x = d_x;
+    p.d = d_dense;
+    fill_dec(*cb, &p.dec);
+    fill_enc(*cb_out, &p.enc);
+    return mix_launch(p, nb, false, stream);
+}
+
+lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float a, const lct_group *gx, float b,
+                              const float *d_coef, const lct_tensor *y_out, const lct_group *gd, int32_t ahead,
+                              void *stream) {
+    lct_status st = check_group(g, y_all, false);
+    if (st == LCT_OK) st = check_group(g, y_out, true);
+    if (st != LCT_OK) return st;
+    if (!gx || (ahead && !gd)) return LCT_EINVAL;
+    for (const lct_group *o : {gx, gd}) {
+        if (!o) continue;
+        if (!o->d_table || !o->n || o->shape_hash != g->shape_hash || o->count != g->count || o->nblk != g->nblk ||
+            o->sf_bytes != g->sf_bytes)
+            return LCT_EINVAL;
+        for (uint32_t k = 0; k < g->count; ++k)
+            if (o->n[k] != g->n[k]) return LCT_EINVAL;
+    }
+    st = check_group_dense(*gx, parts(*y_out, g->nblk));
+    if (st != LCT_OK) return st;
+    if (gd) {
+        st = check_group_dense(*gd, parts(*y_out, g->nblk));
+        if (st == LCT_OK) st = check_group_dense(*gd, parts(*y_all, g->nblk));
+        if (st != LCT_OK) return st;
+        // the dense results: x's own buffers, or disjoint from all of them
+        // (status and scratch of the input, which the check above includes,
+        // are not in use: an overlap with them is refused all the same)
+        try {
+            const std::vector<int32_t> types(g->count, LCT_BF16);
+            const lct_list lx{g->count, gx->n, reinterpret_cast<void *const *>(gx->d_dense), types.data()};
+            const lct_list ld{g->count, gd->n, reinterpret_cast<void *const *>(gd->d_dense), types.data()};
+            st = check_list_alias(lx, rng(d_coef, d_coef ? 4 : 0), false, ld);
+        } catch (const std::bad_alloc &) {
+            return hip_fail(hipErrorOutOfMemory, "table of types");
+        }
+        if (st != LCT_OK) return st;
+    }
+    if (!mix_alias_ok(*y_all, *y_out, g->nblk)) return LCT_EALIAS;
+    st = check_coef(d_coef, parts(*y_out, g->nblk));
+    if (st != LCT_OK) return st;
+    st = check_arch();
+    if (st != LCT_OK) return st;
+    if (g->nblk == 0) return LCT_OK;
+    MixParams p;
+    memset(&p, 0, sizeof p);
+    mix_params(p, *y_all, *y_out, g->nblk, a, b, d_coef, gd != nullptr, ahead);
+    p.g = group_ref(*g);
+    p.gx = group_ref(*gx);
+    if (gd) p.gd = group_ref(*gd);
+    return mix_launch(p, g->nblk, true, stream);
+}
+
+// ---- rows of a compressed table, and their gradient
+
+static bool type_ok(int32_t t) { return t == LCT_BF16 || t == LCT_FP16 || t == LCT_FP32; }
+
+lct_status lct_rows_scratch(uint64_t count, uint64_t cols, uint64_t *bytes) {
+    if (!bytes || count > kMaxTokens || cols > kMaxCols) return LCT_EINVAL;
+    *bytes = row_scratch(count, cols).bytes;
+    return LCT_OK;
+}
+
+lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t cols, const void *d_index,
+                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *stream) {
+    if (!cb || !t || !tables_ok(*cb) || cols == 0 || cols > kMaxCols || count > kMaxTokens || !type_ok(type))
+        return LCT_EINVAL;
+    if (!layout_ok(t->layout) || t->n % cols || t->n / cols > kMaxRows) return LCT_EINVAL;
+    if (count == 0) return LCT_OK;
+    if (t->n > 0) {
+        const lct_status st = check_tensor(t, false);
+        if (st != LCT_OK) return st;
+    }
+    if (!d_index || !d_y) return LCT_EINVAL;
+    if (!aligned(d_index, wide ? 8 : 4) || !aligned(d_y, type_bytes(type))) return LCT_EALIGN;
+    const Range y = rng(d_y, count * cols * type_bytes(type));
+    if (overlap(y, rng(d_index, count * (wide ? 8 : 4))) || (t->n > 0 && overlaps_any(y, parts(*t), false)))
+        return LCT_EALIAS;
+    const lct_status st = check_arch();
+    if (st != LCT_OK) return st;
+    RowsParams p;
+    memset(&p, 0, sizeof p);
+    p.sf = t->sf;
+    p.pay = t->pay;
+    p.cnt = t->cnt;
+    p.obase = t->obase;
+    p.ovf = t->ovf;
+    p.ovf_cap = t->ovf_cap;
+    p.n = t->n;
+    p.rows = t->n / cols;
+    p.cols = cols;
+    p.count = count;
+    p.block_elems = t->layout.block_elems;
+    p.cap_words = t->layout.cap_words;
+    p.wide = wide != 0;
+    p.type = (uint32_t)type;
+    p.index = d_index;
+    p.y = d_y;
+    p.scale = scale;
+    fill_dec(*cb, &p.dec);
+    const int e = launch_rows(p, stream);
+    return e == hipSuccess ? LCT_OK : hip_fail(e, "rows launch");
+}
+
+lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, const void *d_dy, int32_t dy_type,
+                         uint64_t rows, uint64_t cols, float scale, int32_t add, void *d_g, int32_t g_type,
+                         void *d_scratch, void *stream) {
+    if (count > kMaxTokens || rows > kMaxRows || cols > kMaxCols || !type_ok(dy_type) || !type_ok(g_type))
+        return LCT_EINVAL;
+    if (rows == 0 || cols == 0) return LCT_OK;
+    if (!d_g || !d_scratch || (count > 0 && (!d_index || !d_dy))) return LCT_EINVAL;
+    if (!aligned(d_index, wide ? 8 : 4) || !aligned(d_dy, type_bytes(dy_type)) ||
+        !aligned(d_g, type_bytes(g_type)) || !aligned(d_scratch, 256))
+        return LCT_EALIGN;
+    const RowScratch s = row_scratch(count, cols);
+    const Range idx = rng(d_index, count * (wide ? 8 : 4)), dy = rng(d_dy, count * cols * type_bytes(dy_type));
+    const Range g = rng(d_g, rows * cols * type_bytes(g_type)), scr = rng(d_scratch, s.bytes);
+    if (overlap(g, idx) || overlap(g, dy) || overlap(g, scr) || overlap(scr, idx) || overlap(scr, dy))
+        return LCT_EALIAS;
+    const lct_status st = check_arch();
+    if (st != LCT_OK) return st;
+    uint8_t *scratch = static_cast<uint8_t *>(d_scratch);
+    RowGradParams p;
+    memset(&p, 0, sizeof p);
+    if (count > 0) {
+        SortParams q;
+        memset(&q, 0, sizeof q);
+        q.index = d_index;
+        q.count = (uint32_t)count;
+        q.rows = (uint32_t)rows;
+        q.wide = wide != 0;
+        const int e = launch_row_sort(q, s, scratch, &p.key, &p.token, stream);
+        if (e != hipSuccess) return hip_fail(e, "sort launch");
+    }
+    p.dy = d_dy;
+    p.g = d_g;
+    p.part = reinterpret_cast<float *>(scratch + s.part);
+    p.cols = cols;
+    p.count = (uint32_t)count;
+    p.rows = (uint32_t)rows;
+    p.tile = row_tile(count);
+    p.tiles = (uint32_t)((count + p.tile - 1) / p.tile);
+    p.add = add != 0;
+    p.scale = scale;
+    const int e = launch_row_grad(p, (uint32_t)dy_type, (uint32_t)g_type, stream);
+    return e == hipSuccess ? LCT_OK : hip_fail(e, "row gradient launch");
 }
 
 // ---- orthogonalisation

@@ -2894,6 +2894,243 @@ void k_mom(const MomParams p) {
     }
 }
 
+// ------------------------------------------------------------------ mix with a dense tensor
+
+// y' = rne(a * y + bx) with bx = (b * coef) * x rounded to fp32, y compressed, x
+// dense: the decoder's walk with the encoder's writer behind it, a unit per
+// wave.  D: 0 no dense result, 1 y', 2 the value looked ahead, rne(a * y' + bx).
+//
+// LDS: encode table (and its entry of no bits), decode table, then per wave the
+// input's rows between two zero rows; the result's rows go to memory as they
+// fill, once the input's (which they may overwrite) are in LDS.
+constexpr uint32_t kMixWaves = 4;
+constexpr uint32_t kMixETab = 0, kMixDTab = 2048, kMixWave0 = 3072;
+__host__ __device__ constexpr uint32_t mix_wave_bytes(uint32_t cap) { return (cap + 2) * ROWB; }
+
+struct MixUnit {
+    const uint8_t *sf;     // the unit's first element in each array
+    uint8_t *o_sf;
+    const uint16_t *x;
+    uint16_t *d;
+    uint64_t sp0;          // this lane's first spilled field
+    uint32_t n_s, c_s;     // its positions, and how many of them are coded
+};
+
+// Positions first .. end of this lane's stream (multiples of CH).  FAST: no
+// stream ends before, no field is spilled.
+template <bool FAST, uint32_t CAPT, int D>
+__device__ __forceinline__ void mix_stream(const MixParams &p, Reader &rd, uint32_t row0, PayWriter &st,
+                                           const MixUnit &u, float bc, uint32_t first, uint32_t end) {
+    const uint32_t s = lane();
+    const uint32_t capbits = 32 * cap_of<CAPT>(p.cap_words);
+    const int32_t qmax = Reader::bias(row0) + (int32_t)capbits - 2;
+    const uint8_t *sfs = u.sf + s;
+    const uint16_t *xs = u.x + s;
+    uint64_t *ctr = reinterpret_cast<uint64_t *>(p.scratch + kScrStage);
+    uint8_t *stage = p.scratch + scr_stage_offset(p.nblk);
+    const float a = p.a;
+    struct Buf {
+        uint32_t v[CH], x[CH];
+    };
+    double_buffered<Buf>(
+        first, end,
+        [&](Buf &bf, uint32_t j0) {
+            load_chunk<!FAST>(bf.v, sfs, j0, u.n_s);
+            load_chunk<!FAST>(bf.x, xs, j0, u.n_s);
+        },
+        [&](Buf &bf, uint32_t j0) {
+            uint32_t e23[CH], e8[CH];
+            if (FAST || wave_all(j0 + CH <= u.c_s || u.c_s >= u.n_s)) {
+                // four fields per window; a group where some window ran out
+                // (long escapes) is decoded again one field per window
+#pragma unroll
+                for (uint32_t g = 0; g < CH; g += 4) {
+                    const int32_t q0 = rd.q;
+                    uint32_t f[4];
+                    const uint32_t c = rd.next_n<4>(kMixDTab, qmax, f);
+                    if (__builtin_expect(!wave_all(c <= 30), 0)) {
+                        rd.q = q0;
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            f[k] = rd.next(kMixDTab);
+                            rd.q = min(rd.q, qmax);
+                        }
+                    }
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) e23[g + k] = f[k];
+                }
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < CH; ++i) {
+                    const uint32_t j = j0 + i;
+                    e23[i] = rd.next(kMixDTab);
+                    rd.q = min(rd.q, qmax);
+                    if (j >= u.c_s && j < u.n_s) {
+                        const uint64_t k = u.sp0 + (j - u.c_s);
+                        e23[i] = (k < p.ovf_cap ? (uint32_t)p.ovf[k] : 0u) << 23;
+                    }
+                }
+            }
+            uint8_t *o = u.o_sf + s + (size_t)j0 * NS;
+            uint16_t *d = D ? u.d + s + (size_t)j0 * NS : nullptr;
+#pragma unroll
+            for (uint32_t i = 0; i < CH; ++i) {
+                const uint32_t bx = __float_as_uint(bc * __uint_as_float(bf.x[i] << 16));
+                const uint32_t R = sgd_round(bx, join32(bf.v[i], e23[i]), a);
+                if (FAST || j0 + i < u.n_s) {
+                    o[i * NS] = (uint8_t)(sgd_sf16(R) >> 16);
+                    if (D == 1) d[i * NS] = (uint16_t)(R >> 16);
+                    if (D == 2) d[i * NS] = (uint16_t)(sgd_round(bx, R & 0xFFFF0000u, a) >> 16);
+                }
+                e8[i] = (R >> 20) & 0x7F8u;
+            }
+            writer_chunk<!FAST, false>(st, e8, j0, u.n_s, capbits, kMixETab);
+            writer_spill<!FAST>(st, e8, j0, u.n_s, ctr, stage, p.o_ovf_cap);
+        });
+}
+
+template <uint32_t CAPT, bool GROUP, int D>
+__global__ __launch_bounds__(64 * kMixWaves) void k_mix(const MixParams p) {
+    static_assert(kMixWaves == kMaxUnits, "a workgroup is a block");
+    const uint32_t b = blockIdx.x, h = wave_id(), u = b * kMaxUnits + h;
+    const uint32_t k = GROUP ? p.g.blk_tensor[b] : 0u;
+    stage_enc(GROUP ? p.g.enc[k] : p.enc, kMixETab);
+    stage_dec(GROUP ? p.g.dec[k] : p.dec, kMixDTab);
+    __syncthreads();
+    const uint32_t l = lane();
+    const uint32_t cap = cap_of<CAPT>(p.cap_words);
+    const uint32_t base = kMixWave0 + h * mix_wave_bytes(cap), row0 = base + ROWB;
+    st32(base + 4 * l, 0);                      // row -1
+    st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
+    rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
+    const float bc = p.b * device_factor(p.coef);
+    MixUnit m;
+    BlockSpan sp;
+    if (GROUP) {
+        sp = group_span(p.g, k, p.block_elems, b);
+        m.x = group_span(p.gx, k, p.block_elems, b).dense + h * US;
+        m.d = D ? group_span(p.gd, k, p.block_elems, b).dense + h * US : nullptr;
+    } else {
+        sp = flat_span(const_cast<uint16_t *>(p.x), p.n, p.block_elems, b);
+        m.x = sp.dense + h * US;
+        m.d = D ? p.d + sp.sf0 + h * US : nullptr;
+    }
+    const uint32_t nb = sp.nb;
+    m.sf = p.sf + sp.sf0 + h * US;
+    m.o_sf = p.o_sf + sp.sf0 + h * US;
+    m.n_s = m.c_s = stream_len(nb, h * US + l);
+    const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
+    m.sp0 = ob0;
+    Reader rd;
+    rd.init(row0, l);
+    PayWriter st;
+    st.init(0, l, m.n_s);
+    st.rows.init(p.o_pay, b, h, cap);
+    const uint32_t done = ob0 == ob1 ? CH * halves(nb) : 0u;
+    if (done) mix_stream<true, CAPT, D>(p, rd, row0, st, m, bc, 0, done);
+    if (done < walk_end(nb)) {
+        if (ob0 != ob1) {
+            uint32_t excl = 0;
+            unit_spills(p.cnt + (uint64_t)b * NS, nb, h, m.c_s, excl);
+            m.sp0 += excl;
+        }
+        mix_stream<false, CAPT, D>(p, rd, row0, st, m, bc, done, walk_end(nb));
+    }
+    // in place, the counts are parked: other units of the block still read
+    // the input's
+    uint16_t *cnt = p.park_cnt ? reinterpret_cast<uint16_t *>(p.scratch + scr_cnt_offset(p.nblk)) : p.o_cnt;
+    const UnitOut o{p.o_pay, cnt, p.scratch, p.nblk, p.o_ovf_cap, cap, p.park_cnt, 0};
+    unit_finish(st, m.n_s, u, b, h, 0, o);
+}
+
+// ------------------------------------------------------------------ rows of a compressed table
+
+// One row of the table for every index, a workgroup each, a lane per stream:
+// the streams of the row's block are decoded from their start to the row's
+// last position (a code can be found in no other way), and what lies in the row
+// is scaled and stored.  A row that crosses blocks takes them in turn.
+//
+// LDS: decode table, then per wave the block's rows between two zero rows.
+template <uint32_t CAPT>
+__global__ __launch_bounds__(64 * kDecWaves) void k_rows(const RowsParams p) {
+    const uint64_t t = blockIdx.x + (uint64_t)gridDim.x * blockIdx.y;
+    if (t >= p.count) return;
+    const int64_t r = p.wide ? static_cast<const int64_t *>(p.index)[t] : static_cast<const int32_t *>(p.index)[t];
+    const uint64_t y0 = t * p.cols;
+    auto put = [&](uint64_t i, float v) {
+        if (p.type == LCT_FP32)
+            static_cast<float *>(p.y)[i] = v;
+        else if (p.type == LCT_FP16)
+            static_cast<_Float16 *>(p.y)[i] = (_Float16)v;
+        else
+            static_cast<__bf16 *>(p.y)[i] = (__bf16)v;
+    };
+    if (r < 0 || (uint64_t)r >= p.rows) {
+        for (uint64_t i = threadIdx.x; i < p.cols; i += 64 * kDecWaves) put(y0 + i, 0.0f);
+        return;
+    }
+    stage_dec(p.dec, kDecTab);
+    const uint32_t l = lane(), h = wave_id(), s = h * US + l;
+    const uint32_t cap = cap_of<CAPT>(p.cap_words);
+    const uint32_t base = kDecWave0 + h * dec_wave_bytes(cap), row0 = base + ROWB;
+    st32(base + 4 * l, 0);                      // row -1
+    st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
+    __syncthreads();
+    const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap - 2;
+    const uint64_t first = (uint64_t)r * p.cols, last = first + p.cols;   // the row's elements
+    for (uint64_t at = first; at < last;) {
+        const uint32_t b = (uint32_t)(at / p.block_elems);
+        const uint64_t b0 = (uint64_t)b * p.block_elems;
+        const uint32_t nb = (uint32_t)min<uint64_t>(p.block_elems, p.n - b0);
+        const uint32_t lo = (uint32_t)(at - b0), hi = (uint32_t)min<uint64_t>(nb, last - b0);
+        rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
+        const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
+        uint32_t c_s = stream_len(nb, s), excl = 0;
+        if (ob0 != ob1) unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
+        const uint64_t sp0 = ob0 + excl;
+        Reader rd;
+        rd.init(row0, l);
+        // positions before the row's first in any stream are passed over,
+        // four to a window
+        const uint32_t j0 = lo / NS / 4 * 4, j1 = (hi - 1) / NS + 1;
+        auto four = [&](uint32_t (&f)[4]) {
+            const int32_t q0 = rd.q;
+            const uint32_t c = rd.next_n<4>(kDecTab, qmax, f);
+            if (__builtin_expect(!wave_all(c <= 30), 0)) {
+                rd.q = q0;
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    f[k] = rd.next(kDecTab);
+                    rd.q = min(rd.q, qmax);
+                }
+            }
+        };
+        uint32_t f[4];
+        for (uint32_t j = 0; j < j0; j += 4) four(f);
+        for (uint32_t j = j0; j < j1; j += 4) {
+            uint32_t sf[4];
+            bool in[4];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t e = (j + k) * NS + s;
+                in[k] = e >= lo && e < hi;
+                sf[k] = in[k] ? p.sf[b0 + e] : 0u;
+            }
+            four(f);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                if (!in[k]) continue;
+                if (j + k >= c_s) {
+                    const uint64_t i = sp0 + (j + k - c_s);
+                    f[k] = (i < p.ovf_cap ? (uint32_t)p.ovf[i] : 0u) << 23;
+                }
+                put(y0 + (b0 + (j + k) * NS + s - first), p.scale * __uint_as_float(join32(sf[k], f[k])));
+            }
+        }
+        at = b0 + hi;
+    }
+}
+
 // ------------------------------------------------------------------ launches
 
 // Dynamic LDS beyond 64 KiB must be requested per kernel; remember the
@@ -3060,6 +3297,43 @@ int launch_mom(const MomParams &p, void *stream, bool group) {
     std::atomic<size_t>(&gen_granted)[4] = g_mom_lds_granted[(clip ? 4 : 0) + (group ? 3 : 2)];
     const int slot = cap_slot(cap);
     return launch_update(p, full, kMomWaves, lds, granted[slot], gen, kMomWaves, lds, gen_granted[slot], stream);
+}
+
+template <uint32_t C> struct Mix0K { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, false, 0>); } };
+template <uint32_t C> struct Mix1K { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, false, 1>); } };
+template <uint32_t C> struct Mix2K { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, false, 2>); } };
+template <uint32_t C> struct Mix0GK { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, true, 0>); } };
+template <uint32_t C> struct Mix1GK { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, true, 1>); } };
+template <uint32_t C> struct Mix2GK { static const void *fn() { return reinterpret_cast<const void *>(&k_mix<C, true, 2>); } };
+// flat and group, no dense result, the value, looked ahead
+std::atomic<size_t> g_mix_lds_granted[6][4];
+
+int launch_mix(const MixParams &p, void *stream, bool group) {
+    const uint32_t cap = p.cap_words, d = !p.dense ? 0 : p.ahead ? 2 : 1;
+    const void *fn = group ? (d == 0   ? ByCap<Mix0GK>::pick(cap)
+                              : d == 1 ? ByCap<Mix1GK>::pick(cap)
+                                       : ByCap<Mix2GK>::pick(cap))
+                           : (d == 0   ? ByCap<Mix0K>::pick(cap)
+                              : d == 1 ? ByCap<Mix1K>::pick(cap)
+                                       : ByCap<Mix2K>::pick(cap));
+    return launch(fn, (uint64_t)p.nblk * kMaxUnits, kMixWaves, false,
+                  kMixWave0 + (size_t)kMixWaves * mix_wave_bytes(cap), p, stream,
+                  g_mix_lds_granted[d + (group ? 3 : 0)][cap_slot(cap)]);
+}
+
+template <uint32_t C> struct RowsK { static const void *fn() { return reinterpret_cast<const void *>(&k_rows<C>); } };
+std::atomic<size_t> g_rows_lds_granted[4];
+
+int launch_rows(const RowsParams &p, void *stream) {
+    const void *fn = ByCap<RowsK>::pick(p.cap_words);
+    const size_t lds = decode_lds(p.cap_words);
+    const int attr = ensure_lds(fn, lds, g_rows_lds_granted[cap_slot(p.cap_words)]);
+    if (attr != hipSuccess) return attr;
+    const uint64_t x = std::min<uint64_t>(p.count, 1u << 20), y = (p.count + x - 1) / x;
+    void *args[] = {const_cast<RowsParams *>(&p)};
+    const hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)x, (uint32_t)y), dim3(64 * kDecWaves), args, lds,
+                                         (hipStream_t)stream);
+    return (int)(e != hipSuccess ? e : hipGetLastError());
 }
 
 int launch_decode(const DecodeParams &p, void *stream, bool group) {

@@ -225,6 +225,100 @@ struct MomParams {
     DecTab wdec, mdec;
 };
 
+// The mix of a compressed tensor with a dense one: y' = rne(a * y + bx), bx =
+// (b * coef) * x, y' encoded; d (null: not wanted) gets y', or ahead, rne(a *
+// y' + bx).
+struct MixParams {
+    const uint8_t *sf;
+    const uint32_t *pay;
+    const uint16_t *cnt;
+    const uint64_t *obase;
+    const uint8_t *ovf;
+    uint64_t ovf_cap;
+    const uint16_t *x;
+    uint16_t *d;
+    uint8_t *o_sf;
+    uint32_t *o_pay;
+    uint16_t *o_cnt;
+    uint64_t *o_obase;
+    uint8_t *o_ovf;
+    uint64_t o_ovf_cap;
+    uint32_t *status;
+    uint8_t *scratch;
+    uint64_t n;
+    uint32_t block_elems, cap_words, nblk;
+    float a, b;
+    uint32_t park_cnt;     // the result's counts overwrite the input's: park them in scratch
+    uint32_t dense, ahead;
+    const float *coef;     // null: 1
+    GroupRef g, gx, gd;    // group kernels: y's codes, x's and d's buffers
+    EncTab enc;
+    DecTab dec;
+};
+
+// Rows of a compressed tensor taken as a table of `cols` columns.
+struct RowsParams {
+    const uint8_t *sf;
+    const uint32_t *pay;
+    const uint16_t *cnt;
+    const uint64_t *obase;
+    const uint8_t *ovf;
+    uint64_t ovf_cap;
+    uint64_t n, rows, cols, count;
+    uint32_t block_elems, cap_words, wide, type;   // wide: 64-bit indices; type: the result's
+    const void *index;
+    void *y;
+    float scale;
+    DecTab dec;
+};
+
+// The gradient of a table's rows (rows.hip).  Tokens are sorted by row in
+// passes of at most kSortBits bits over chunks of kSortChunk tokens, then
+// summed in tiles.
+constexpr uint32_t kSortBits = 9, kSortDigits = 1u << kSortBits;
+constexpr uint32_t kSortThreads = 256, kSortChunk = 1024;
+constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 31, kMaxCols = 1ull << 24;
+constexpr uint32_t kRowTile = 16, kRowTileMax = 256;   // tokens of a tile: more where there are many
+constexpr uint64_t kRowTiles = 4096;
+constexpr uint32_t kClearRows = 16;                    // rows that a clearing wave looks at
+inline uint32_t row_tile(uint64_t count) {
+    uint64_t t = kRowTile;
+    while (t < kRowTileMax && count > kRowTiles * t) t *= 2;
+    return (uint32_t)t;
+}
+struct SortParams {
+    const void *index;          // the first pass reads indices, the others keys
+    const uint32_t *from, *from_token;
+    uint32_t *to, *to_token, *hist;
+    uint32_t count, rows, wide, bits, shift, chunks;
+};
+struct RowGradParams {
+    const uint32_t *key, *token;   // sorted
+    const void *dy;
+    void *g;
+    float *part;                   // [tiles][2][cols]
+    uint64_t cols;
+    uint32_t count, rows, tile, tiles, add;
+    float scale;
+};
+// The gradient's working memory.
+struct RowScratch {
+    uint64_t key0, key1, tok0, tok1, hist, part, bytes;
+};
+inline RowScratch row_scratch(uint64_t count, uint64_t cols) {
+    RowScratch s;
+    const uint64_t list = align256(4 * count), chunks = (count + kSortChunk - 1) / kSortChunk;
+    const uint64_t tile = row_tile(count), tiles = (count + tile - 1) / tile;
+    s.key0 = 0;
+    s.key1 = list;
+    s.tok0 = 2 * list;
+    s.tok1 = 3 * list;
+    s.hist = 4 * list;
+    s.part = s.hist + align256(4ull * kSortDigits * chunks);
+    s.bytes = s.part + align256(8 * tiles * cols);
+    return s;
+}
+
 // Shift sample of a compressed tensor: the values at floor(i * n / m), i < m.
 struct SampleParams {
     const uint8_t *sf;
@@ -430,6 +524,12 @@ int launch_encode(const EncodeParams &p, void *stream, bool group = false);
 int launch_decode(const DecodeParams &p, void *stream, bool group = false);
 int launch_sgd(const SgdParams &p, void *stream, bool group = false);
 int launch_mom(const MomParams &p, void *stream, bool group = false);
+int launch_mix(const MixParams &p, void *stream, bool group = false);
+int launch_rows(const RowsParams &p, void *stream);
+// A table's gradient (rows.hip).
+int launch_row_sort(SortParams p, const RowScratch &s, uint8_t *scratch, const uint32_t **key, const uint32_t **token,
+                    void *stream);
+int launch_row_grad(const RowGradParams &p, uint32_t from, uint32_t to, void *stream);
 int launch_gather(const uint16_t *x, uint64_t n, uint32_t m, void *stream, uint16_t *host_out);
 // The shift sample of a compressed tensor, copied to host_out; synchronises.
 int launch_sample(const SampleParams &p, void *stream, uint16_t *host_out);
