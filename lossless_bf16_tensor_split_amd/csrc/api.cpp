@@ -702,7 +702,9 @@ bool ortho_coef_ok(const float (&coef)[3], uint32_t steps) {
     return true;
 }
 
-uint64_t ortho_bytes(uint64_t mp, uint64_t np) { return 2 * (4 * mp * np + 3 * mp * mp); }
+uint64_t ortho_bytes(uint64_t mp, uint64_t np, bool pairs) {
+    return 2 * ((pairs ? 6 : 4) * mp * np + (pairs ? 4 : 3) * mp * mp);
+}
 
 // Batches of matrices, in list order: f(p, b, bytes) with the matrices' sizes
 // and places in the working memory; the other fields are the caller's.  Stops
@@ -724,6 +726,7 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
             o.n = (uint32_t)std::max(r, c);
             o.type = (uint32_t)x.type[k];
             o.tall = r > c;
+            o.pairs = o.m <= kOrthoPairs;
             o.index = k;
             o.x = x.d_x[k];
         }
@@ -752,7 +755,7 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
             const uint64_t r = b.tile / kOrthoSmall;   // a large tile is two wide ones
             b.sym_tiles += (uint32_t)(mt * (mt + 1) / 2 * r);
             b.next_tiles += (uint32_t)(mt * nt * r);
-            bytes += ortho_bytes(o.mp, o.np);
+            bytes += ortho_bytes(o.mp, o.np, o.pairs);
         }
         const lct_status st = f(p, b, bytes);
         if (st != LCT_OK) return st;

@@ -460,7 +460,9 @@ inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
 // kernel arguments.  A matrix has m rows and n >= m columns (`tall`: the
 // caller's is the transpose), padded to mp and np, whole tiles; its working
 // memory starts at byte `off`: X as a pair, two copies of its transpose, A as a
-// pair, B, all FP16.
+// pair, B, all FP16; for short matrices (m at most kOrthoPairs) then the low
+// parts of B and of X' too.
+constexpr uint32_t kOrthoPairs = 256;
 constexpr uint32_t kOrthoMax = 32;        // matrices per launch
 constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;   // tiles
 constexpr uint32_t kOrthoLargeFrom = 200;                  // large tiles of a batch from which on they are taken
@@ -479,7 +481,7 @@ struct OrthoMat {
     void *y;
     uint64_t off;
     uint32_t m, n, mp, np;
-    uint32_t type, tall, index;   // index: in the whole list (its norm's place)
+    uint32_t type, tall, pairs, index;   // pairs: every operand is one; index: in the whole list (its norm's place)
     float scale;
     uint32_t prep0, sym0, next0;  // first tile of each kind of launch
 };

@@ -18,8 +18,9 @@
 //   - sums are FP32 throughout.
 // X's high part alone enters the products X X' and B X, and B is one FP16
 // number: those roundings act within the rows that X has.  The result is then
-// 1.7e-3 to 2.3e-3 off the exact one (norms), of which rounding it to BF16
-// makes 1.66e-3.
+// 1.7e-3 to 2.2e-3 off the exact one (norms), of which rounding it to BF16
+// makes 1.66e-3.  Of short matrices, whose few elements leave 2.4e-3 to 5e-3,
+// every operand is a pair and every product three: 1.66e-3 to 1.9e-3.
 //
 // Layout.  Every operand of a product is read along its rows: X X' from X,
 // A A from A (symmetric), and B X from B and X transposed, of which a copy is
@@ -44,6 +45,7 @@ typedef __attribute__((address_space(1))) const uint8_t glb_u8;
 // Where a matrix's parts lie in the working memory (elements of FP16).
 struct Parts {
     f16 *xh, *xl, *xt0, *xt1, *ah, *al, *bh;
+    f16 *xtl0, *xtl1, *bl;   // low parts of X' and B, where every operand is a pair
 };
 __device__ __forceinline__ Parts parts_of(uint8_t *scratch, const OrthoMat &o) {
     f16 *p = reinterpret_cast<f16 *>(scratch + o.off);
@@ -56,6 +58,9 @@ __device__ __forceinline__ Parts parts_of(uint8_t *scratch, const OrthoMat &o) {
     r.ah = p + 4 * x;
     r.al = r.ah + a;
     r.bh = r.al + a;
+    r.bl = r.bh + a;
+    r.xtl0 = r.bl + a;
+    r.xtl1 = r.xtl0 + x;
     return r;
 }
 
@@ -84,8 +89,8 @@ __global__ __launch_bounds__(256) void k_ortho_prep(const OrthoParams p) {
     const uint32_t k = matrix_of(p, blockIdx.x, [](const OrthoMat &o) { return o.prep0; });
     const OrthoMat &o = p.mat[k];
     const Parts w = parts_of(p.scratch, o);
-    const uint32_t t = blockIdx.x - o.prep0, nt = o.np / kPrepTile;
-    const uint32_t i0 = t / nt * kPrepTile, j0 = t % nt * kPrepTile;
+    const uint32_t tl = blockIdx.x - o.prep0, nt = o.np / kPrepTile;
+    const uint32_t i0 = tl / nt * kPrepTile, j0 = tl % nt * kPrepTile;
     const float norm = p.norm[o.index];
     const float inv = norm <= 3.0e38f ? (float)(p.xscale / ((double)norm + 1e-7)) : __builtin_nanf("");
     const uint32_t c = threadIdx.x % 64, r0 = threadIdx.x / 64;
@@ -107,7 +112,10 @@ __global__ __launch_bounds__(256) void k_ortho_prep(const OrthoParams p) {
         const uint64_t at = (uint64_t)(i0 + r) * o.np + j0 + c;
         w.xh[at] = h;
         w.xl[at] = (f16)(v - (float)h);
-        w.xt0[(uint64_t)(j0 + r) * o.mp + i0 + c] = (f16)tile[c][r];
+        const uint64_t t = (uint64_t)(j0 + r) * o.mp + i0 + c;
+        const float u = tile[c][r];
+        w.xt0[t] = (f16)u;
+        if (o.pairs) w.xtl0[t] = (f16)(u - (float)(f16)u);
     }
 }
 
@@ -152,20 +160,20 @@ struct Product {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // Pairs of operands (p[s], q[s]), each of `steps` steps, summed.
-    template <uint32_t SEGS>
-    __device__ __forceinline__ void run(const f16 *const (&p)[SEGS], const f16 *const (&q)[SEGS], uint32_t steps,
-                                        uint64_t ld, uint8_t *lds) {
+    // P Q' over `steps` steps; with three segments, P and Q being the first of
+    // pairs, P Q' + P Ql' + Pl Q'.
+    __device__ __forceinline__ void run(const f16 *ph, const f16 *pl, const f16 *qh, const f16 *ql, uint32_t segs,
+                                        uint32_t steps, uint64_t ld, uint8_t *lds) {
         const uint32_t l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
         for (uint32_t a = 0; a < FP; ++a)
 #pragma unroll
             for (uint32_t b = 0; b < FQ; ++b) acc[a][b] = f32x16{0.0f};
-        const uint32_t total = SEGS * steps;
+        const uint32_t total = segs * steps;
         // a load: 16 rows of 64 bytes, a lane's row and (exchanged) piece
         const uint32_t ldb = 2 * (uint32_t)ld;   // (T rows span less than 2^32 bytes)
         const uint32_t mine = (16 * w + (l >> 2)) * ldb + 16 * ((l & 3) ^ (l >> 4));
-        __amdgpu_buffer_rsrc_t rp = rsrc(p[0], ldb), rq = rsrc(q[0], ldb);
+        __amdgpu_buffer_rsrc_t rp = rsrc(ph, ldb), rq = rsrc(qh, ldb);
         uint32_t at = 0, seg = 0;   // the next load's step of its segment, in bytes
         auto load = [&](bool side, uint32_t it, uint8_t *buf) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(side ? rq : rp,
@@ -174,11 +182,10 @@ struct Product {
         };
         auto next_step = [&]() {
             at += kRowB;
-            if (SEGS > 1 && at == steps * kRowB) {
+            if (at == steps * kRowB && ++seg < segs) {
                 at = 0;
-                ++seg;
-                rp = rsrc(p[seg == 1 ? 1 % SEGS : 2 % SEGS], ldb);
-                rq = rsrc(q[seg == 1 ? 1 % SEGS : 2 % SEGS], ldb);
+                rp = rsrc(seg == 1 ? ph : pl, ldb);
+                rq = rsrc(seg == 1 ? ql : qh, ldb);
             }
         };
         const uint32_t pr = ((w >> 1) * SP + (l & 31)) * kRowB, qr = ((w & 1) * SQ + (l & 31)) * kRowB + kSide;
@@ -417,9 +424,9 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const
     const uint64_t ld = SQUARE ? o.mp : o.np, i0 = ti * TP * ld, j0 = tj * TQ * ld;
     Product<TP, TQ, NB> pr;
     if constexpr (SQUARE)
-        pr.template run<3>({w.ah + i0, w.ah + i0, w.al + i0}, {w.ah + j0, w.al + j0, w.ah + j0}, o.mp / kStep, ld, smem);
+        pr.run(w.ah + i0, w.al + i0, w.ah + j0, w.al + j0, 3, o.mp / kStep, ld, smem);
     else
-        pr.template run<1>({w.xh + i0}, {w.xh + j0}, o.np / kStep, ld, smem);
+        pr.run(w.xh + i0, w.xl + i0, w.xh + j0, w.xl + j0, o.pairs ? 3 : 1, o.np / kStep, ld, smem);
     // this wave's part: rows pi.. of P (of A), pj.. of Q
     const uint32_t wv = threadIdx.x >> 6;
     const uint64_t pi = ti * TP + (wv >> 1) * (TP / 2), pj = tj * TQ + (wv & 1) * (TQ / 2);
@@ -434,6 +441,10 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const
         pr.add_along(w.al + along, o.mp, p.ka, smem);
         pr.template store<true>(w.bh + along, o.mp, smem, high);
         if (mirror) pr.template store<false>(w.bh + across, o.mp, smem, high);
+        if (o.pairs) {
+            pr.template store<true>(w.bl + along, o.mp, smem, low);
+            if (mirror) pr.template store<false>(w.bl + across, o.mp, smem, low);
+        }
     } else {
         pr.template store<true>(w.ah + along, o.mp, smem, high);
         pr.template store<true>(w.al + along, o.mp, smem, low);
@@ -455,7 +466,8 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_next(cons
     const uint32_t t = tile - o.next0, mt = o.mp / TQ;
     const uint64_t i0 = t % mt * TQ, j0 = t / mt * TP;
     Product<TP, TQ, NB> pr;
-    pr.template run<1>({(p.turn ? w.xt1 : w.xt0) + j0 * o.mp}, {w.bh + i0 * o.mp}, o.mp / kStep, o.mp, smem);
+    pr.run((p.turn ? w.xt1 : w.xt0) + j0 * o.mp, (p.turn ? w.xtl1 : w.xtl0) + j0 * o.mp, w.bh + i0 * o.mp,
+           w.bl + i0 * o.mp, o.pairs ? 3 : 1, o.mp / kStep, o.mp, smem);
     const uint32_t wv = threadIdx.x >> 6;
     const uint64_t pj = j0 + (wv >> 1) * (TP / 2), pi = i0 + (wv & 1) * (TQ / 2);
     const uint64_t along = pi * o.np + pj, across = pj * o.mp + pi;
@@ -469,6 +481,7 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_next(cons
         pr.template store<true>(w.xh + along, o.np, smem, high);
         pr.template store<true>(w.xl + along, o.np, smem, low);
         pr.template store<false>((p.turn ? w.xt0 : w.xt1) + across, o.mp, smem, high);
+        if (o.pairs) pr.template store<false>((p.turn ? w.xtl0 : w.xtl1) + across, o.mp, smem, low);
         return;
     }
     const float scale = o.scale;
