@@ -587,7 +587,9 @@ lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float
  * lct_tensor_rows: y_t = scale * W[index_t] (the product in fp32, rounded to y's
  * type), W a compressed tensor of n = rows * cols elements (or a group's member,
  * lct_group_tensor) decoded with cb.  A code is found only through its stream
- * from the start, so a row costs the decoding of its block up to the row.
+ * from the start, so a row costs the decoding of its block up to the row; with
+ * d_scratch (lct_rows_scratch(count, 0) bytes, as below; may be null) many
+ * tokens are sorted, and share what they decode of a block.
  *
  * lct_rows_grad: G[v] = scale * (sum of dy_t over the t with index_t = v), for
  * every row of G, those without a token becoming zero; with add, added to what
@@ -596,7 +598,8 @@ lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float
  * lct_rows_scratch(count, cols) bytes of device memory, 256-byte aligned, shared
  * only by calls that do not overlap in time. */
 lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t cols, const void *d_index,
-                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *stream);
+                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *d_scratch,
+                           void *stream);
 lct_status lct_rows_scratch(uint64_t count, uint64_t cols, uint64_t *bytes);
 lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, const void *d_dy, int32_t dy_type,
                          uint64_t rows, uint64_t cols, float scale, int32_t add, void *d_g, int32_t g_type,

@@ -160,7 +160,7 @@ def _load():
     L.lct_momentum_step_clip_group.argtypes = [G, T, G, T, G, P, f32, f32, T, T, P]
     L.lct_mix_step.argtypes = [CB, T, f32, P, f32, P, CB, T, P, i32, P]
     L.lct_mix_step_group.argtypes = [G, T, f32, G, f32, P, T, G, i32, P]
-    L.lct_tensor_rows.argtypes = [CB, T, u64, P, i32, u64, f32, P, i32, P]
+    L.lct_tensor_rows.argtypes = [CB, T, u64, P, i32, u64, f32, P, i32, P, P]
     L.lct_rows_scratch.argtypes = [u64, u64, C.POINTER(u64)]
     L.lct_rows_grad.argtypes = [P, i32, u64, P, i32, u64, u64, f32, i32, P, i32, P, P]
     L.lct_orthogonal_scratch.argtypes = [LI, P, C.POINTER(u64)]
@@ -990,11 +990,22 @@ def lct_mix_step_group(g: LctGroup, y_all: LctTensor, a: float, gx: LctGroup, b:
 # ------------------------------------------------------------------ tables looked up by rows
 
 class RowsWork:
-    """Working memory of ``lct_rows_grad`` (kept between calls; shared only by
-    calls that do not overlap in time)."""
+    """Working memory of ``lct_tensor_rows`` and ``lct_rows_grad`` (kept between
+    calls; shared only by calls that do not overlap in time)."""
 
     def __init__(self, scratch: torch.Tensor):
         self.scratch = scratch
+
+    def _for(self, count: int, cols: int) -> torch.Tensor:
+        """The memory, once it is found fit for so many indices and columns."""
+        scr = self.scratch
+        _current(scr.device, "the working memory")
+        need = C.c_uint64(0)
+        _check(lib.lct_rows_scratch(count, cols, C.byref(need)), "lct_rows_scratch")
+        if not scr.is_contiguous() or scr.numel() * scr.element_size() < need.value:
+            raise ValueError("the working memory holds %d bytes; the call needs %d"
+                             % (scr.numel() * scr.element_size(), need.value))
+        return scr
 
 
 def alloc_rows(count: int, cols: int = 0, device="cuda") -> RowsWork:
@@ -1032,15 +1043,17 @@ def _matrix(t: torch.Tensor, rows: int | None, what: str) -> int:
 def lct_tensor_rows(cb: Codebook, t: LctTensor, index: torch.Tensor, y: torch.Tensor, work: RowsWork | None = None,
                     scale: float = 1.0, stream=None) -> None:
     """y[k] = scale * row index[k] of the table t (rows of y's last dimension;
-    zeros for an index outside it)."""
+    zeros for an index outside it).  With work, tokens of a long batch share
+    what they decode."""
     wide, ty = _index(index), _matrix(y, index.numel(), "y")
     cols = y.shape[-1]
     if cols == 0 or t.n % cols:
         raise ValueError("the table's %d elements are no whole rows of %d" % (t.n, cols))
     _current(t.sf.device, "the table")
+    scr = None if work is None else work._for(index.numel(), 0)
     ct = t.c(need_scratch=False)
     _check(lib.lct_tensor_rows(C.byref(cb), C.byref(ct), cols, _ptr(index), wide, index.numel(), scale, _ptr(y), ty,
-                               _stream(stream)), "lct_tensor_rows")
+                               _ptr(scr), _stream(stream)), "lct_tensor_rows")
 
 
 def lct_rows_grad(index: torch.Tensor, dy: torch.Tensor, g: torch.Tensor, work: RowsWork, scale: float = 1.0,
@@ -1051,13 +1064,7 @@ def lct_rows_grad(index: torch.Tensor, dy: torch.Tensor, g: torch.Tensor, work: 
     ty, tg = _matrix(dy, index.numel(), "dy"), _matrix(g, None, "g")
     if g.dim() != 2 or g.shape[1] != dy.shape[-1]:
         raise ValueError("g has the shape %s, dy's rows %d columns" % (tuple(g.shape), dy.shape[-1]))
-    scr = work.scratch
-    _current(scr.device, "the working memory")
-    need = C.c_uint64(0)
-    _check(lib.lct_rows_scratch(index.numel(), g.shape[1], C.byref(need)), "lct_rows_scratch")
-    if not scr.is_contiguous() or scr.numel() * scr.element_size() < need.value:
-        raise ValueError("the working memory holds %d bytes; the gradient needs %d"
-                         % (scr.numel() * scr.element_size(), need.value))
+    scr = work._for(index.numel(), g.shape[1])
     _check(lib.lct_rows_grad(_ptr(index), wide, index.numel(), _ptr(dy), ty, g.shape[0], g.shape[1], scale, bool(add),
                              _ptr(g), tg, _ptr(scr), _stream(stream)), "lct_rows_grad")
 

@@ -1574,6 +1574,17 @@ lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float
 
 // ---- rows of a compressed table, and their gradient
 
+static int sort_rows(const void *index, int32_t wide, uint64_t count, uint64_t rows, const RowScratch &s,
+                     void *scratch, const uint32_t **key, const uint32_t **token, void *stream) {
+    SortParams q;
+    memset(&q, 0, sizeof q);
+    q.index = index;
+    q.count = (uint32_t)count;
+    q.rows = (uint32_t)rows;
+    q.wide = wide != 0;
+    return launch_row_sort(q, s, static_cast<uint8_t *>(scratch), key, token, stream);
+}
+
 static bool type_ok(int32_t t) { return t == LCT_BF16 || t == LCT_FP16 || t == LCT_FP32; }
 
 lct_status lct_rows_scratch(uint64_t count, uint64_t cols, uint64_t *bytes) {
@@ -1583,7 +1594,8 @@ lct_status lct_rows_scratch(uint64_t count, uint64_t cols, uint64_t *bytes) {
 }
 
 lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t cols, const void *d_index,
-                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *stream) {
+                           int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *d_scratch,
+                           void *stream) {
     if (!cb || !t || !tables_ok(*cb) || cols == 0 || cols > kMaxCols || count > kMaxTokens || !type_ok(type))
         return LCT_EINVAL;
     if (!layout_ok(t->layout) || t->n % cols || t->n / cols > kMaxRows) return LCT_EINVAL;
@@ -1594,9 +1606,12 @@ lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t
     }
     if (!d_index || !d_y) return LCT_EINVAL;
     if (!aligned(d_index, wide ? 8 : 4) || !aligned(d_y, type_bytes(type))) return LCT_EALIGN;
-    const Range y = rng(d_y, count * cols * type_bytes(type));
-    if (overlap(y, rng(d_index, count * (wide ? 8 : 4))) || (t->n > 0 && overlaps_any(y, parts(*t), false)))
-        return LCT_EALIAS;
+    if (!aligned(d_scratch, 256)) return LCT_EALIGN;
+    const RowScratch s = row_scratch(count, 0);
+    const Range y = rng(d_y, count * cols * type_bytes(type)), idx = rng(d_index, count * (wide ? 8 : 4));
+    const Range scr = rng(d_scratch, d_scratch ? s.bytes : 0);
+    if (overlap(y, idx) || overlap(y, scr) || overlap(scr, idx)) return LCT_EALIAS;
+    if (t->n > 0 && (overlaps_any(y, parts(*t), false) || overlaps_any(scr, parts(*t), false))) return LCT_EALIAS;
     const lct_status st = check_arch();
     if (st != LCT_OK) return st;
     RowsParams p;
@@ -1619,7 +1634,16 @@ lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t
     p.y = d_y;
     p.scale = scale;
     fill_dec(*cb, &p.dec);
-    const int e = launch_rows(p, stream);
+    int e = hipSuccess;
+    p.run = 1;
+    p.piece = (uint32_t)std::min<uint64_t>((cols + 15) / 16 * 16, kRowsRoom);
+    if (d_scratch && count >= kRowsSortFrom) {
+        for (uint32_t r = kRowsRun; r > 1 && p.run == 1; r /= 2)
+            if (r * p.piece <= kRowsRoom) p.run = r;
+        e = sort_rows(d_index, wide, count, p.rows, s, d_scratch, &p.key, &p.token, stream);
+        if (e != hipSuccess) return hip_fail(e, "sort launch");
+    }
+    e = launch_rows(p, stream);
     return e == hipSuccess ? LCT_OK : hip_fail(e, "rows launch");
 }
 
@@ -1644,13 +1668,7 @@ lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, cons
     RowGradParams p;
     memset(&p, 0, sizeof p);
     if (count > 0) {
-        SortParams q;
-        memset(&q, 0, sizeof q);
-        q.index = d_index;
-        q.count = (uint32_t)count;
-        q.rows = (uint32_t)rows;
-        q.wide = wide != 0;
-        const int e = launch_row_sort(q, s, scratch, &p.key, &p.token, stream);
+        const int e = sort_rows(d_index, wide, count, rows, s, d_scratch, &p.key, &p.token, stream);
         if (e != hipSuccess) return hip_fail(e, "sort launch");
     }
     p.dy = d_dy;

@@ -2907,11 +2907,18 @@ constexpr uint32_t kMixWaves = 4;
 constexpr uint32_t kMixETab = 0, kMixDTab = 2048, kMixWave0 = 3072;
 __host__ __device__ constexpr uint32_t mix_wave_bytes(uint32_t cap) { return (cap + 2) * ROWB; }
 
+// Named as global memory: a group's pointers come from its table, and the
+// compiler would make their accesses flat ones, whose loads every wait for LDS
+// waits for.
+typedef __attribute__((address_space(1))) uint16_t glb_u16;
+__device__ __forceinline__ glb_u16 *global16(const uint16_t *p) {
+    return reinterpret_cast<glb_u16 *>(reinterpret_cast<uintptr_t>(p));
+}
 struct MixUnit {
     const uint8_t *sf;     // the unit's first element in each array
     uint8_t *o_sf;
-    const uint16_t *x;
-    uint16_t *d;
+    glb_u16 *x;
+    glb_u16 *d;
     uint64_t sp0;          // this lane's first spilled field
     uint32_t n_s, c_s;     // its positions, and how many of them are coded
 };
@@ -2925,7 +2932,7 @@ __device__ __forceinline__ void mix_stream(const MixParams &p, Reader &rd, uint3
     const uint32_t capbits = 32 * cap_of<CAPT>(p.cap_words);
     const int32_t qmax = Reader::bias(row0) + (int32_t)capbits - 2;
     const uint8_t *sfs = u.sf + s;
-    const uint16_t *xs = u.x + s;
+    glb_u16 *xs = u.x + s;
     uint64_t *ctr = reinterpret_cast<uint64_t *>(p.scratch + kScrStage);
     uint8_t *stage = p.scratch + scr_stage_offset(p.nblk);
     const float a = p.a;
@@ -2972,7 +2979,7 @@ __device__ __forceinline__ void mix_stream(const MixParams &p, Reader &rd, uint3
                 }
             }
             uint8_t *o = u.o_sf + s + (size_t)j0 * NS;
-            uint16_t *d = D ? u.d + s + (size_t)j0 * NS : nullptr;
+            glb_u16 *d = D ? u.d + s + (size_t)j0 * NS : nullptr;
 #pragma unroll
             for (uint32_t i = 0; i < CH; ++i) {
                 const uint32_t bx = __float_as_uint(bc * __uint_as_float(bf.x[i] << 16));
@@ -3008,12 +3015,12 @@ __global__ __launch_bounds__(64 * kMixWaves) void k_mix(const MixParams p) {
     BlockSpan sp;
     if (GROUP) {
         sp = group_span(p.g, k, p.block_elems, b);
-        m.x = group_span(p.gx, k, p.block_elems, b).dense + h * US;
-        m.d = D ? group_span(p.gd, k, p.block_elems, b).dense + h * US : nullptr;
+        m.x = global16(group_span(p.gx, k, p.block_elems, b).dense + h * US);
+        m.d = D ? global16(group_span(p.gd, k, p.block_elems, b).dense + h * US) : nullptr;
     } else {
         sp = flat_span(const_cast<uint16_t *>(p.x), p.n, p.block_elems, b);
-        m.x = sp.dense + h * US;
-        m.d = D ? p.d + sp.sf0 + h * US : nullptr;
+        m.x = global16(sp.dense + h * US);
+        m.d = D ? global16(p.d + sp.sf0 + h * US) : nullptr;
     }
     const uint32_t nb = sp.nb;
     m.sf = p.sf + sp.sf0 + h * US;
@@ -3045,89 +3052,185 @@ __global__ __launch_bounds__(64 * kMixWaves) void k_mix(const MixParams p) {
 
 // ------------------------------------------------------------------ rows of a compressed table
 
-// One row of the table for every index, a workgroup each, a lane per stream:
-// the streams of the row's block are decoded from their start to the row's
-// last position (a code can be found in no other way), and what lies in the row
-// is scaled and stored.  A row that crosses blocks takes them in turn.
+// Rows of the table for the indices, a lane per stream: the streams of a row's
+// block are decoded from their start to the row's last position (a code can be
+// found in no other way), and the exponents of what lies in the row go to LDS.
+// When all are there, they meet their sign-fraction bytes, are scaled and
+// stored, 16 neighbours a thread: with loads and stores in the decoder's loop,
+// every load would wait for the stores before it.
 //
-// LDS: decode table, then per wave the block's rows between two zero rows.
-template <uint32_t CAPT>
+// In the order of the indices a workgroup does one of them.  Of many tokens
+// (p.key: their rows, sorted, and p.token) it takes the neighbours whose rows
+// begin in one block, at most p.run of them: it goes on decoding from row to
+// row, and a row that several want is decoded once.  A row longer than the
+// room for it is done in pieces (p.run is 1 then).
+//
+// LDS: decode table, then per wave the block's rows between two zero rows, then
+// the exponents, p.piece bytes for each of p.run rows.
+template <uint32_t CAPT, int TYPE, bool SORTED>
 __global__ __launch_bounds__(64 * kDecWaves) void k_rows(const RowsParams p) {
-    const uint64_t t = blockIdx.x + (uint64_t)gridDim.x * blockIdx.y;
-    if (t >= p.count) return;
-    const int64_t r = p.wide ? static_cast<const int64_t *>(p.index)[t] : static_cast<const int32_t *>(p.index)[t];
-    const uint64_t y0 = t * p.cols;
-    auto put = [&](uint64_t i, float v) {
-        if (p.type == LCT_FP32)
-            static_cast<float *>(p.y)[i] = v;
-        else if (p.type == LCT_FP16)
-            static_cast<_Float16 *>(p.y)[i] = (_Float16)v;
-        else
-            static_cast<__bf16 *>(p.y)[i] = (__bf16)v;
-    };
-    if (r < 0 || (uint64_t)r >= p.rows) {
-        for (uint64_t i = threadIdx.x; i < p.cols; i += 64 * kDecWaves) put(y0 + i, 0.0f);
-        return;
+    using out_t = std::conditional_t<TYPE == LCT_FP32, float, std::conditional_t<TYPE == LCT_FP16, _Float16, __bf16>>;
+    constexpr uint32_t T = 64 * kDecWaves;
+    uint64_t t = blockIdx.x + (uint64_t)gridDim.x * blockIdx.y;
+    if (SORTED) {
+        // the first tokens of all runs of p.run first, then the second, ...:
+        // most of the work is theirs, and neighbouring workgroups are on
+        // different XCDs (in the tokens' order all of it went to one)
+        const uint64_t runs = (p.count + p.run - 1) / p.run;
+        t = t % runs * p.run + t / runs;
+        if (blockIdx.x + (uint64_t)gridDim.x * blockIdx.y >= runs * p.run) return;
     }
-    stage_dec(p.dec, kDecTab);
+    if (t >= p.count) return;
     const uint32_t l = lane(), h = wave_id(), s = h * US + l;
+    auto zeros = [&](uint64_t token) {
+        out_t *y = static_cast<out_t *>(p.y) + token * p.cols;
+        for (uint64_t i = threadIdx.x; i < p.cols; i += T) y[i] = (out_t)0.0f;
+    };
+    // the rows and tokens that this workgroup does: lanes 0 .. todo - 1
+    uint32_t key = 0xFFFFFFFFu, token = (uint32_t)t, todo = 1;
+    if (SORTED) {
+        const uint32_t q = (uint32_t)(t % p.run);
+        const uint64_t i = t - q + l;
+        const bool have = l < p.run && i < p.count;
+        key = have ? p.key[i] : 0xFFFFFFFFu;
+        token = have ? p.token[i] : 0u;
+        const uint32_t blk = key < p.rows ? (uint32_t)(key * p.cols / p.block_elems) : 0xFFFFFFFFu;
+        const uint32_t mine = (uint32_t)__builtin_amdgcn_readlane((int)blk, (int)q);
+        if (mine == 0xFFFFFFFFu) return zeros((uint32_t)__builtin_amdgcn_readlane((int)token, (int)q));
+        const uint64_t alike = __ballot(blk == mine);   // neighbours, the keys being sorted
+        if (q && (alike >> (q - 1) & 1)) return;
+        todo = __popcll(alike);
+        key = __shfl(key, q + l, 64);
+        token = __shfl(token, q + l, 64);
+        if (l >= todo) key = 0xFFFFFFFFu;
+    } else {
+        const int64_t r = p.wide ? static_cast<const int64_t *>(p.index)[t] : static_cast<const int32_t *>(p.index)[t];
+        if (r < 0 || (uint64_t)r >= p.rows) return zeros(t);
+        key = (uint32_t)r;
+    }
+    // a place for each different row
+    const uint32_t before = __shfl_up(key, 1, 64);
+    const uint64_t heads = __ballot(l < todo && (l == 0 || before != key));
+    const uint32_t place = __popcll(heads & ((2ull << l) - 1)) - 1;
     const uint32_t cap = cap_of<CAPT>(p.cap_words);
     const uint32_t base = kDecWave0 + h * dec_wave_bytes(cap), row0 = base + ROWB;
+    const uint32_t exps = kDecWave0 + kDecWaves * dec_wave_bytes(cap);
+    stage_dec(p.dec, kDecTab);
     st32(base + 4 * l, 0);                      // row -1
     st32(row0 + cap * ROWB + 4 * l, 0);         // row cap
     __syncthreads();
     const int32_t qmax = Reader::bias(row0) + 32 * (int32_t)cap - 2;
-    const uint64_t first = (uint64_t)r * p.cols, last = first + p.cols;   // the row's elements
-    for (uint64_t at = first; at < last;) {
-        const uint32_t b = (uint32_t)(at / p.block_elems);
-        const uint64_t b0 = (uint64_t)b * p.block_elems;
-        const uint32_t nb = (uint32_t)min<uint64_t>(p.block_elems, p.n - b0);
-        const uint32_t lo = (uint32_t)(at - b0), hi = (uint32_t)min<uint64_t>(nb, last - b0);
-        rows_to_lds<false>(p.pay, row0, nullptr, 0, b, h, cap);
+    Reader rd;
+    uint64_t held = ~0ull;     // the block in LDS
+    uint32_t nb = 0, c_s = 0;  // its length, and what of this lane's stream is coded
+    uint64_t sp0 = 0;          // this lane's first spilled field
+    uint32_t j = 0;            // the next four positions to decode,
+    int32_t q_last = 0;        // and where the reader was before the last four
+    auto open = [&](uint64_t b) {
+        if (b == held) return;
+        held = b;
+        nb = (uint32_t)min<uint64_t>(p.block_elems, p.n - b * p.block_elems);
+        rows_to_lds<false>(p.pay, row0, nullptr, 0, (uint32_t)b, h, cap);
         const uint64_t ob0 = p.obase[b], ob1 = p.obase[b + 1];
-        uint32_t c_s = stream_len(nb, s), excl = 0;
-        if (ob0 != ob1) unit_spills(p.cnt + (uint64_t)b * NS, nb, h, c_s, excl);
-        const uint64_t sp0 = ob0 + excl;
-        Reader rd;
+        uint32_t excl = 0;
+        c_s = stream_len(nb, s);
+        if (ob0 != ob1) unit_spills(p.cnt + b * NS, nb, h, c_s, excl);
+        sp0 = ob0 + excl;
         rd.init(row0, l);
-        // positions before the row's first in any stream are passed over,
-        // four to a window
-        const uint32_t j0 = lo / NS / 4 * 4, j1 = (hi - 1) / NS + 1;
-        auto four = [&](uint32_t (&f)[4]) {
-            const int32_t q0 = rd.q;
-            const uint32_t c = rd.next_n<4>(kDecTab, qmax, f);
-            if (__builtin_expect(!wave_all(c <= 30), 0)) {
-                rd.q = q0;
-#pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) {
-                    f[k] = rd.next(kDecTab);
-                    rd.q = min(rd.q, qmax);
-                }
-            }
-        };
-        uint32_t f[4];
-        for (uint32_t j = 0; j < j0; j += 4) four(f);
-        for (uint32_t j = j0; j < j1; j += 4) {
-            uint32_t sf[4];
-            bool in[4];
+        j = 0;
+    };
+    auto four = [&](uint32_t (&f)[4]) {
+        q_last = rd.q;
+        const uint32_t c = rd.next_n<4>(kDecTab, qmax, f);
+        if (__builtin_expect(!wave_all(c <= 30), 0)) {
+            rd.q = q_last;
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
-                const uint32_t e = (j + k) * NS + s;
-                in[k] = e >= lo && e < hi;
-                sf[k] = in[k] ? p.sf[b0 + e] : 0u;
-            }
-            four(f);
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                if (!in[k]) continue;
-                if (j + k >= c_s) {
-                    const uint64_t i = sp0 + (j + k - c_s);
-                    f[k] = (i < p.ovf_cap ? (uint32_t)p.ovf[i] : 0u) << 23;
-                }
-                put(y0 + (b0 + (j + k) * NS + s - first), p.scale * __uint_as_float(join32(sf[k], f[k])));
+                f[k] = rd.next(kDecTab);
+                rd.q = min(rd.q, qmax);
             }
         }
-        at = b0 + hi;
+        j += 4;
+    };
+    // the exponents of elements [first, last) to LDS at `to`
+    auto decode = [&](uint64_t first, uint64_t last, uint32_t to) {
+        for (uint64_t at = first; at < last;) {
+            const uint64_t b = at / p.block_elems, b0 = b * p.block_elems;
+            open(b);
+            const uint32_t lo = (uint32_t)(at - b0), hi = (uint32_t)min<uint64_t>(nb, last - b0);
+            const uint32_t j0 = lo / NS & ~3u, j1 = (hi - 1) / NS + 1;
+            const uint32_t place0 = to + (uint32_t)(b0 - first);   // (of the block's element 0)
+            uint32_t f[4];
+            if (j > j0) {      // what was before ended in the same four: once more
+                j = j0;
+                rd.q = q_last;
+            }
+            while (j < j0) four(f);
+            while (j < j1) {
+                const uint32_t i0 = j;
+                four(f);
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const uint32_t e = (i0 + k) * NS + s;
+                    if (e < lo || e >= hi) continue;
+                    if (i0 + k >= c_s) {
+                        const uint64_t i = sp0 + (i0 + k - c_s);
+                        f[k] = (i < p.ovf_cap ? (uint32_t)p.ovf[i] : 0u) << 23;
+                    }
+                    st8(place0 + e, f[k] >> 23);
+                }
+            }
+            at = b0 + hi;
+        }
+    };
+    typedef u32x4 u32x4b __attribute__((aligned(1)));
+    for (uint64_t c0 = 0; c0 < p.cols; c0 += p.piece) {
+        const uint32_t len = (uint32_t)min<uint64_t>(p.piece, p.cols - c0);
+        uint64_t left = heads;
+        for (uint32_t k = 0; left; ++k, left &= left - 1) {
+            const uint64_t r = (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(left));
+            decode(r * p.cols + c0, r * p.cols + c0 + len, exps + k * p.piece);
+        }
+        __syncthreads();
+        const uint32_t chunks = (len + 15) / 16, total = todo * chunks;
+        for (uint32_t i0 = 0; i0 < total; i0 += T) {
+            const uint32_t i = i0 + threadIdx.x, u = min(i / chunks, todo - 1), c = (i - u * chunks) * 16;
+            const uint64_t r = __shfl(key, u, 64), tk = __shfl(token, u, 64);
+            const uint32_t from = exps + __shfl(place, u, 64) * p.piece + c;
+            if (i >= total) continue;
+            const uint8_t *sfp = p.sf + r * p.cols + c0 + c;
+            const uint32_t have = min(16u, len - c);
+            uint32_t sf[4] = {0, 0, 0, 0};
+            if (have == 16) {
+                const u32x4 v = *reinterpret_cast<const u32x4b *>(sfp);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sf[k] = v[k];
+            } else {
+#pragma unroll
+                for (uint32_t k = 0; k < 16; ++k)
+                    if (k < have) sf[k / 4] |= (uint32_t)sfp[k] << (8 * (k % 4));
+            }
+            const u32x4 ex = ld128(from);
+            out_t o[16];
+#pragma unroll
+            for (uint32_t k = 0; k < 16; ++k)
+                o[k] = (out_t)(p.scale * __uint_as_float(join32s(sf[k / 4], (ex[k / 4] >> (8 * (k % 4))) << 23,
+                                                                  byte_sel(k % 4))));
+            out_t *y = static_cast<out_t *>(p.y) + tk * p.cols + c0 + c;
+            if (have == 16) {
+                struct Out {
+                    u32x4 v[sizeof(o) / 16];
+                };
+                const Out w = __builtin_bit_cast(Out, o);
+#pragma unroll
+                for (uint32_t k = 0; k < sizeof(o) / 16; ++k) reinterpret_cast<u32x4b *>(y)[k] = w.v[k];
+            } else {
+#pragma unroll
+                for (uint32_t k = 0; k < 16; ++k)
+                    if (k < have) y[k] = o[k];
+            }
+        }
+        if (c0 + p.piece < p.cols) __syncthreads();
     }
 }
 
@@ -3321,15 +3424,24 @@ int launch_mix(const MixParams &p, void *stream, bool group) {
                   g_mix_lds_granted[d + (group ? 3 : 0)][cap_slot(cap)]);
 }
 
-template <uint32_t C> struct RowsK { static const void *fn() { return reinterpret_cast<const void *>(&k_rows<C>); } };
-std::atomic<size_t> g_rows_lds_granted[4];
+template <int TYPE, bool SORTED>
+struct RowsOf {
+    template <uint32_t C> struct K { static const void *fn() { return reinterpret_cast<const void *>(&k_rows<C, TYPE, SORTED>); } };
+    static const void *pick(uint32_t cap) { return ByCap<K>::pick(cap); }
+};
+std::atomic<size_t> g_rows_lds_granted[6][4];
 
 int launch_rows(const RowsParams &p, void *stream) {
-    const void *fn = ByCap<RowsK>::pick(p.cap_words);
-    const size_t lds = decode_lds(p.cap_words);
-    const int attr = ensure_lds(fn, lds, g_rows_lds_granted[cap_slot(p.cap_words)]);
+    const uint32_t cap = p.cap_words, which = 2 * p.type + (p.key ? 1 : 0);
+    const void *fns[6] = {RowsOf<LCT_BF16, false>::pick(cap), RowsOf<LCT_BF16, true>::pick(cap),
+                          RowsOf<LCT_FP16, false>::pick(cap), RowsOf<LCT_FP16, true>::pick(cap),
+                          RowsOf<LCT_FP32, false>::pick(cap), RowsOf<LCT_FP32, true>::pick(cap)};
+    const void *fn = fns[which];
+    const size_t lds = decode_lds(cap) + (size_t)p.run * p.piece;
+    const int attr = ensure_lds(fn, lds, g_rows_lds_granted[which][cap_slot(cap)]);
     if (attr != hipSuccess) return attr;
-    const uint64_t x = std::min<uint64_t>(p.count, 1u << 20), y = (p.count + x - 1) / x;
+    const uint64_t all = (p.count + p.run - 1) / p.run * p.run;
+    const uint64_t x = std::min<uint64_t>(all, 1u << 20), y = (all + x - 1) / x;
     void *args[] = {const_cast<RowsParams *>(&p)};
     const hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)x, (uint32_t)y), dim3(64 * kDecWaves), args, lds,
                                          (hipStream_t)stream);

@@ -267,16 +267,23 @@ struct RowsParams {
     uint64_t n, rows, cols, count;
     uint32_t block_elems, cap_words, wide, type;   // wide: 64-bit indices; type: the result's
     const void *index;
+    const uint32_t *key, *token;   // many tokens: their rows, sorted, and the tokens (null: in order, by index)
     void *y;
+    uint32_t run, piece;   // sorted tokens of a workgroup; bytes of LDS for a row's exponents (a multiple of 16)
     float scale;
     DecTab dec;
 };
+constexpr uint32_t kRowsRun = 16;          // sorted tokens that a workgroup takes at most,
+constexpr uint32_t kRowsRoom = 32768;      // and bytes of LDS for their exponents
+constexpr uint64_t kRowsSortFrom = 1024;   // tokens from which on they are sorted
 
 // The gradient of a table's rows (rows.hip).  Tokens are sorted by row in
 // passes of at most kSortBits bits over chunks of kSortChunk tokens, then
 // summed in tiles.
 constexpr uint32_t kSortBits = 9, kSortDigits = 1u << kSortBits;
 constexpr uint32_t kSortThreads = 256, kSortChunk = 1024;
+constexpr uint32_t kSortOne = 4096;                    // up to so many tokens one workgroup sorts them
+constexpr uint32_t kSortFew = 64;                      // chunks whose counts the placing kernel adds up itself
 constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 31, kMaxCols = 1ull << 24;
 constexpr uint32_t kRowTile = 16, kRowTileMax = 256;   // tokens of a tile: more where there are many
 constexpr uint64_t kRowTiles = 4096;
@@ -290,7 +297,7 @@ struct SortParams {
     const void *index;          // the first pass reads indices, the others keys
     const uint32_t *from, *from_token;
     uint32_t *to, *to_token, *hist;
-    uint32_t count, rows, wide, bits, shift, chunks;
+    uint32_t count, rows, wide, bits, shift, chunks, passes;
 };
 struct RowGradParams {
     const uint32_t *key, *token;   // sorted
@@ -314,7 +321,7 @@ inline RowScratch row_scratch(uint64_t count, uint64_t cols) {
     s.tok0 = 2 * list;
     s.tok1 = 3 * list;
     s.hist = 4 * list;
-    s.part = s.hist + align256(4ull * kSortDigits * chunks);
+    s.part = s.hist + align256(4ull * kSortDigits * (chunks + 1));
     s.bytes = s.part + align256(8 * tiles * cols);
     return s;
 }

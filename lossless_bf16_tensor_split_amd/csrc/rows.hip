@@ -48,27 +48,44 @@ __device__ __forceinline__ uint64_t alike(uint32_t digit, uint32_t bits, bool ha
     return m;
 }
 
-// A chunk's tokens of each digit: hist[digit][chunk].
+// A chunk's tokens of each digit: hist[chunk][digit].
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortParams p) {
     __shared__ uint32_t h[kSortDigits];
     const uint32_t digits = 1u << p.bits;
     for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) h[d] = 0;
     __syncthreads();
     const uint32_t i0 = blockIdx.x * kSortChunk;
-    for (uint32_t k = threadIdx.x; k < kSortChunk; k += kSortThreads)
-        if (i0 + k < p.count) atomicAdd(&h[key_of(p, i0 + k) >> p.shift & (digits - 1)], 1u);
+#pragma unroll
+    for (uint32_t k = 0; k < kSortChunk; k += kSortThreads) {
+        const uint32_t i = i0 + k + threadIdx.x;
+        if (i < p.count) atomicAdd(&h[key_of(p, i) >> p.shift & (digits - 1)], 1u);
+    }
     __syncthreads();
-    for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) p.hist[(uint64_t)d * p.chunks + blockIdx.x] = h[d];
+    for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) p.hist[blockIdx.x * kSortDigits + d] = h[d];
 }
 
-// hist's exclusive running sum, in place, by one workgroup: a run of
-// neighbours per thread.
-__global__ __launch_bounds__(1024) void k_sort_scan(uint32_t *hist, uint32_t n) {
-    __shared__ uint32_t s[16];
-    const uint32_t per = (n + 1023) / 1024, a = min(n, threadIdx.x * per), e = min(n, a + per);
+// Many chunks: each digit's running sum over the chunks, in place, its total
+// behind them (hist[chunks][digit]).
+__global__ __launch_bounds__(64) void k_sort_prefix(uint32_t *hist, uint32_t chunks) {
+    const uint32_t d = blockIdx.x * 64 + threadIdx.x;
     uint32_t sum = 0;
-    for (uint32_t i = a; i < e; ++i) sum += hist[i];
-    uint32_t inc = sum;
+    for (uint32_t c = 0; c < chunks; c += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) v[k] = c + k < chunks ? hist[(uint64_t)(c + k) * kSortDigits + d] : 0u;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            if (c + k < chunks) hist[(uint64_t)(c + k) * kSortDigits + d] = sum;
+            sum += v[k];
+        }
+    }
+    hist[(uint64_t)chunks * kSortDigits + d] = sum;
+}
+
+// v's exclusive running sum over the workgroup's threads (T of them).
+template <uint32_t T>
+__device__ __forceinline__ uint32_t group_scan(uint32_t v, uint32_t (&s)[T / 64]) {
+    uint32_t inc = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const uint32_t t = __shfl_up(inc, d, 64);
@@ -76,58 +93,162 @@ __global__ __launch_bounds__(1024) void k_sort_scan(uint32_t *hist, uint32_t n) 
     }
     if (lane() == 63) s[threadIdx.x >> 6] = inc;
     __syncthreads();
-    uint32_t at = inc - sum;
+    uint32_t at = inc - v;
     for (uint32_t w = 0; w < threadIdx.x >> 6; ++w) at += s[w];
-    for (uint32_t i = a; i < e; ++i) {
-        const uint32_t v = hist[i];
-        hist[i] = at;
-        at += v;
+    return at;
+}
+
+// Ranks of a wave's R keys a lane within their digits, h being the wave's
+// counts (cleared before, its totals after): 64 keys at a time, so that the
+// order within a digit stays.
+template <uint32_t R>
+__device__ __forceinline__ void ranks(const uint32_t (&key)[R], const bool (&have)[R], uint32_t shift, uint32_t bits,
+                                      uint32_t *h, uint32_t (&rank)[R]) {
+    const uint32_t l = lane();
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r) {
+        const uint32_t d = key[r] >> shift & ((1u << bits) - 1);
+        const uint64_t m = alike(d, bits, have[r]);
+        const uint32_t before = __popcll(m & ((1ull << l) - 1));
+        rank[r] = have[r] ? h[d] + before : 0u;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (have[r] && before == 0) h[d] += __popcll(m);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-// The chunk's tokens to their places: a wave takes a run of them, 64 at a
-// time, and counts its own digits before it, so that the order within a digit
-// stays.
+// The chunk's tokens to their places.
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(const SortParams p) {
-    constexpr uint32_t W = kSortThreads / 64, R = kSortChunk / kSortThreads;
+    constexpr uint32_t W = kSortThreads / 64, R = kSortChunk / kSortThreads, D = kSortDigits / kSortThreads;
     __shared__ uint32_t h[W][kSortDigits];
-    const uint32_t digits = 1u << p.bits, w = threadIdx.x >> 6, l = lane();
+    __shared__ uint32_t s[W];
+    const uint32_t w = threadIdx.x >> 6, l = lane();
     for (uint32_t d = threadIdx.x; d < W * kSortDigits; d += kSortThreads) (&h[0][0])[d] = 0;
-    __syncthreads();
-    const uint32_t i0 = blockIdx.x * kSortChunk + w * (R * 64);
-    uint32_t key[R], rank[R];
+    // this thread's digits, neighbours: all tokens of each, and those of the
+    // chunks before this one
+    const uint32_t digits = 1u << p.bits, d0 = threadIdx.x * D;
+    uint32_t all[D] = {}, mine[D] = {}, sum = 0;
+    if (d0 < digits) {
+        if (p.chunks <= kSortFew) {
+            for (uint32_t c = 0; c < p.chunks; c += 8) {
+                uint32_t v[8][D];
 #pragma unroll
-    for (uint32_t r = 0; r < R; ++r) {
-        const uint32_t i = i0 + r * 64 + l;
-        const bool have = i < p.count;
-        key[r] = have ? key_of(p, i) : 0u;
-        const uint32_t d = key[r] >> p.shift & (digits - 1);
-        const uint64_t m = alike(d, p.bits, have);
-        const uint32_t before = __popcll(m & ((1ull << l) - 1));
-        rank[r] = have ? h[w][d] + before : 0u;
-        __builtin_amdgcn_wave_barrier();
-        if (have && before == 0) h[w][d] += __popcll(m);
-        __builtin_amdgcn_wave_barrier();
-    }
-    __syncthreads();
-    // each wave's first place of each digit
-    for (uint32_t d = threadIdx.x; d < digits; d += kSortThreads) {
-        uint32_t at = p.hist[(uint64_t)d * p.chunks + blockIdx.x];
-        for (uint32_t k = 0; k < W; ++k) {
-            const uint32_t v = h[k][d];
-            h[k][d] = at;
-            at += v;
+                for (uint32_t k = 0; k < 8; ++k)
+#pragma unroll
+                    for (uint32_t e = 0; e < D; ++e)
+                        v[k][e] = c + k < p.chunks ? p.hist[(c + k) * kSortDigits + d0 + e] : 0u;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+#pragma unroll
+                    for (uint32_t e = 0; e < D; ++e) {
+                        if (c + k < blockIdx.x) mine[e] += v[k][e];
+                        all[e] += v[k][e];
+                    }
+            }
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < D; ++e) {
+                mine[e] = p.hist[(uint64_t)blockIdx.x * kSortDigits + d0 + e];
+                all[e] = p.hist[(uint64_t)p.chunks * kSortDigits + d0 + e];
+            }
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < D; ++e) {
+            if (d0 + e >= digits) all[e] = 0;
+            sum += all[e];
         }
     }
+    uint32_t at = group_scan<kSortThreads>(sum, s);   // (its barrier: h is cleared)
+    const uint32_t i0 = blockIdx.x * kSortChunk + w * (R * 64);
+    uint32_t key[R], rank[R];
+    bool have[R];
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r) {
+        const uint32_t i = i0 + r * 64 + l;
+        have[r] = i < p.count;
+        key[r] = have[r] ? key_of(p, i) : 0u;
+    }
+    ranks<R>(key, have, p.shift, p.bits, h[w], rank);
+    __syncthreads();
+    // each wave's first place of each digit
+#pragma unroll
+    for (uint32_t e = 0; e < D; ++e) {
+        if (d0 + e >= digits) break;
+        uint32_t to = at + mine[e];
+        for (uint32_t k = 0; k < W; ++k) {
+            const uint32_t v = h[k][d0 + e];
+            h[k][d0 + e] = to;
+            to += v;
+        }
+        at += all[e];
+    }
     __syncthreads();
 #pragma unroll
     for (uint32_t r = 0; r < R; ++r) {
         const uint32_t i = i0 + r * 64 + l;
-        if (i >= p.count) continue;
+        if (!have[r]) continue;
         const uint32_t to = h[w][key[r] >> p.shift & (digits - 1)] + rank[r];
         p.to[to] = key[r];
         p.to_token[to] = p.from ? p.from_token[i] : i;
     }
+}
+
+// Few tokens: every pass by one workgroup, in LDS.
+__global__ __launch_bounds__(1024) void k_sort_one(const SortParams p) {
+    constexpr uint32_t W = 16, R = kSortOne / 1024;
+    __shared__ uint32_t h[W][kSortDigits];
+    __shared__ uint32_t keys[kSortOne], toks[kSortOne];
+    __shared__ uint32_t s[W];
+    const uint32_t w = threadIdx.x >> 6, l = lane(), i0 = w * (R * 64);
+    const uint32_t digits = 1u << p.bits;
+    uint32_t key[R], tok[R], rank[R];
+    bool have[R];
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r) {
+        tok[r] = i0 + r * 64 + l;
+        have[r] = tok[r] < p.count;
+        key[r] = have[r] ? key_of(p, tok[r]) : 0u;
+    }
+    for (uint32_t pass = 0; pass < p.passes; ++pass) {
+        const uint32_t shift = pass * p.bits;
+        for (uint32_t d = threadIdx.x; d < W * kSortDigits; d += 1024) (&h[0][0])[d] = 0;
+        __syncthreads();
+        ranks<R>(key, have, shift, p.bits, h[w], rank);
+        __syncthreads();
+        uint32_t sum = 0;
+        if (threadIdx.x < digits)
+            for (uint32_t k = 0; k < W; ++k) sum += h[k][threadIdx.x];
+        uint32_t to = group_scan<1024>(sum, s);
+        if (threadIdx.x < digits)
+            for (uint32_t k = 0; k < W; ++k) {
+                const uint32_t v = h[k][threadIdx.x];
+                h[k][threadIdx.x] = to;
+                to += v;
+            }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t r = 0; r < R; ++r)
+            if (have[r]) {
+                const uint32_t at = h[w][key[r] >> shift & (digits - 1)] + rank[r];
+                keys[at] = key[r];
+                toks[at] = tok[r];
+            }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t r = 0; r < R; ++r)
+            if (have[r]) {
+                key[r] = keys[i0 + r * 64 + l];
+                tok[r] = toks[i0 + r * 64 + l];
+            }
+    }
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r)
+        if (have[r]) {
+            p.to[i0 + r * 64 + l] = key[r];
+            p.to_token[i0 + r * 64 + l] = tok[r];
+        }
 }
 
 // ------------------------------------------------------------------ sums
@@ -368,6 +489,15 @@ int launch_row_sort(SortParams p, const RowScratch &s, uint8_t *scratch, const u
     p.hist = reinterpret_cast<uint32_t *>(scratch + s.hist);
     p.chunks = (p.count + kSortChunk - 1) / kSortChunk;
     p.bits = (all + passes - 1) / passes;
+    p.passes = passes;
+    if (p.count <= kSortOne) {
+        p.to = keys[0];
+        p.to_token = toks[0];
+        hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(1024), 0, (hipStream_t)stream, p);
+        *key = keys[0];
+        *token = toks[0];
+        return (int)hipGetLastError();
+    }
     for (uint32_t k = 0; k < passes; ++k) {
         p.shift = k * p.bits;
         p.from = k ? keys[(k - 1) & 1] : nullptr;
@@ -375,7 +505,8 @@ int launch_row_sort(SortParams p, const RowScratch &s, uint8_t *scratch, const u
         p.to = keys[k & 1];
         p.to_token = toks[k & 1];
         hipLaunchKernelGGL(k_sort_count, dim3(p.chunks), dim3(kSortThreads), 0, (hipStream_t)stream, p);
-        hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(1024), 0, (hipStream_t)stream, p.hist, p.chunks << p.bits);
+        if (p.chunks > kSortFew)
+            hipLaunchKernelGGL(k_sort_prefix, dim3(kSortDigits / 64), dim3(64), 0, (hipStream_t)stream, p.hist, p.chunks);
         hipLaunchKernelGGL(k_sort_place, dim3(p.chunks), dim3(kSortThreads), 0, (hipStream_t)stream, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return (int)e;

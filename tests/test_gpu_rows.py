@@ -79,7 +79,7 @@ def test_lookup_layouts_and_spills(L, B, cw):
         same(y, looked_up(w, index, 1.0, BF))
 
 
-@pytest.mark.parametrize("count", [1, 2, 63, 64, 65, 1000, 5000, 40_000])
+@pytest.mark.parametrize("count", [1, 2, 63, 64, 65, 1000, 1024, 4096, 4097, 5000, 40_000, 100_000])
 def test_lookup_counts(L, count):
     """Few and many tokens (more than the table has rows), frequent ones often,
     in a batch of two dimensions; an unaligned output."""
@@ -89,11 +89,27 @@ def test_lookup_counts(L, count):
     index = (torch.exp(u * np.log(rows + 1.0)) - 1).long().clamp(0, rows - 1)
     if count > 60:
         index[::50] = -1
-    flat = torch.full((count * cols + 9,), 7.0, dtype=BF, device="cuda")
-    y = flat[1:1 + count * cols].view(count, cols)
-    L.lct_tensor_rows(cb, t, index, y, L.alloc_rows(count), scale=2.5)
-    same(y, looked_up(w, index, 2.5, BF))
-    assert bool((flat[0] == 7.0) & (flat[1 + count * cols:] == 7.0).all())
+    for work in (L.alloc_rows(count), None):
+        flat = torch.full((count * cols + 9,), 7.0, dtype=BF, device="cuda")
+        y = flat[1:1 + count * cols].view(count, cols)
+        L.lct_tensor_rows(cb, t, index, y, work, scale=2.5)
+        same(y, looked_up(w, index, 2.5, BF))
+        assert bool((flat[0] == 7.0) & (flat[1 + count * cols:] == 7.0).all())
+
+
+@pytest.mark.parametrize("cols", [1, 100, 256, 300, 4096, 20_000])
+def test_sorted_lookups_of_rows_that_share_blocks_and_positions(L, cols):
+    """Every row several times, in no order: rows that end within the position
+    of a stream where the next begins, rows over several blocks, spills."""
+    rows = max(2, 200_000 // cols)
+    count = max(2048, 3 * min(rows, 5000))
+    for lay in (L.lct_layout_init(L.CLEAN), L.layout(4096, 2)):
+        w, cb, t = table(L, rows, cols, lay, cols)
+        torch.manual_seed(2)
+        index = torch.randint(-1, rows + 1, (count,), device="cuda", dtype=torch.int32)
+        y = torch.full((count, cols), 7.0, dtype=SF, device="cuda")
+        L.lct_tensor_rows(cb, t, index, y, L.alloc_rows(count), scale=0.5)
+        same(y, looked_up(w, index, 0.5, SF))
 
 
 def test_lookup_in_a_groups_member(L):
