@@ -274,7 +274,7 @@ struct RowsParams {
     DecTab dec;
 };
 constexpr uint32_t kRowsRun = 16;          // sorted tokens that a workgroup takes at most,
-constexpr uint32_t kRowsRoom = 32768;      // and bytes of LDS for their exponents
+constexpr uint32_t kRowsRoom = 12288;      // and bytes of LDS for their exponents
 constexpr uint64_t kRowsSortFrom = 1024;   // tokens from which on they are sorted
 
 // The gradient of a table's rows (rows.hip).  Tokens are sorted by row in
