@@ -734,7 +734,7 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
         // the longest products first: short ones fill what they leave
         std::stable_sort(p.mat, p.mat + p.count,
                          [](const OrthoMat &a, const OrthoMat &b) { return (uint64_t)a.m + a.n > (uint64_t)b.m + b.n; });
-        OrthoBatch b = {kOrthoLarge, 0, 0, 0};
+        OrthoBatch b = {kOrthoLarge, 0, 0, 0, 1, 1};
         uint64_t tiles = 0;
         for (uint32_t j = 0; j < p.count; ++j) {
             const uint64_t mt = (p.mat[j].m + kOrthoLarge - 1) / kOrthoLarge;
@@ -756,6 +756,19 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
             b.sym_tiles += (uint32_t)(mt * (mt + 1) / 2 * r);
             b.next_tiles += (uint32_t)(mt * nt * r);
             bytes += ortho_bytes(o.mp, o.np, o.pairs);
+        }
+        if (b.tile == kOrthoSmall) {
+            // parts of K for the longest sums; what is shorter gets shorter parts
+            uint32_t gram = 0, square = 0;
+            for (uint32_t j = 0; j < p.count; ++j) {
+                gram = std::max(gram, p.mat[j].np / 32 * (p.mat[j].pairs ? 3 : 1));
+                square = std::max(square, p.mat[j].mp / 32 * 3);
+            }
+            const uint32_t room = std::min(kOrthoSplitMax, kOrthoSplitTo / b.sym_tiles);
+            if (gram >= kOrthoLong) b.split_gram = std::max(1u, std::min(room, gram / kOrthoPart));
+            if (square >= kOrthoLong) b.split_square = std::max(1u, std::min(room, square / kOrthoPart));
+            p.partial = reinterpret_cast<float *>(bytes);   // (an offset so far)
+            bytes += 4ull * kOrthoSmall * kOrthoSmall * b.sym_tiles * std::max(b.split_gram, b.split_square);
         }
         const lct_status st = f(p, b, bytes);
         if (st != LCT_OK) return st;
@@ -1720,6 +1733,7 @@ lct_status lct_list_orthogonalize(const lct_list *x, const uint64_t *rows, const
     }
     return ortho_batches(*x, rows, [&](OrthoParams &p, OrthoBatch &b, uint64_t) {
         p.scratch = scr + s.batch;
+        p.partial = reinterpret_cast<float *>(p.scratch + reinterpret_cast<uint64_t>(p.partial));
         p.norm = norm;
         p.xscale = kOrthoX;
         p.a = cf[0];

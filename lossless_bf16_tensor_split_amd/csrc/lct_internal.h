@@ -473,6 +473,10 @@ constexpr uint32_t kOrthoPairs = 256;
 constexpr uint32_t kOrthoMax = 32;        // matrices per launch
 constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;   // tiles
 constexpr uint32_t kOrthoLargeFrom = 200;                  // large tiles of a batch from which on they are taken
+// Few small tiles (at most half of what the device holds at once) with long
+// sums (kOrthoLong steps of 32 and more): K is cut into parts of at least
+// kOrthoPart steps.
+constexpr uint32_t kOrthoSplitTo = 256, kOrthoSplitMax = 8, kOrthoPart = 8, kOrthoLong = 48;
 // Elements that a batch of matrices gathers: 2048 tiles of 256 x 256, eight
 // per CU.
 constexpr uint64_t kOrthoBatch = 1ull << 27;
@@ -497,11 +501,13 @@ struct OrthoParams {
     const float *norm;
     double xscale;
     float a, ka, kaa, kx, kbx;    // factors of a X, A, A A, X X' and B X for numbers as held
-    uint32_t count, turn;         // turn: which copy of X' is read
+    float *partial;               // sums of parts of K, where it is cut
+    uint32_t count, turn, split;  // turn: which copy of X' is read; split: parts of K
     OrthoMat mat[kOrthoMax];
 };
 struct OrthoBatch {
     uint32_t tile, prep_tiles, sym_tiles, next_tiles;
+    uint32_t split_gram, split_square;   // parts that the symmetric products' K is cut into
 };
 
 // The allocation-free update's static working memory (per device).

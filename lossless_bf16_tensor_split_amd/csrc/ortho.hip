@@ -39,6 +39,7 @@ typedef _Float16 f16;
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(1))) const uint8_t glb_u8;
 
@@ -161,20 +162,23 @@ struct Product {
     }
 
     // P Q' over `steps` steps; with three segments, P and Q being the first of
-    // pairs, P Q' + P Ql' + Pl Q'.
+    // pairs, P Q' + P Ql' + Pl Q'.  Of all these steps part `part` of `parts`.
     __device__ __forceinline__ void run(const f16 *ph, const f16 *pl, const f16 *qh, const f16 *ql, uint32_t segs,
-                                        uint32_t steps, uint64_t ld, uint8_t *lds) {
+                                        uint32_t steps, uint64_t ld, uint8_t *lds, uint32_t part = 0,
+                                        uint32_t parts = 1) {
         const uint32_t l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
         for (uint32_t a = 0; a < FP; ++a)
 #pragma unroll
             for (uint32_t b = 0; b < FQ; ++b) acc[a][b] = f32x16{0.0f};
-        const uint32_t total = segs * steps;
+        const uint32_t begin = segs * steps * part / parts, total = segs * steps * (part + 1) / parts - begin;
+        if (total == 0) return;
         // a load: 16 rows of 64 bytes, a lane's row and (exchanged) piece
         const uint32_t ldb = 2 * (uint32_t)ld;   // (T rows span less than 2^32 bytes)
         const uint32_t mine = (16 * w + (l >> 2)) * ldb + 16 * ((l & 3) ^ (l >> 4));
-        __amdgpu_buffer_rsrc_t rp = rsrc(ph, ldb), rq = rsrc(qh, ldb);
-        uint32_t at = 0, seg = 0;   // the next load's step of its segment, in bytes
+        // the next load's step of its segment, in bytes
+        uint32_t seg = begin / steps, at = (begin - seg * steps) * kRowB;
+        __amdgpu_buffer_rsrc_t rp = rsrc(seg == 2 ? pl : ph, ldb), rq = rsrc(seg == 1 ? ql : qh, ldb);
         auto load = [&](bool side, uint32_t it, uint8_t *buf) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(side ? rq : rp,
                                                      (lds_u8 *)(buf + (side ? kSide : 0) + (it * 64 + 16 * w) * kRowB),
@@ -356,6 +360,43 @@ struct Product {
             g(row, 8 * c, *reinterpret_cast<const u32x4 *>(own + R::at(row, c)));
         }
     }
+    // The sums as they lie, 16 bytes a lane at a time: to memory, and added
+    // from there.
+    __device__ __forceinline__ void leave(float *to) const {
+#pragma unroll
+        for (uint32_t a = 0; a < FP; ++a)
+#pragma unroll
+            for (uint32_t b = 0; b < FQ; ++b)
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r)
+                    *reinterpret_cast<f32x4 *>(to + (((a * FQ + b) * 4 + r) * kThreads + threadIdx.x) * 4) =
+                        f32x4{acc[a][b][4 * r], acc[a][b][4 * r + 1], acc[a][b][4 * r + 2], acc[a][b][4 * r + 3]};
+    }
+    // acc = the sums of wave w of `parts` parts, one after another
+    __device__ __forceinline__ void join(const float *from, uint32_t parts, uint32_t w) {
+        constexpr uint32_t N = FP * FQ * 4;
+        const float *mine = from + (w * 64 + (threadIdx.x & 63)) * 4;
+        f32x4 sum[N], a[N], b[N];
+        auto get = [&](f32x4 (&v)[N], uint32_t s) {
+#pragma unroll
+            for (uint32_t e = 0; e < N; ++e)
+                v[e] = *reinterpret_cast<const f32x4 *>(mine + (uint64_t)s * (TP * TQ) + e * (kThreads * 4));
+        };
+        get(sum, 0);
+        for (uint32_t s = 1; s < parts; s += 2) {
+            get(a, s);
+            get(b, min(s + 1, parts - 1));
+#pragma unroll
+            for (uint32_t e = 0; e < N; ++e) sum[e] += a[e];
+            if (s + 1 < parts)
+#pragma unroll
+                for (uint32_t e = 0; e < N; ++e) sum[e] += b[e];
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < N; ++e)
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) acc[e / 4 / FQ][e / 4 % FQ][e % 4 * 4 + q] = sum[e][q];
+    }
     // (the sums are hidden from the compiler between passes, or it keeps one
     // pass's conversions for the next)
     template <bool ALONG, class V>
@@ -408,10 +449,17 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t s, uint32_t &i, ui
 
 // A = X X' (SQUARE false) or B = b A + c A A: the tiles on and above the
 // diagonal, each written to its mirror image too.
-template <uint32_t TP, uint32_t TQ, uint32_t NB, bool SQUARE>
-__global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const OrthoParams p) {
+//
+// With few tiles and long sums (one matrix of 777 x 2049 has 28 of them) K is
+// cut into p.split parts, a workgroup each, which leave their sums in memory
+// (PART); the launch that follows (JOIN) adds them, in order, and goes on as
+// the whole kernel does, a workgroup for each wave's quarter of a tile.
+enum Stage { WHOLE, PART, JOIN };
+template <uint32_t TP, uint32_t TQ, uint32_t NB, bool SQUARE, Stage STAGE>
+__global__ __launch_bounds__(STAGE == JOIN ? 64 : kThreads, STAGE == JOIN ? 1 : 2) void k_ortho_sym(const OrthoParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t t = tile_number();
+    const uint32_t g = STAGE == WHOLE ? tile_number() : blockIdx.x;
+    const uint32_t t = STAGE == PART ? g / p.split : STAGE == JOIN ? g / 4 : g;
     const uint32_t k = matrix_of(p, t, [](const OrthoMat &o) { return o.sym0; });
     const OrthoMat &o = p.mat[k];
     const Parts w = parts_of(p.scratch, o);
@@ -423,12 +471,20 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const
     tj = tj * R + (t - o.sym0) % R;
     const uint64_t ld = SQUARE ? o.mp : o.np, i0 = ti * TP * ld, j0 = tj * TQ * ld;
     Product<TP, TQ, NB> pr;
-    if constexpr (SQUARE)
-        pr.run(w.ah + i0, w.al + i0, w.ah + j0, w.al + j0, 3, o.mp / kStep, ld, smem);
-    else
-        pr.run(w.xh + i0, w.xl + i0, w.xh + j0, w.xl + j0, o.pairs ? 3 : 1, o.np / kStep, ld, smem);
+    if constexpr (STAGE != JOIN) {
+        const uint32_t part = STAGE == PART ? g % p.split : 0, parts = STAGE == PART ? p.split : 1;
+        if constexpr (SQUARE)
+            pr.run(w.ah + i0, w.al + i0, w.ah + j0, w.al + j0, 3, o.mp / kStep, ld, smem, part, parts);
+        else
+            pr.run(w.xh + i0, w.xl + i0, w.xh + j0, w.xl + j0, o.pairs ? 3 : 1, o.np / kStep, ld, smem, part, parts);
+    }
+    if constexpr (STAGE == PART) {
+        pr.leave(p.partial + (uint64_t)g * (TP * TQ));
+        return;
+    }
     // this wave's part: rows pi.. of P (of A), pj.. of Q
-    const uint32_t wv = threadIdx.x >> 6;
+    const uint32_t wv = STAGE == JOIN ? g % 4 : threadIdx.x >> 6;
+    if constexpr (STAGE == JOIN) pr.join(p.partial + (uint64_t)t * p.split * (TP * TQ), p.split, wv);
     const uint64_t pi = ti * TP + (wv >> 1) * (TP / 2), pj = tj * TQ + (wv & 1) * (TQ / 2);
     const uint64_t along = pj * o.mp + pi, across = pi * o.mp + pj;
     const float f = SQUARE ? p.kaa : p.kx;
@@ -457,7 +513,7 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_sym(const
 
 // X <- a X + B X; the last step writes y in its place.
 template <uint32_t TP, uint32_t TQ, uint32_t NB, bool LAST>
-__global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_next(const OrthoParams p) {
+__global__ __launch_bounds__(kThreads, 2) void k_ortho_next(const OrthoParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t tile = tile_number();
     const uint32_t k = matrix_of(p, tile, [](const OrthoMat &o) { return o.next0; });
@@ -514,36 +570,53 @@ __global__ __launch_bounds__(kThreads, TQ == 256 ? 1 : 2) void k_ortho_next(cons
 }
 
 // Dynamic LDS beyond 64 KiB must be requested per kernel, once.
-std::atomic<bool> g_granted[8];
+std::atomic<bool> g_granted[4];
 
 int launch_tiles(const void *fn, uint32_t grid, size_t lds, const OrthoParams &p, void *stream,
-                 std::atomic<bool> &granted) {
+                 std::atomic<bool> &granted, uint32_t threads = kThreads) {
     if (lds > 64 * 1024 && !granted.load()) {
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return (int)e;
         granted.store(true);
     }
     void *args[] = {const_cast<OrthoParams *>(&p)};
-    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(kThreads), args, lds, (hipStream_t)stream);
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3(threads), args, lds, (hipStream_t)stream);
     return (int)(e != hipSuccess ? e : hipGetLastError());
+}
+
+// A symmetric product, whole or (small tiles) in parts.
+template <uint32_t TP, uint32_t TQ, uint32_t NB, bool SQUARE>
+int run_sym(OrthoParams &p, uint32_t tiles, uint32_t split, void *stream, std::atomic<bool> &granted) {
+    constexpr size_t lds = Product<TP, TQ, NB>::kLds;
+    if constexpr (TP == kOrthoSmall) {
+        static_assert(lds <= 64 * 1024, "granted without asking");
+        if (split > 1) {
+            p.split = split;
+            int e = launch_tiles(reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, SQUARE, PART>), tiles * split,
+                                 lds, p, stream, granted);
+            if (e == hipSuccess)
+                e = launch_tiles(reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, SQUARE, JOIN>), tiles * 4,
+                                 Product<TP, TQ, NB>::kPart, p, stream, granted, 64);
+            return e;
+        }
+    }
+    return launch_tiles(reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, SQUARE, WHOLE>), tiles, lds, p, stream,
+                        granted);
 }
 
 template <uint32_t TP, uint32_t TQ, uint32_t NB>
 int run_batch(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stream) {
-    const void *gram = reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, false>);
-    const void *square = reinterpret_cast<const void *>(&k_ortho_sym<TP, TQ, NB, true>);
     const void *next = reinterpret_cast<const void *>(&k_ortho_next<TP, TQ, NB, false>);
     const void *last = reinterpret_cast<const void *>(&k_ortho_next<TP, TQ, NB, true>);
     constexpr size_t lds = Product<TP, TQ, NB>::kLds;
-    std::atomic<bool> *granted = g_granted + (TP == 256 ? 4 : 0);
     for (uint32_t s = 0; s < steps; ++s) {
         p.turn = s & 1;
         const bool end = s + 1 == steps;
-        int e = launch_tiles(gram, b.sym_tiles, lds, p, stream, granted[0]);
-        if (e == hipSuccess) e = launch_tiles(square, b.sym_tiles, lds, p, stream, granted[1]);
+        int e = run_sym<TP, TQ, NB, false>(p, b.sym_tiles, b.split_gram, stream, g_granted[0]);
+        if (e == hipSuccess) e = run_sym<TP, TQ, NB, true>(p, b.sym_tiles, b.split_square, stream, g_granted[1]);
         if (e == hipSuccess)
-            e = end ? launch_tiles(last, b.next_tiles, lds, p, stream, granted[3])
-                    : launch_tiles(next, b.next_tiles, lds, p, stream, granted[2]);
+            e = end ? launch_tiles(last, b.next_tiles, lds, p, stream, g_granted[3])
+                    : launch_tiles(next, b.next_tiles, lds, p, stream, g_granted[2]);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -555,7 +628,8 @@ int launch_ortho(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stre
     hipLaunchKernelGGL(k_ortho_prep, dim3(b.prep_tiles), dim3(256), 0, (hipStream_t)stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    return b.tile == 256 ? run_batch<256, 128, 3>(p, b, steps, stream) : run_batch<128, 128, 4>(p, b, steps, stream);
+    return b.tile == kOrthoLarge ? run_batch<256, 128, 3>(p, b, steps, stream)
+                                 : run_batch<128, 128, 4>(p, b, steps, stream);
 }
 
 }  // namespace lct
