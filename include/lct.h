@@ -580,7 +580,7 @@ lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float
  *
  * Common: d_index holds count indices, int64 (wide) or int32; an index outside
  * 0 .. rows - 1 (a padding token's) gives a row of zeros and no gradient.  At
- * most 2^30 indices, 2^31 rows and 2^24 columns.  Matrices are dense, row by
+ * most 2^30 indices, 2^29 rows and 2^24 columns.  Matrices are dense, row by
  * row, of any lct_dtype, with the alignment of their elements.  Enqueue only.
  * Errors: LCT_EINVAL, LCT_EALIGN, LCT_EALIAS, LCT_EARCH, LCT_EHIP.
  *

@@ -1650,7 +1650,7 @@ lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t
     int e = hipSuccess;
     p.run = 1;
     p.piece = (uint32_t)std::min<uint64_t>((cols + 15) / 16 * 16, kRowsRoom);
-    if (d_scratch && count >= kRowsSortFrom) {
+    if (d_scratch && count >= kRowsSortFrom && count >= 2 * nblocks(t->n, t->layout)) {
         for (uint32_t r = kRowsRun; r > 1 && p.run == 1; r /= 2)
             if (r * p.piece <= kRowsRoom) p.run = r;
         e = sort_rows(d_index, wide, count, p.rows, s, d_scratch, &p.key, &p.token, stream);

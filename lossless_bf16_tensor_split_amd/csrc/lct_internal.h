@@ -275,7 +275,12 @@ struct RowsParams {
 };
 constexpr uint32_t kRowsRun = 16;          // sorted tokens that a workgroup takes at most,
 constexpr uint32_t kRowsRoom = 12288;      // and bytes of LDS for their exponents
-constexpr uint64_t kRowsSortFrom = 1024;   // tokens from which on they are sorted
+// Tokens are sorted from so many on, if there are two to a block of the table.
+// In us, in order and (sorted, with the sort): 50,304 x 768 (590 blocks), 2048
+// tokens 29 (36), 4096 45 (44), 16,384 139 (84); 151,936 x 2560 (5936 blocks),
+// 4096 tokens 52 (56), 8192 91 (86), 100 (118) where none is frequent, 16,384
+// 164 (134).
+constexpr uint64_t kRowsSortFrom = 4096;
 
 // The gradient of a table's rows (rows.hip).  Tokens are sorted by row in
 // passes of at most kSortBits bits over chunks of kSortChunk tokens, then
@@ -284,7 +289,8 @@ constexpr uint32_t kSortBits = 9, kSortDigits = 1u << kSortBits;
 constexpr uint32_t kSortThreads = 256, kSortChunk = 1024;
 constexpr uint32_t kSortOne = 4096;                    // up to so many tokens one workgroup sorts them
 constexpr uint32_t kSortFew = 64;                      // chunks whose counts the placing kernel adds up itself
-constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 31, kMaxCols = 1ull << 24;
+// (so that every launch's threads stay below 2^32 in a dimension)
+constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 29, kMaxCols = 1ull << 24;
 constexpr uint32_t kRowTile = 16, kRowTileMax = 256;   // tokens of a tile: more where there are many
 constexpr uint64_t kRowTiles = 4096;
 constexpr uint32_t kClearRows = 16;                    // rows that a clearing wave looks at
@@ -471,8 +477,13 @@ inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
 // parts of B and of X' too.
 constexpr uint32_t kOrthoPairs = 256;
 constexpr uint32_t kOrthoMax = 32;        // matrices per launch
-constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;   // tiles
-constexpr uint32_t kOrthoLargeFrom = 200;                  // large tiles of a batch from which on they are taken
+constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;
+// Tiles of 128 x 128, or (kOrthoLarge) of 256 x 128, whose operands take three
+// quarters of the traffic but which leave more of the device idle in the last
+// round.  In us, small and (large): 160 large tiles' worth (2560 x 4096) 1179
+// (1576), 380 (2560 x 9728) 2025 (2378), 432 (24 matrices) 1204 (1299), 1540
+// (seven matrices) 8457 (7604).
+constexpr uint32_t kOrthoLargeFrom = 800;
 // Few small tiles (at most half of what the device holds at once) with long
 // sums (kOrthoLong steps of 32 and more): K is cut into parts of at least
 // kOrthoPart steps.

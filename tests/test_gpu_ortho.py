@@ -95,11 +95,13 @@ def test_larger_matrices(L, m, n):
 
 
 def test_many_large_matrices(L):
-    """Enough tiles for the large ones, in one batch and in several."""
-    xs = [matrix(m, n, "full", BF, k) for k, (m, n) in enumerate([(768, 2304), (768, 768), (1300, 900)] * 12)]
+    """Enough of them for the large tiles, in two batches, short ones among
+    them."""
+    shapes = [(1024, 2048)] * 13 + [(200, 300), (2304, 768), (1, 5)] + [(1024, 2048)] * 13 + [(900, 1300)] * 8
+    xs = [matrix(m, n, "full", BF, k) for k, (m, n) in enumerate(shapes)]
     ys = L.orthogonalize(xs)
-    for x, y in zip(xs[:3] + xs[-3:], ys[:3] + ys[-3:]):
-        check(y, x, 5, L.NEWTON_SCHULZ, 1.0, str(tuple(x.shape)))
+    for k in (0, 13, 14, 15, 20, len(xs) - 1):
+        check(ys[k], xs[k], 5, L.NEWTON_SCHULZ, 1.0, str(tuple(xs[k].shape)))
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 6])

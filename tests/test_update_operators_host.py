@@ -110,7 +110,7 @@ def test_grad_refusals(L):
 
     assert call() in (L.EARCH, L.EHIP)
     assert call(index=None) == call(dy=None) == call(g=None) == call(scr=None) == L.EINVAL
-    assert call(ty=5) == call(tg=5) == call(count=1 << 31) == call(rows=1 << 32) == call(cols=1 << 25) == L.EINVAL
+    assert call(ty=5) == call(tg=5) == call(count=1 << 31) == call(rows=(1 << 29) + 1) == call(cols=1 << 25) == L.EINVAL
     assert call(index=A + 4) == call(dy=B + 1) == call(g=D + 2, tg=L.FP32) == call(scr=SCR + 8) == L.EALIGN
     assert call(g=B) == call(g=A) == call(scr=A) == call(scr=B) == call(g=SCR) == L.EALIAS
     assert call(rows=0, g=None, scr=None) == call(cols=0, g=None, scr=None) == L.OK
