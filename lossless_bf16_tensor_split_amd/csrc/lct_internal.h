@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/lct.h"
 
 namespace lct {
@@ -291,13 +293,25 @@ constexpr uint32_t kSortOne = 4096;                    // up to so many tokens o
 constexpr uint32_t kSortFew = 64;                      // chunks whose counts the placing kernel adds up itself
 // (so that every launch's threads stay below 2^32 in a dimension)
 constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 29, kMaxCols = 1ull << 24;
-constexpr uint32_t kRowTile = 16, kRowTileMax = 256;   // tokens of a tile: more where there are many
+// Tokens of a tile: four where there are few (each row that ends in a tile waits
+// for what G holds), more where there are many.
+constexpr uint32_t kRowTileFew = 4, kRowTile = 16, kRowTileMax = 256;
+constexpr uint64_t kRowFew = 4096;                     // tokens up to which they are few
 constexpr uint64_t kRowTiles = 4096;
 constexpr uint32_t kClearRows = 16;                    // rows that a clearing wave looks at
 inline uint32_t row_tile(uint64_t count) {
+    if (count <= kRowFew) return kRowTileFew;
     uint64_t t = kRowTile;
     while (t < kRowTileMax && count > kRowTiles * t) t *= 2;
     return (uint32_t)t;
+}
+// The most tiles that up to `count` tokens make: memory for many tokens does for
+// fewer, whose tiles are shorter.
+inline uint64_t row_tiles_most(uint64_t count) {
+    uint64_t most = (count + row_tile(count) - 1) / row_tile(count);
+    if (count > kRowFew) most = std::max<uint64_t>(most, kRowFew / kRowTileFew);
+    if (count > kRowTiles * kRowTile) most = std::max(most, kRowTiles);
+    return most;
 }
 struct SortParams {
     const void *index;          // the first pass reads indices, the others keys
@@ -321,14 +335,13 @@ struct RowScratch {
 inline RowScratch row_scratch(uint64_t count, uint64_t cols) {
     RowScratch s;
     const uint64_t list = align256(4 * count), chunks = (count + kSortChunk - 1) / kSortChunk;
-    const uint64_t tile = row_tile(count), tiles = (count + tile - 1) / tile;
     s.key0 = 0;
     s.key1 = list;
     s.tok0 = 2 * list;
     s.tok1 = 3 * list;
     s.hist = 4 * list;
     s.part = s.hist + align256(4ull * kSortDigits * (chunks + 1));
-    s.bytes = s.part + align256(8 * tiles * cols);
+    s.bytes = s.part + align256(8 * row_tiles_most(count) * cols);
     return s;
 }
 

@@ -80,6 +80,13 @@ def test_rows_scratch(L):
     assert L.lib.lct_rows_scratch(1, 1, None) == L.EINVAL
 
 
+def test_rows_scratch_for_many_tokens_does_for_fewer(L):
+    counts = sorted({c for k in range(0, 23) for c in ((1 << k) - 1, 1 << k, (1 << k) + 1, 3 << k, (3 << k) + 1)})
+    for cols in (0, 1, 64, 2560):
+        sizes = [rows_scratch(L, c, cols) for c in counts]
+        assert sizes == sorted(sizes), cols
+
+
 def test_lookup_refusals(L):
     if torch.cuda.is_available():
         pytest.skip("made-up addresses stay off a device")
