@@ -595,7 +595,8 @@ lct_status lct_mix_step_group(const lct_group *g, const lct_tensor *y_all, float
  * every row of G, those without a token becoming zero; with add, added to what
  * the rows with tokens hold and the others left alone.  Sums are FP32 in a fixed
  * order (equal calls give equal bits), rounded once to G's type.  d_scratch:
- * lct_rows_scratch(count, cols) bytes of device memory, 256-byte aligned, shared
+ * lct_rows_scratch(count, cols) bytes of device memory (what does for many tokens
+ * does for fewer), 256-byte aligned, shared
  * only by calls that do not overlap in time. */
 lct_status lct_tensor_rows(const lct_codebook *cb, const lct_tensor *t, uint64_t cols, const void *d_index,
                            int32_t wide, uint64_t count, float scale, void *d_y, int32_t type, void *d_scratch,
