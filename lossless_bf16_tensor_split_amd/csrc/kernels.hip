@@ -2904,7 +2904,7 @@ void k_mom(const MomParams p) {
 // input's rows between two zero rows; the result's rows go to memory as they
 // fill, once the input's (which they may overwrite) are in LDS.
 constexpr uint32_t kMixWaves = 4;
-constexpr uint32_t kMixETab = 0, kMixDTab = 2048, kMixWave0 = 3072;
+constexpr uint32_t kMixETab = 0, kMixDTab = 2048, kMixWave0 = kMixDTab + 1024;
 __host__ __device__ constexpr uint32_t mix_wave_bytes(uint32_t cap) { return (cap + 2) * ROWB; }
 
 // Named as global memory: a group's pointers come from its table, and the
