@@ -93,7 +93,8 @@ __global__ __launch_bounds__(256) void k_ortho_prep(const OrthoParams p) {
     const uint32_t tl = blockIdx.x - o.prep0, nt = o.np / kPrepTile;
     const uint32_t i0 = tl / nt * kPrepTile, j0 = tl % nt * kPrepTile;
     const float norm = p.norm[o.index];
-    const float inv = norm <= 3.0e38f ? (float)(p.xscale / ((double)norm + 1e-7)) : __builtin_nanf("");
+    // (false for NaN)
+    const float inv = norm < __builtin_inff() ? (float)(p.xscale / ((double)norm + 1e-7)) : __builtin_nanf("");
     const uint32_t c = threadIdx.x % 64, r0 = threadIdx.x / 64;
     if (!o.tall) {
         for (uint32_t r = r0; r < kPrepTile; r += 4) {
