@@ -1744,7 +1744,7 @@ lct_status lct_list_orthogonalize(const lct_list *x, const uint64_t *rows, const
         for (uint32_t j = 0; j < p.count; ++j) {
             OrthoMat &o = p.mat[j];
             o.y = const_cast<void *>(y->d_x[o.index]);
-            o.scale = (float)((scale ? (double)scale[o.index] : 1.0) / kOrthoX);
+            o.scale = scale ? scale[o.index] : 1.0f;
         }
         const int e = launch_ortho(p, b, steps, stream);
         return e == hipSuccess ? LCT_OK : hip_fail(e, "orthogonalisation launch");

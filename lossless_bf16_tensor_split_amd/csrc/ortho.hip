@@ -613,6 +613,12 @@ int run_batch(OrthoParams &p, const OrthoBatch &b, uint32_t steps, void *stream)
     for (uint32_t s = 0; s < steps; ++s) {
         p.turn = s & 1;
         const bool end = s + 1 == steps;
+        if (end) {
+            // the last sums stand for X itself: a tiny factor of the result
+            // would be a subnormal number after kOrthoX is taken from it
+            p.a = (float)(p.a / kOrthoX);
+            p.kbx = (float)(p.kbx / kOrthoX);
+        }
         int e = run_sym<TP, TQ, NB, false>(p, b.sym_tiles, b.split_gram, stream, g_granted[0]);
         if (e == hipSuccess) e = run_sym<TP, TQ, NB, true>(p, b.sym_tiles, b.split_square, stream, g_granted[1]);
         if (e == hipSuccess)
