@@ -1,5 +1,5 @@
-"""Orthogonalised updates on the GPU at the ends of their numbers."""
-import math
+"""Orthogonalised updates on the GPU at the ends of their numbers, and where one
+product can be seen by itself: products of few terms whose leading parts cancel."""
 import random
 
 import pytest
@@ -54,3 +54,71 @@ def test_tiny_and_huge_factors(L):
     step = torch.clamp(2.0 ** torch.floor(torch.log2(want.abs() + 1e-300)), min=2.0 ** -126) * 2.0 ** -7
     off = (got - want).abs() - 2.0 ** -18 * want.abs()
     assert bool((off <= step / 2).all()), (off / step).max()
+
+
+def cancelled(coef, pairs):
+    """One step on a matrix that holds a 3 x 3 square of ones and nothing else,
+    with the numbers that the kernels hold, relative to X0's 1 / 3: every row of
+    the square alike, so one element stands for all."""
+    a, b, c = coef
+    half = lambda v, s: float(torch.tensor(v * s, dtype=torch.float64).float().half()) / s      # noqa: E731
+
+    def pair(v, s):
+        h = half(v, s)
+        return h, half(v - h, s)
+
+    xh, xl = pair(1 / (3 + 1e-7), 2.0 ** 15)
+    lo = xl if pairs else 0.0
+    ah, al = pair(3 * (xh * xh + 2 * xh * lo), 2.0 ** 14)
+    bh, bl = pair(b * (ah + al) + c * 3 * (ah * ah + 2 * ah * al), 2.0 ** 13)
+    bl = bl if pairs else 0.0
+    return a * (xh + xl) + 3 * (bh * xh + bh * lo + bl * xh)
+
+
+@pytest.mark.parametrize("m,n,coefs", [
+    (200, 300, [(2, -3, 1), (1, -1, 0)]), (200, 2049, [(2, -3, 1), (1, -1, 0)]), (256, 1024, [(2, -3, 1), (1, -1, 0)]),
+    (300, 400, [(0, -1, 1), (1, -2, 1)]), (400, 257, [(0, -1, 1), (1, -2, 1)]), (777, 2049, [(0, -1, 1), (1, -2, 1)]),
+    (5120, 10240, [(0, -1, 1), (1, -2, 1)])])
+def test_every_product_of_the_pairs(L, m, n, coefs):
+    """Coefficients whose sum is zero: of a matrix with one singular value, one,
+    nothing is left but what the numbers held in fewer bits leave, 1e-4 of X and
+    more.  So a low part that is missing from a product, or a piece of a product's
+    long side, would change the result by 1e-4 of X or more (with a single B its
+    rounding hides A's low part unless the terms of B cancel too: a = 0 there).
+    The square of ones visits every 32 rows and every 32 columns.
+
+    Tolerance: each of the sums of up to nine products rounds at most nine times,
+    its factor and the additions three times more, 2^-24 each, for A (which enters
+    with |b|, and with |c| twice), A A, B X and a X: together less than 128 * 2^-24
+    of X for these coefficients.  A pair's low part may round the other way, 2^-22,
+    six times.  A single B may where it is small, 2^-11 of the result (where it is
+    not, it lies a sixth of a step from the border).  And half a BF16 step of
+    the result."""
+    steps = max((m + 31) // 32, (n + 31) // 32)
+    more = []
+    if m * n > 1 << 24:       # a large one: fewer places, and short matrices beside it, in large tiles too
+        places = [0, 1, 63, 64, 101, 159, 160, 200, 318, 319]
+        more = [(200, 2049), (2049, 200)]
+    else:
+        places = range(steps)
+    shapes = [(m, n), *more]
+    xs = [torch.zeros(s, dtype=BF, device="cuda") for s in shapes]
+    ys = [torch.empty_like(x) for x in xs]
+    xl, yl = L.LctMatrices(xs), L.LctMatrices(ys)
+    work = L.alloc_orthogonal(xl)
+    for k in places:
+        at = []
+        for x in xs:
+            r, c = ([(k * 32 + o) % s for o in (1, 14, 27)] for s in x.shape)
+            x.zero_()
+            x[torch.tensor(r)[:, None], torch.tensor(c)] = 1.0
+            at.append((torch.tensor(r)[:, None], torch.tensor(c)))
+        for coef in coefs:
+            L.lct_list_orthogonalize(xl, yl, work, steps=1, coef=coef)
+            for x, y, i in zip(xs, ys, at):
+                short = min(x.shape) <= 256
+                want = cancelled(coef, short)
+                tol = (128 * 2.0 ** -24 + 6 * 2.0 ** -22) / 3 + (2.0 ** -9 + 2.0 ** -11) * abs(want)
+                got = y[i].double()
+                assert float((got - want).abs().max()) <= tol, (tuple(x.shape), k, coef, got, want)
+                assert int((y != 0).sum()) <= 9
