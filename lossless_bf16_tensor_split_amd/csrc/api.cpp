@@ -702,6 +702,8 @@ bool ortho_coef_ok(const float (&coef)[3], uint32_t steps) {
     return true;
 }
 
+uint64_t up_to(uint64_t v, uint64_t step) { return (v + step - 1) / step * step; }
+
 uint64_t ortho_bytes(uint64_t mp, uint64_t np, bool pairs) {
     return 2 * ((pairs ? 6 : 4) * mp * np + (pairs ? 4 : 3) * mp * mp);
 }
@@ -735,12 +737,14 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
         std::stable_sort(p.mat, p.mat + p.count,
                          [](const OrthoMat &a, const OrthoMat &b) { return (uint64_t)a.m + a.n > (uint64_t)b.m + b.n; });
         OrthoBatch b = {kOrthoLarge, 0, 0, 0, 1, 1};
-        uint64_t tiles = 0;
+        uint64_t tiles = 0, large = 0, small = 0;   // (their work: m m n with whole tiles' sides)
         for (uint32_t j = 0; j < p.count; ++j) {
-            const uint64_t mt = (p.mat[j].m + kOrthoLarge - 1) / kOrthoLarge;
-            tiles += mt * ((p.mat[j].n + kOrthoLarge - 1) / kOrthoLarge);
+            const uint64_t m = p.mat[j].m, n = p.mat[j].n, ml = up_to(m, kOrthoLarge), ms = up_to(m, kOrthoSmall);
+            tiles += ml / kOrthoLarge * (up_to(n, kOrthoLarge) / kOrthoLarge);
+            large += ml * ml * up_to(n, kOrthoLarge);
+            small += ms * ms * up_to(n, kOrthoSmall);
         }
-        if (tiles < kOrthoLargeFrom) b.tile = kOrthoSmall;
+        if (tiles < kOrthoLargeFrom || large > small + small / kOrthoLargePad) b.tile = kOrthoSmall;
         uint64_t bytes = 0;
         for (uint32_t j = 0; j < p.count; ++j) {
             OrthoMat &o = p.mat[j];

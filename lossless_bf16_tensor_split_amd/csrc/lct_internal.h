@@ -497,6 +497,13 @@ constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;
 // (1576), 380 (2560 x 9728) 2025 (2378), 432 (24 matrices) 1204 (1299), 1540
 // (seven matrices) 8457 (7604).
 constexpr uint32_t kOrthoLargeFrom = 800;
+// Large tiles pad more: they are taken if the padded work (m m n, of a batch)
+// grows by a fifth at most.  In us, small and (large): 24 of 1000 x 2000, as
+// much work in either, 2402 (2167); 2 of 4100 x 8200, 1.08 times as much, 9794
+// (9333); 8 of 2100 x 4200, 1.16 times, 5993 (5917); 20 of 1100 x 2200, 1.23
+// times, 2739 (3258); 32 of 600 x 2000, 1.44 times, 1409 (1789); 32 of 64 x
+// 6400, 4 times, 805 (2963).
+constexpr uint32_t kOrthoLargePad = 5;
 // Few small tiles (at most half of what the device holds at once) with long
 // sums (kOrthoLong steps of 32 and more): K is cut into parts of at least
 // kOrthoPart steps.
