@@ -717,12 +717,13 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
     while (k < x.count) {
         OrthoParams p;
         memset(&p, 0, sizeof p);
-        uint64_t elems = 0;
+        uint64_t elems = 0;   // with whole tiles' sides, which is what takes memory and time
         for (; k < x.count && p.count < kOrthoMax; ++k) {
             if (x.n[k] == 0) continue;
             const uint64_t r = rows[k], c = x.n[k] / r;
-            if (p.count > 0 && elems + x.n[k] > kOrthoBatch) break;
-            elems += x.n[k];
+            const uint64_t padded = up_to(r, kOrthoSmall) * up_to(c, kOrthoSmall);
+            if (p.count > 0 && elems + padded > kOrthoBatch) break;
+            elems += padded;
             OrthoMat &o = p.mat[p.count++];
             o.m = (uint32_t)std::min(r, c);
             o.n = (uint32_t)std::max(r, c);

@@ -508,8 +508,8 @@ constexpr uint32_t kOrthoLargePad = 5;
 // sums (kOrthoLong steps of 32 and more): K is cut into parts of at least
 // kOrthoPart steps.
 constexpr uint32_t kOrthoSplitTo = 256, kOrthoSplitMax = 8, kOrthoPart = 8, kOrthoLong = 48;
-// Elements that a batch of matrices gathers: 2048 tiles of 256 x 256, eight
-// per CU.
+// Elements that a batch of matrices gathers, with sides rounded up to small
+// tiles: 2048 tiles of 256 x 256, eight per CU.
 constexpr uint64_t kOrthoBatch = 1ull << 27;
 // FP16 numbers stand for X, A and B times these powers of two.  Singular
 // values stay below kOrthoBound (checked for the coefficients), so X's

@@ -122,3 +122,12 @@ def test_every_product_of_the_pairs(L, m, n, coefs):
                 got = y[i].double()
                 assert float((got - want).abs().max()) <= tol, (tuple(x.shape), k, coef, got, want)
                 assert int((y != 0).sum()) <= 9
+
+
+def test_lists_of_matrices_with_a_short_side(L):
+    """More than a batch holds with whole tiles' sides, and a side near the
+    longest."""
+    for shapes in ([(16, 8192)] * 33 + [(8192, 9)], [(1, 300_000)] * 5 + [(3, 7)] + [(300_001, 1)] * 3, [(2, 1 << 22), (5, 5)]):
+        xs = [torch.randn(s, device="cuda").to(BF) for s in shapes]
+        for k, (x, y) in enumerate(zip(xs, L.orthogonalize(xs))):
+            check(y, x, 5, L.NEWTON_SCHULZ, 1.0, "%d: %s" % (k, tuple(x.shape)))

@@ -47,3 +47,14 @@ def test_large_matrices_beside_short_ones(L):
     with them; none takes more than four times its own rounding."""
     shapes = [(2560, 9728)] * 4 + [(100, 9000), (1, 5)]
     assert need(L, shapes) <= sum(most(s) for s in shapes[:4]) + 4 * sum(most(s) for s in shapes[4:]) + ROOM
+
+
+@pytest.mark.parametrize("shape", [(1, 1 << 22), (1 << 22, 1), (9, 65536), (100, 300_000), (1, 1 << 20), (200, 500_000)])
+def test_lists_of_matrices_with_a_short_side(L, shape):
+    """A batch gathers at most 2^27 elements with whole tiles' sides (a larger
+    matrix is one by itself), however few of them are the matrices' own."""
+    one = most(shape)
+    m, n = (-(-s // 128) * 128 for s in shape)
+    batch = max(1, min(32, (1 << 27) // (m * n)))
+    for count in (1, 31, 32, 200):
+        assert need(L, [shape] * count) <= min(count, batch) * one + ROOM, count
