@@ -625,6 +625,11 @@ lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, cons
  * checks: (3.4445, -4.775, 2.0315) and (15, -10, 3) / 8 do.  A matrix whose norm
  * is not finite in FP32 gives NaN, a matrix of zeros zeros.  Equal calls give
  * equal bits.
+ * y's distance from the exact result, in norms of it, is 1.7e-3 where nothing but
+ * its rounding counts: with at most 256 rows or columns, up to 3 steps, or
+ * coefficients that lead to a fixed point.  With both sides longer the usual
+ * coefficients (the first) make it about 2.4e-3 at most after 5 steps, 3.6e-3 after
+ * 8, 4.7e-3 after 12, and up to 3e-2 after 32.
  * d_scratch: device working memory of lct_orthogonal_scratch() bytes (256-byte
  * aligned), overlapping no tensor, shared only by calls that do not overlap in
  * time.  Long lists are done in batches of consecutive matrices, whose memory

@@ -1114,7 +1114,9 @@ def alloc_orthogonal(x: LctMatrices) -> OrthoWork:
 def lct_list_orthogonalize(x: LctMatrices, y: LctMatrices, work: OrthoWork, steps: int = 5, coef=NEWTON_SCHULZ,
                            scale=None, stream=None) -> None:
     """y_k = s_k * (x_k with its singular values driven towards one); scale: a
-    number, or one per matrix."""
+    number, or one per matrix.  Matrices whose both sides are longer than 256 are
+    off by about 2.4e-3 of their norm after 5 steps with the usual coefficients,
+    more after more; the others by their rounding to BF16, 1.7e-3."""
     if x.shapes != y.shapes:
         raise ValueError("the lists' matrices have other shapes")
     if len(coef) != 3:

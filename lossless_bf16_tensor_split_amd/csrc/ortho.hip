@@ -17,10 +17,17 @@
 //   - A is kept as a pair too, and A A is summed as hi hi + hi lo + lo hi;
 //   - sums are FP32 throughout.
 // X's high part alone enters the products X X' and B X, and B is one FP16
-// number: those roundings act within the rows that X has.  The result is then
-// 1.7e-3 to 2.2e-3 off the exact one (norms), of which rounding it to BF16
-// makes 1.66e-3.  Of short matrices, whose few elements leave 2.4e-3 to 5e-3,
-// every operand is a pair and every product three: 1.66e-3 to 1.9e-3.
+// number: those roundings act within the rows that X has.  Rounding the result
+// to BF16 leaves 1.66e-3 of it (norms); with these roundings it is, after 1 to
+// 3 steps, 1.7e-3 to 1.8e-3 off the exact one, 1.7e-3 to 2.1e-3 after 4, 1.8e-3
+// to 2.4e-3 after 5, 2.4e-3 to 3.6e-3 after 8, 3.3e-3 to 4.7e-3 after 12 and
+// 5e-3 to 3e-2 after 16 to 32 (257 x 257 to 4096 x 4096, full and low rank and
+// with rows that fade by e^8): the usual coefficients drive no singular value to
+// a fixed point, and what a step leaves goes on growing.  Those that do, (15,
+// -10, 3) / 8 and (3, -1, 0) / 2, stay at 1.7e-3 to 1.8e-3 after 32.  Of short
+// matrices (kOrthoPairs), whose few elements would leave 2.4e-3 to 5e-3 after
+// five, every operand is a pair and every product three: 1.6e-3 to 1.7e-3 after
+// any number of steps.
 //
 // Layout.  Every operand of a product is read along its rows: X X' from X,
 // A A from A (symmetric), and B X from B and X transposed, of which a copy is

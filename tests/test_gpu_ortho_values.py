@@ -131,3 +131,20 @@ def test_lists_of_matrices_with_a_short_side(L):
         xs = [torch.randn(s, device="cuda").to(BF) for s in shapes]
         for k, (x, y) in enumerate(zip(xs, L.orthogonalize(xs))):
             check(y, x, 5, L.NEWTON_SCHULZ, 1.0, "%d: %s" % (k, tuple(x.shape)))
+
+
+@pytest.mark.parametrize("m,n", [(257, 300), (300, 2100), (1024, 700)])
+def test_errors_of_many_steps(L, m, n):
+    """The error of many steps is that of the documented roundings: as large as
+    the same iteration leaves in 64 bits with them.  They are made anew for each
+    element, so the two errors' norms, of m and more directions, differ by chance
+    as 1 / sqrt(m), at most a sixteenth; three times that is allowed."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, n, generator=g, device="cuda")
+    for steps in (5, 8, 12):
+        y = torch.empty(m, n, dtype=BF, device="cuda")
+        xl = L.LctMatrices([x])
+        L.lct_list_orthogonalize(xl, L.LctMatrices([y]), L.alloc_orthogonal(xl), steps=steps)
+        e, r = exact(x, steps, L.NEWTON_SCHULZ), exact(x, steps, L.NEWTON_SCHULZ, rounded=True)
+        got, model = float((y.double() - e).norm()), float((r - e).norm())
+        assert abs(got - model) <= 3 / 16 * model, (steps, got / float(e.norm()), model / float(e.norm()))
