@@ -632,10 +632,13 @@ lct_status lct_rows_grad(const void *d_index, int32_t wide, uint64_t count, cons
  * 8, 4.7e-3 after 12, and up to 3e-2 after 32.
  * d_scratch: device working memory of lct_orthogonal_scratch() bytes (256-byte
  * aligned), overlapping no tensor, shared only by calls that do not overlap in
- * time.  Long lists are done in batches of consecutive matrices, whose memory
- * it holds at a time: about 8 bytes per element of the largest batch (sides
- * rounded up to whole tiles).  Enqueues only.  Errors: LCT_EINVAL, LCT_EALIGN,
- * LCT_EALIAS, LCT_EARCH, LCT_EHIP. */
+ * time.  Long lists are done in batches of consecutive matrices, whose memory it
+ * holds at a time: of a matrix of m rows and n >= m columns (or the other way
+ * round) 8 m n + 6 m m bytes, where m <= 256 12 m n + 8 m m, with m and n rounded
+ * up to multiples of 128 (in a batch of large matrices, 256); sums of cut products,
+ * at most 16 MiB; and the norms'.  A batch gathers at most 32 matrices and, unless
+ * it is one alone, 2^27 elements, so rounded to 128.  Enqueues only.  Errors:
+ * LCT_EINVAL, LCT_EALIGN, LCT_EALIAS, LCT_EARCH, LCT_EHIP. */
 lct_status lct_orthogonal_scratch(const lct_list *x, const uint64_t *rows, uint64_t *bytes);
 lct_status lct_list_orthogonalize(const lct_list *x, const uint64_t *rows, const lct_list *y, uint32_t steps,
                                   const float coef[3], const float *scale, void *d_scratch, void *stream);

@@ -58,3 +58,10 @@ def test_lists_of_matrices_with_a_short_side(L, shape):
     batch = max(1, min(32, (1 << 27) // (m * n)))
     for count in (1, 31, 32, 200):
         assert need(L, [shape] * count) <= min(count, batch) * one + ROOM, count
+
+
+@pytest.mark.parametrize("shape", [(256, 256), (257, 256), (257, 300), (2560, 9728), (1000, 1000), (4096, 4096), (1, 1)])
+def test_memory_of_a_matrix(L, shape):
+    """The documented bytes of one matrix, and not much less."""
+    bytes = most(shape) if min(shape) < 4096 else most([-(-s // 256) * 256 for s in shape])
+    assert bytes <= need(L, [shape]) <= bytes + ROOM
