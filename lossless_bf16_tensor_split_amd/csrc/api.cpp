@@ -772,8 +772,9 @@ lct_status ortho_batches(const lct_list &x, const uint64_t *rows, F f) {
             const uint32_t room = std::min(kOrthoSplitMax, kOrthoSplitTo / b.sym_tiles);
             if (gram >= kOrthoLong) b.split_gram = std::max(1u, std::min(room, gram / kOrthoPart));
             if (square >= kOrthoLong) b.split_square = std::max(1u, std::min(room, square / kOrthoPart));
+            const uint32_t parts = std::max(b.split_gram, b.split_square);
             p.partial = reinterpret_cast<float *>(bytes);   // (an offset so far)
-            bytes += 4ull * kOrthoSmall * kOrthoSmall * b.sym_tiles * std::max(b.split_gram, b.split_square);
+            if (parts > 1) bytes += 4ull * kOrthoSmall * kOrthoSmall * b.sym_tiles * parts;
         }
         const lct_status st = f(p, b, bytes);
         if (st != LCT_OK) return st;
