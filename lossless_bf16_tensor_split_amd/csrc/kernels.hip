@@ -2900,9 +2900,10 @@ void k_mom(const MomParams p) {
 // dense: the decoder's walk with the encoder's writer behind it, a unit per
 // wave.  D: 0 no dense result, 1 y', 2 the value looked ahead, rne(a * y' + bx).
 //
-// LDS: encode table (and its entry of no bits), decode table, then per wave the
-// input's rows between two zero rows; the result's rows go to memory as they
-// fill, once the input's (which they may overwrite) are in LDS.
+// LDS: encode table, decode table (right behind it: there is no entry of no bits,
+// which this writer does not need), then per wave the input's rows between two
+// zero rows; the result's rows go to memory as they fill, once the input's (which
+// they may overwrite) are in LDS.
 constexpr uint32_t kMixWaves = 4;
 constexpr uint32_t kMixETab = 0, kMixDTab = 2048, kMixWave0 = kMixDTab + 1024;
 __host__ __device__ constexpr uint32_t mix_wave_bytes(uint32_t cap) { return (cap + 2) * ROWB; }
