@@ -289,12 +289,22 @@ constexpr uint64_t kRowsSortFrom = 4096;
 // summed in tiles.
 constexpr uint32_t kSortBits = 9, kSortDigits = 1u << kSortBits;
 constexpr uint32_t kSortThreads = 256, kSortChunk = 1024;
-constexpr uint32_t kSortOne = 4096;                    // up to so many tokens one workgroup sorts them
-constexpr uint32_t kSortFew = 64;                      // chunks whose counts the placing kernel adds up itself
+// Up to so many tokens one workgroup sorts them.  A gradient's us by that kernel
+// and (by a launch or more a pass): of 4001 x 331, 2048 tokens 27 (34), 4096 39
+// (46), with a kernel for 8192 of them 47 (48); of 300,000 x 40, 4096 25 (35).
+// One for 8192 takes 4 to 7 us more for the fewer, one for 1024 2 to 3 us less.
+constexpr uint32_t kSortOne = 4096;
+// Chunks whose counts the placing kernel adds up itself; (by a launch of their
+// own): 50,304 x 40, 17 chunks 59 us (62), 64 118 (121), 98 134 (137), 256 229 (231).
+constexpr uint32_t kSortFew = 64;
 // (so that every launch's threads stay below 2^32 in a dimension)
 constexpr uint64_t kMaxTokens = 1ull << 30, kMaxRows = 1ull << 29, kMaxCols = 1ull << 24;
 // Tokens of a tile: four where there are few (each row that ends in a tile waits
-// for what G holds), more where there are many.
+// for what G holds), more where there are many (fewer sums to join).  A gradient's
+// us with tiles of 4, 8, 16 and 32: 777 tokens added to 4001 x 331 21, 23, 31, 46;
+// 4096 to 32,000 x 1024 31, 29, 32, 38 (25, 27, 32, 42 where none is frequent);
+// 8192 53, 45, 47, 57 (39, 40, 45, 57); 16,384 to 50,304 x 768 109, 77, 69, 80;
+// 65,536 371, 229, 156, 135; 16,384 of 151,936 x 2560, written, 259, 237, 225, 233.
 constexpr uint32_t kRowTileFew = 4, kRowTile = 16, kRowTileMax = 256;
 constexpr uint64_t kRowFew = 4096;                     // tokens up to which they are few
 constexpr uint64_t kRowTiles = 4096;
@@ -487,7 +497,9 @@ inline uint64_t norm_scratch_bytes(uint64_t count, uint64_t nblk) {
 // caller's is the transpose), padded to mp and np, whole tiles; its working
 // memory starts at byte `off`: X as a pair, two copies of its transpose, A as a
 // pair, B, all FP16; for short matrices (m at most kOrthoPairs) then the low
-// parts of B and of X' too.
+// parts of B and of X' too.  The error that this takes away stands in ortho.hip;
+// what it takes, in us, with and (without): 64 x 64 140 (114), 200 x 300 226
+// (169), 24 of 256 x 2048 565 (370); it would take 24 of 512 x 2048 1292 (671).
 constexpr uint32_t kOrthoPairs = 256;
 constexpr uint32_t kOrthoMax = 32;        // matrices per launch
 constexpr uint32_t kOrthoSmall = 128, kOrthoLarge = 256;
@@ -504,9 +516,16 @@ constexpr uint32_t kOrthoLargeFrom = 800;
 // times, 2739 (3258); 32 of 600 x 2000, 1.44 times, 1409 (1789); 32 of 64 x
 // 6400, 4 times, 805 (2963).
 constexpr uint32_t kOrthoLargePad = 5;
-// Few small tiles (at most half of what the device holds at once) with long
-// sums (kOrthoLong steps of 32 and more): K is cut into parts of at least
-// kOrthoPart steps.
+// Few small tiles (kOrthoSplitTo parts of them at most, half of what the device
+// holds at once) with long sums (kOrthoLong steps of 32 and more): K is cut into
+// up to kOrthoSplitMax parts of at least kOrthoPart steps.  In us, cut and
+// (whole): 128 x 4096 239 (527), 256 x 16,384 464 (1812), 400 x 2000 244 (288),
+// 777 x 2049 317 (366), 1536 x 1536 406 (520), 2048 x 2048 (whole by the rule) 617,
+// 4 of 777 x 2049 464 (490).  With other limits, for 777 x 2049, 1536 x 1536 and 9
+// of 300 x 2000 (317, 406 and 301): 128 parts 291, 520 and 313, 512 parts 317, 440
+// and 321; sums of 24 steps 317, 407 and 318, of 96 366, 414 and 332; parts of 4
+// steps 317, 407 and 300, of 16 294, 406 and 301; at most 4 parts 291, 407 and 299
+// (256 x 16,384 then 656), 16 308, 406 and 300.
 constexpr uint32_t kOrthoSplitTo = 256, kOrthoSplitMax = 8, kOrthoPart = 8, kOrthoLong = 48;
 // Elements that a batch of matrices gathers, with sides rounded up to small
 // tiles: 2048 tiles of 256 x 256, eight per CU.
